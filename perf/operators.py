@@ -225,6 +225,11 @@ def _prepare_plan(case, d):
     s = {"op": "plan", "page": pg, "num_pages": pool, "ctx_len": _ints(ctx), "new_len": _ints(new),
          "block_table": _table(held, width, pages), "free_pages": pages[sum(held):].contiguous(),
          "free_head": _ints([0]), "tokens": _pages(T, 64) * 64, "most_new": max(new), "parent": None}
+    # the buffers that a server fills anew every step: cu_q, kv_len, slots, positions, free_next
+    # and the draft masks
+    s["out"] = tuple(torch.empty(n, dtype=torch.int32, device="cuda")
+                     for n in (len(b) + 1, len(b), s["tokens"], s["tokens"], 1))
+    s["out"] += (torch.empty(s["tokens"], dtype=torch.int64, device="cuda") if case["tree"] else None,)
     if case["tree"]:
         flat = [x for _, p in b for x in p]
         s["parent"] = _ints(flat + [-1] * (s["tokens"] - T))
@@ -292,7 +297,7 @@ def _run_own(s):
     if s["op"] == "plan":
         p = mla.mla_paged_plan(s["ctx_len"], s["new_len"], s["block_table"], s["free_pages"],
                                s["free_head"], s["page"], s["num_pages"], s["tokens"],
-                               parent=s["parent"])
+                               parent=s["parent"], out=s["out"])
         return {"cu_q": p.cu_q, "kv_len": p.kv_len, "slots": p.slots, "positions": p.positions,
                 "free_next": p.free_next, "block_table": s["block_table"],
                 "draft_mask": p.draft_mask}
