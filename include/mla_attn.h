@@ -78,7 +78,10 @@ typedef enum {
   MLA_ERR_CUDA = 6,      /* a CUDA runtime call or kernel launch failed */
   MLA_ERR_KVLEN = 7,     /* (device) some kv_len[b] outside [1, Tk] */
   MLA_ERR_TIMEOUT = 8,   /* (device) a bounded wait inside a kernel gave up */
-  MLA_ERR_ARG = 9        /* an option value is out of range */
+  MLA_ERR_ARG = 9,       /* an option value is out of range */
+  MLA_ERR_PAGE = 10,     /* (device) a page or slot outside the pool, or no free page left */
+  MLA_ERR_TREE = 11      /* (device) a parent that does not come before its token, or more
+                            drafted tokens in a sequence than a 64-bit mask holds */
 } mla_status;
 
 /*
@@ -318,6 +321,82 @@ MLA_API mla_status mla_attn_rope_append_fwd(const uint16_t* q_nope, const uint16
                                             float softmax_scale, const float* rope_table,
                                             int table_rows, uint16_t* out, void* workspace,
                                             size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * ---- Serving over a paged latent cache ---------------------------------------------------
+ *
+ * The latent cache (512-wide latent row + 64-wide rotary key per token, see
+ * mla_latent_decode_fwd) can be held in pages that the sequences of a batch share out
+ * between them:
+ *
+ *   c_pages  [num_pages, page_size, 512]   bf16      page_size a power of two, 16 .. 1024;
+ *   pe_pages [num_pages, page_size, 64]    bf16      num_pages * page_size < 2^31
+ *   block_table [B, max_pages]             int32     position p of sequence b is row
+ *                                                    p % page_size of page
+ *                                                    block_table[b, p / page_size]
+ *   slot = page * page_size + row                    the same place as one number
+ *
+ * A step's new tokens are packed: sequence b holds rows cu_q[b] .. cu_q[b+1] - 1 of every
+ * per-token tensor.  The per-token tensors may be longer than cu_q[B] (a captured graph has
+ * one size for many batches): rows from cu_q[B] on are padding, and outputs are left as they
+ * were there unless stated otherwise.
+ */
+
+/*
+ * Bookkeeping of one step: takes pages for the new tokens from a free list and lists where
+ * every token goes.  For sequence b with ctx = ctx_len[b] cached tokens and n = new_len[b]
+ * new ones (n may be 0):
+ *
+ *   cu_q[b]   = new_len[0] + .. + new_len[b-1]      (cu_q[B] = all new tokens)
+ *   kv_len[b] = ctx + n
+ *   block_table[b, k] for ceil(ctx / page_size) <= k < ceil(kv_len / page_size) receives the
+ *               next pages of free_pages, in order of b, then k, starting at free_pages[
+ *               free_head[0]]; free_next[0] = the first entry not taken.  No other entry of
+ *               the table is written.
+ *   slots[t]     = the slot of position ctx + i     (t = cu_q[b] + i)
+ *   positions[t] = ctx + depth, where depth is i without `parent`, and with it the number of
+ *               ancestors of the token: parent[t] is the index within the sequence's new
+ *               tokens of the token's parent (0 <= parent < i), or -1 for a root.
+ *   draft_mask[t] (with parent only): bit j set where j is i or an ancestor of i: the form
+ *               mla_latent_tree_fwd takes.  At most 64 new tokens per sequence then.
+ * Rows t from cu_q[B] to T - 1: slots -1, positions 0, draft_mask 0.
+ *
+ * free_next must not be free_head (every block reads one while one block writes the other).
+ * Problems only the device sees go to the status word, and the call completes: lengths below
+ * zero or past max_pages * page_size, or more than T new tokens in all (MLA_ERR_KVLEN:
+ * lengths are clamped, tokens past the table get slot -1); a free list that runs out, or an
+ * entry outside [0, num_pages) (MLA_ERR_PAGE: table entry and slots become -1); a bad parent
+ * or a sequence of more than 64 drafted tokens (MLA_ERR_TREE: the token becomes a root; the
+ * tokens past 64 see nothing).
+ * Lengths must not overlap the outputs.  workspace: 256 bytes (the status word), zeroed once.
+ */
+MLA_API mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int B,
+                                  int32_t* block_table, int max_pages, const int32_t* free_pages,
+                                  int n_free, const int32_t* free_head, int page_size,
+                                  int num_pages, const int32_t* parent, int T, int32_t* cu_q,
+                                  int32_t* kv_len, int32_t* slots, int32_t* positions,
+                                  int64_t* draft_mask, int32_t* free_next, void* workspace,
+                                  size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * Append to the paged latent cache: row t of c_kv_new [T, 512] and k_pe_new [T, 64] goes to
+ * slot slots[t] of c_pages / pe_pages; a negative slot marks a row that is skipped.  With
+ * rope_table (from mla_rope_table, table_rows rows; positions [T] then required) k_pe_new is
+ * unrotated and is rotated at positions[t] on its way, and so is q_pe [T, H, 64], if given,
+ * into q_pe_out [T, H, 64] (which may be q_pe itself); rotated values are rounded to bf16.
+ * Without rope_table the rows are copied and q_pe must be NULL.
+ *
+ * Slots must be distinct: of two rows with one slot, the cache keeps some mixture.  A slot
+ * past the pool is not written (MLA_ERR_PAGE in the status word), a position outside the table
+ * is clamped to it (MLA_ERR_KVLEN).  workspace: 256 bytes (the status word), zeroed once.
+ */
+MLA_API mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k_pe_new,
+                                     const int32_t* slots, int T, uint16_t* c_pages,
+                                     uint16_t* pe_pages, int num_pages, int page_size,
+                                     const int32_t* positions, const float* rope_table,
+                                     int table_rows, const uint16_t* q_pe, int H,
+                                     uint16_t* q_pe_out, void* workspace,
+                                     size_t workspace_bytes, void* cuda_stream);
 
 /*
  * Synchronises cuda_stream, reads the device status word in the workspace, clears it,

@@ -11,6 +11,7 @@ import ctypes
 import enum
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -31,6 +32,8 @@ class MlaStatus(enum.IntEnum):
     ERR_KVLEN = 7
     ERR_TIMEOUT = 8
     ERR_ARG = 9
+    ERR_PAGE = 10
+    ERR_TREE = 11
 
 
 PATH_AUTO, PATH_PREFILL, PATH_DECODE = 0, 1, 2
@@ -67,7 +70,8 @@ EXPORTED = ("mla_attn_workspace_bytes", "mla_attn_fwd", "mla_attn_fwd_ex",
             "mla_attn_rope_workspace_bytes", "mla_attn_rope_append_fwd",
             "mla_attn_masked_workspace_bytes", "mla_attn_masked_fwd",
             "mla_latent_workspace_bytes", "mla_latent_decode_fwd",
-            "mla_oproj_workspace_bytes", "mla_oproj_fwd")
+            "mla_oproj_workspace_bytes", "mla_oproj_fwd", "mla_paged_plan",
+            "mla_latent_append")
 
 
 def library():
@@ -121,6 +125,11 @@ def library():
         lib.mla_attn_rope_append_fwd.restype = i
         lib.mla_attn_rope_append_fwd.argtypes = [p, p, p, p, p, p, p, p, p, i, i, i, i, i, f,
                                                  p, i, p, p, sz, p]
+        lib.mla_paged_plan.restype = i
+        lib.mla_paged_plan.argtypes = [p, p, i, p, i, p, i, p, i, i, p, i, p, p, p, p, p, p, p,
+                                       sz, p]
+        lib.mla_latent_append.restype = i
+        lib.mla_latent_append.argtypes = [p, p, p, i, p, p, i, i, p, p, i, p, i, p, p, sz, p]
         _lib = lib
         return lib
 
@@ -170,6 +179,11 @@ def _ptr(t):
 
 
 def _check(t, name, dtype, shape, device):
+    try:  # the usual case, in few steps
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -180,6 +194,30 @@ def _check(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _enqueue(name, dev, stream, workspace, ws_bytes, args):
+    """Calls entry point `name` with args, then workspace, its size and the stream, with `dev`
+    current.  For calls of a few microseconds the host side counts: no device context unless
+    the device changes, and the stream's address without a Stream object."""
+    fn = getattr(library(), name)
+    index = dev.index if dev.index is not None else torch.cuda.current_device()
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    ws = workspace or _default_workspace(dev)
+    buf = ws.buf
+    if buf is None or buf.numel() < ws_bytes:
+        buf = ws.get(ws_bytes, stream=stream or torch.cuda.current_stream(dev))
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, buf.data_ptr(), buf.numel(), s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, buf.data_ptr(), buf.numel(), s)
+    if rc != 0:
+        raise MlaAttnError(rc, name + ": ")
 
 
 class PreparedCall:
@@ -391,6 +429,105 @@ def mla_oproj_fwd(attn, w_o, out=None, workspace: "Workspace | None" = None, str
     return out
 
 
+class PagedPlan(NamedTuple):
+    """What mla_paged_plan lists: offsets of the sequences' new tokens [B + 1], cached lengths
+    with them [B], per token its slot and position [T], the first free-list entry left [1], and
+    for drafted trees the tokens' ancestor masks [T] (int64), else None."""
+    cu_q: torch.Tensor
+    kv_len: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    free_next: torch.Tensor
+    draft_mask: "torch.Tensor | None"
+
+
+def mla_paged_plan(ctx_len, new_len, block_table, free_pages, free_head, page_size: int,
+                   num_pages: int, num_tokens: int, parent=None, out=None,
+                   workspace: "Workspace | None" = None, stream=None) -> PagedPlan:
+    """Takes pages for a step's new tokens and lists where every token goes.
+
+    ctx_len, new_len [B] int32 (cached and new tokens per sequence); block_table
+    [B, max_pages] int32, updated in place; free_pages [n] int32, taken from entry
+    free_head[0] (int32 [1]) on; parent [num_tokens] int32 for drafted trees (index within the
+    sequence's new tokens, -1 for a root).  num_tokens: rows of the per-token outputs, at least
+    the new tokens (rows behind them get slot -1).  ``out``: a PagedPlan (or a tuple like it)
+    to fill instead of new tensors; its free_next must not be free_head."""
+    dev = ctx_len.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    B, T, i32 = ctx_len.shape[0], int(num_tokens), torch.int32
+    _check(ctx_len, "ctx_len", i32, (B,), dev)
+    _check(new_len, "new_len", i32, (B,), dev)
+    _check(block_table, "block_table", i32, (B, block_table.shape[-1]), dev)
+    _check(free_pages, "free_pages", i32, (free_pages.shape[0],), dev)
+    _check(free_head, "free_head", i32, (1,), dev)
+    if parent is not None:
+        _check(parent, "parent", i32, (T,), dev)
+    if out is None:
+        new = lambda n, dt=i32: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
+        out = PagedPlan(new(B + 1), new(B), new(T), new(T), new(1),
+                        None if parent is None else new(T, torch.int64))
+    elif not isinstance(out, PagedPlan):
+        out = PagedPlan(*out)
+    _check(out.cu_q, "cu_q", i32, (B + 1,), dev)
+    _check(out.kv_len, "kv_len", i32, (B,), dev)
+    _check(out.slots, "slots", i32, (T,), dev)
+    _check(out.positions, "positions", i32, (T,), dev)
+    _check(out.free_next, "free_next", i32, (1,), dev)
+    if parent is None:
+        if out.draft_mask is not None:
+            raise ValueError("draft_mask is listed with parent only")
+    else:
+        _check(out.draft_mask, "draft_mask", torch.int64, (T,), dev)
+    _enqueue("mla_paged_plan", dev, stream, workspace, 256, (
+        ctx_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(),
+        block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(),
+        int(page_size), int(num_pages), _addr(parent), T, out.cu_q.data_ptr(),
+        out.kv_len.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
+        _addr(out.draft_mask), out.free_next.data_ptr()))
+    return out
+
+
+def mla_latent_append(c_kv_new, k_pe_new, slots, c_pages, pe_pages, positions=None,
+                      rope_table=None, q_pe=None, q_pe_out=None,
+                      workspace: "Workspace | None" = None, stream=None):
+    """Writes the rows c_kv_new [T,512], k_pe_new [T,64] to their slots [T] (int32; negative:
+    skipped) of a paged latent cache c_pages [num_pages, page_size, 512] / pe_pages
+    [num_pages, page_size, 64].  With rope_table (mla_rope_table) and positions [T] (int32)
+    k_pe_new is rotated on its way, and so is q_pe [T,H,64] into q_pe_out (new if None; may be
+    q_pe).  Returns q_pe_out (None without q_pe)."""
+    dev = c_pages.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    T, bf, i32 = c_kv_new.shape[0], torch.bfloat16, torch.int32
+    num_pages, page_size = c_pages.shape[:2]
+    _check(c_kv_new, "c_kv_new", bf, (T, 512), dev)
+    _check(k_pe_new, "k_pe_new", bf, (T, 64), dev)
+    _check(slots, "slots", i32, (T,), dev)
+    _check(c_pages, "c_pages", bf, (num_pages, page_size, 512), dev)
+    _check(pe_pages, "pe_pages", bf, (num_pages, page_size, 64), dev)
+    rows, H = 0, 0
+    if rope_table is not None:
+        rows = rope_table.shape[0]
+        _check(rope_table, "rope_table", torch.float32, (rows, 64), dev)
+        _check(positions, "positions", i32, (T,), dev)
+        if q_pe is not None:
+            H = q_pe.shape[1]
+            _check(q_pe, "q_pe", bf, (T, H, 64), dev)
+            if q_pe_out is None:
+                q_pe_out = torch.empty_like(q_pe)
+            _check(q_pe_out, "q_pe_out", bf, (T, H, 64), dev)
+    elif q_pe is not None:
+        raise ValueError("q_pe is rotated with rope_table only")
+    if q_pe is None and q_pe_out is not None:
+        raise ValueError("q_pe_out without q_pe")
+    _enqueue("mla_latent_append", dev, stream, workspace, 256, (
+        c_kv_new.data_ptr(), k_pe_new.data_ptr(), slots.data_ptr(), T, c_pages.data_ptr(),
+        pe_pages.data_ptr(), num_pages, page_size, _addr(positions), _addr(rope_table), rows,
+        _addr(q_pe), H, _addr(q_pe_out)))
+    return q_pe_out
+
+
 def mla_rope_frequencies(cfg: RopeConfig | None = None):
     """(inv_freq[32] as a list of floats, mscale ratio) computed by the library's host code."""
     cfg = cfg or RopeConfig()
@@ -471,7 +608,9 @@ _default_ws: dict = {}
 
 
 def _default_workspace(dev) -> Workspace:
-    key = str(dev)
-    if key not in _default_ws:
-        _default_ws[key] = Workspace(dev)
-    return _default_ws[key]
+    # "cuda" and "cuda:0" are one workspace: a status is read where the calls recorded it
+    key = dev.index if dev.index is not None else torch.cuda.current_device()
+    ws = _default_ws.get(key)
+    if ws is None:
+        ws = _default_ws.setdefault(key, Workspace(torch.device("cuda", key)))
+    return ws

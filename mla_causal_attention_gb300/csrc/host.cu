@@ -106,6 +106,19 @@ size_t rope_bytes(int B, int H, int Tq) {
   return q_rot_bytes(B, H, Tq) + round256((size_t)B * Tq * 64 * 2);
 }
 
+// A paged latent cache: page_size a power of two in [16, 1024], all slots below 2^31.
+mla_status check_pool(int num_pages, int page_size) {
+  if (num_pages < 1 || page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0 ||
+      (int64_t)num_pages * page_size > 0x7fffffff)
+    return MLA_ERR_SHAPE;
+  return MLA_OK;
+}
+int page_shift(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
 bool rope_config_ok(const mla_rope_config& c) {
   const double v[7] = {c.rope_theta, c.factor, c.original_max_position, c.beta_fast,
                        c.beta_slow, c.mscale, c.mscale_all_dim};
@@ -171,6 +184,8 @@ const char* mla_status_string(mla_status s) {
     case MLA_ERR_KVLEN: return "MLA_ERR_KVLEN: kv_len[b] outside [1, Tk]";
     case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT: a bounded wait in a kernel gave up";
     case MLA_ERR_ARG: return "MLA_ERR_ARG: option out of range";
+    case MLA_ERR_PAGE: return "MLA_ERR_PAGE: page or slot outside the pool, or no free page left";
+    case MLA_ERR_TREE: return "MLA_ERR_TREE: bad parent or more than 64 drafted tokens";
   }
   return "unknown mla_status";
 }
@@ -568,6 +583,79 @@ mla_status mla_oproj_fwd(const uint16_t* attn, const uint16_t* w_o, int B, int H
                                                                                 : MLA_ERR_CUDA;
 }
 
+mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int B,
+                          int32_t* block_table, int max_pages, const int32_t* free_pages,
+                          int n_free, const int32_t* free_head, int page_size, int num_pages,
+                          const int32_t* parent, int T, int32_t* cu_q, int32_t* kv_len,
+                          int32_t* slots, int32_t* positions, int64_t* draft_mask,
+                          int32_t* free_next, void* workspace, size_t workspace_bytes,
+                          void* cuda_stream) {
+  if (!ctx_len || !new_len || !block_table || !free_head || !cu_q || !kv_len || !slots ||
+      !positions || !free_next || (n_free > 0 && !free_pages) || (parent != nullptr) != (draft_mask != nullptr))
+    return MLA_ERR_NULL;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  const mla_status ps = check_pool(num_pages, page_size);
+  if (ps != MLA_OK) return ps;
+  if (B < 1 || T < 1 || max_pages < 1 || n_free < 0 || T > (1 << 30) || B > (1 << 24) ||
+      (int64_t)max_pages * page_size > 0x7fffffff)
+    return MLA_ERR_SHAPE;
+  const void* words[] = {ctx_len, new_len, block_table, free_pages, free_head, parent,
+                         cu_q, kv_len, free_next};
+  for (const void* w : words)
+    if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0) return MLA_ERR_ALIGN;
+  if (!aligned16(slots) || !aligned16(positions) || !aligned16(draft_mask) ||
+      !aligned16(workspace))
+    return MLA_ERR_ALIGN;
+  if (free_next == free_head) return MLA_ERR_ARG;
+  if (workspace_bytes < kStatusBytes) return MLA_ERR_WORKSPACE;
+  const mla_status st = check_device(nullptr);
+  if (st != MLA_OK) return st;
+  PagedPlanArgs a{};
+  a.ctx_len = ctx_len; a.new_len = new_len; a.block_table = block_table;
+  a.free_pages = free_pages; a.free_head = free_head; a.parent = parent;
+  a.cu_q = cu_q; a.kv_len = kv_len; a.slots = slots; a.positions = positions;
+  a.draft_mask = draft_mask; a.free_next = free_next; a.status = static_cast<int*>(workspace);
+  a.B = B; a.T = T; a.max_pages = max_pages; a.n_free = n_free; a.num_pages = num_pages;
+  a.page_shift = page_shift(page_size);
+  return launch_paged_plan(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k_pe_new,
+                             const int32_t* slots, int T, uint16_t* c_pages, uint16_t* pe_pages,
+                             int num_pages, int page_size, const int32_t* positions,
+                             const float* rope_table, int table_rows, const uint16_t* q_pe,
+                             int H, uint16_t* q_pe_out, void* workspace, size_t workspace_bytes,
+                             void* cuda_stream) {
+  if (!c_kv_new || !k_pe_new || !slots || !c_pages || !pe_pages) return MLA_ERR_NULL;
+  if (rope_table ? !positions : (q_pe != nullptr)) return MLA_ERR_NULL;
+  if ((q_pe != nullptr) != (q_pe_out != nullptr)) return MLA_ERR_NULL;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  const mla_status ps = check_pool(num_pages, page_size);
+  if (ps != MLA_OK) return ps;
+  if (T < 1 || (rope_table && table_rows < 1) || (q_pe && (H < 1 || H > 65536)) ||
+      (int64_t)T * 512 > kMaxElems || (q_pe && (int64_t)T * H * 64 > kMaxElems))
+    return MLA_ERR_SHAPE;
+  if (!aligned16(c_kv_new) || !aligned16(k_pe_new) || !aligned16(c_pages) ||
+      !aligned16(pe_pages) || !aligned16(rope_table) || !aligned16(q_pe) ||
+      !aligned16(q_pe_out) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(slots) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
+    return MLA_ERR_ALIGN;
+  if (workspace_bytes < kStatusBytes) return MLA_ERR_WORKSPACE;
+  const mla_status st = check_device(nullptr);
+  if (st != MLA_OK) return st;
+  LatentAppendArgs a{};
+  a.c_new = c_kv_new; a.pe_new = k_pe_new; a.slots = slots; a.c_pages = c_pages;
+  a.pe_pages = pe_pages; a.positions = positions; a.rope_table = rope_table; a.q_pe = q_pe;
+  a.q_pe_out = q_pe_out; a.status = static_cast<int*>(workspace);
+  a.T = T; a.H = q_pe ? H : 0; a.table_rows = table_rows; a.rows = num_pages * page_size;
+  return launch_latent_append(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
 mla_status mla_attn_fwd(const uint16_t* q_nope, const uint16_t* q_pe, const uint16_t* k_nope,
                         const uint16_t* k_pe_shared, const uint16_t* v, const int32_t* kv_len,
                         int B, int H, int Tq, int Tk, int past_len, float softmax_scale,
@@ -586,7 +674,7 @@ mla_status mla_attn_get_status(void* workspace, void* cuda_stream) {
     return MLA_ERR_CUDA;
   if (cudaMemsetAsync(workspace, 0, sizeof(int), stream) != cudaSuccess) return MLA_ERR_CUDA;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return MLA_ERR_CUDA;
-  if (host < 0 || host > MLA_ERR_ARG) return MLA_ERR_CUDA;
+  if (host < 0 || host > MLA_ERR_TREE) return MLA_ERR_CUDA;
   return static_cast<mla_status>(host);
 }
 

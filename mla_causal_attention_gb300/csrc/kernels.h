@@ -191,6 +191,41 @@ struct LatentArgs {
 constexpr int kLatTile = 128;  // keys per tile of the latent kernel
 cudaError_t launch_latent(const LatentArgs& a, cudaStream_t stream);
 
+// Block tables, slots, positions and draft masks of one step (see mla_paged_plan).
+struct PagedPlanArgs {
+  const int32_t* ctx_len;
+  const int32_t* new_len;
+  int32_t* block_table;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  const int32_t* parent;  // may be null
+  int32_t* cu_q;
+  int32_t* kv_len;
+  int32_t* slots;
+  int32_t* positions;
+  int64_t* draft_mask;  // null without parent
+  int32_t* free_next;
+  int* status;
+  int B, T, max_pages, n_free, num_pages, page_shift;
+};
+cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream);
+
+// Rotary step on new rows and their scatter into the paged latent cache.
+struct LatentAppendArgs {
+  const uint16_t* c_new;
+  const uint16_t* pe_new;
+  const int32_t* slots;
+  uint16_t* c_pages;
+  uint16_t* pe_pages;
+  const int32_t* positions;
+  const float* rope_table;  // null: rows are copied as they are
+  const uint16_t* q_pe;     // may be null
+  uint16_t* q_pe_out;
+  int* status;
+  int T, H, table_rows, rows;  // H = 0 without q_pe; rows = slots of the pool
+};
+cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 

@@ -1,0 +1,342 @@
+// paged.cu -- bookkeeping and append of a paged latent cache.
+//
+//   paged_plan_kernel     pages for a step's new tokens, and where every token goes
+//   latent_append_kernel  rotary step on the new rows and their scatter into the pages
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace mla {
+namespace {
+
+// ---- plan -------------------------------------------------------------------------------
+// Two prefix sums over the sequences (new tokens, pages taken) and then independent work per
+// token and per table entry.  The sums are redone by every block instead of passed between
+// blocks: a chunk of 1024 sequences is two loads per thread and one block scan, less than a
+// second launch would cost, and no block then waits on another.  Blocks write only table
+// entries that no block reads (entries read lie below ceil(ctx / page_size)), so one launch
+// does everything.  Bound by launch and latency: a decode step's plan moves 2 KB.
+constexpr int kPlanThreads = 256;
+constexpr int kPlanPer = 4;                              // sequences per thread and chunk
+constexpr int kPlanChunk = kPlanThreads * kPlanPer;      // sequences per scan
+constexpr int kPlanTok = 4;                              // consecutive tokens per thread
+
+struct PlanSeq {
+  int64_t ctx, n, kv;
+  int have, take;
+};
+// Lengths clamped to what the table holds; *bad if they had to be.
+__device__ __forceinline__ PlanSeq plan_seq(const PagedPlanArgs& a, int b, bool* bad) {
+  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+  const int64_t ctx = a.ctx_len[b], n = a.new_len[b];
+  PlanSeq s;
+  s.ctx = min(max(ctx, (int64_t)0), cap);
+  s.n = min(max(n, (int64_t)0), (int64_t)a.T);
+  s.kv = min(s.ctx + s.n, cap);
+  if (s.ctx != ctx || s.n != n || s.kv != s.ctx + s.n) *bad = true;
+  const int64_t up = (1 << a.page_shift) - 1;
+  s.have = (int)((s.ctx + up) >> a.page_shift);
+  s.take = (int)((s.kv + up) >> a.page_shift) - s.have;
+  return s;
+}
+
+// The k-th page a step takes, or -1 where the free list has run out or holds no page.
+__device__ __forceinline__ int plan_page(const PagedPlanArgs& a, int64_t head, int64_t k) {
+  const int64_t at = head + k;
+  if (at >= a.n_free) return -1;
+  const int page = a.free_pages[at];
+  return page >= 0 && page < a.num_pages ? page : -1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPlanArgs a) {
+  __shared__ int64_t s_tok[kPlanChunk + 1];  // first token of each sequence of the chunk
+  __shared__ int64_t s_pg[kPlanChunk + 1];   // first page taken
+  __shared__ int64_t s_warp[2][kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t head0 = a.free_head[0];
+  const int64_t head = min(max(head0, (int64_t)0), (int64_t)a.n_free);
+  if (head != head0 && tid == 0 && blockIdx.x == 0) set_status(a.status, MLA_ERR_PAGE);
+  const int psize = 1 << a.page_shift;
+  const int64_t last_pos = ((int64_t)a.max_pages << a.page_shift) - 1;
+
+  // This block's tokens: an equal share of the T rows, in whole groups of kPlanTok.
+  const int64_t groups = (a.T + kPlanTok - 1) / kPlanTok;
+  const int64_t t0 = groups * blockIdx.x / gridDim.x * kPlanTok;
+  const int64_t t1 = min(groups * (blockIdx.x + 1) / gridDim.x * kPlanTok, (int64_t)a.T);
+
+  int64_t tok = 0, pg = 0;  // totals of the chunks before this one
+  int chunk = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanChunk, ++chunk) {
+    // Blocks share out the chunks' table rows; past its tokens and rows a block is done, but
+    // block 0 goes on to the totals.
+    const bool rows_mine = a.B <= kPlanChunk || chunk % gridDim.x == blockIdx.x;
+    if (blockIdx.x != 0 && tok >= t1 && a.B > kPlanChunk) {
+      int next = chunk;  // the next chunk whose rows this block writes
+      while (next % gridDim.x != blockIdx.x) ++next;
+      if ((int64_t)next * kPlanChunk >= a.B) break;
+    }
+    const int nb = min(kPlanChunk, a.B - b0);
+    int64_t my_tok[kPlanPer], my_pg[kPlanPer], sum_tok = 0, sum_pg = 0;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      const int i = tid * kPlanPer + k;
+      my_tok[k] = sum_tok;
+      my_pg[k] = sum_pg;
+      if (i < nb) {
+        const PlanSeq s = plan_seq(a, b0 + i, &bad);
+        sum_tok += s.n;
+        sum_pg += s.take;
+        if (a.parent && s.n > 64 && blockIdx.x == 0) set_status(a.status, MLA_ERR_TREE);
+      }
+    }
+    if (bad && blockIdx.x == 0) set_status(a.status, MLA_ERR_KVLEN);
+    int64_t inc_tok = sum_tok, inc_pg = sum_pg;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, inc_tok, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc_pg, o);
+      if (lane >= o) {
+        inc_tok += x;
+        inc_pg += y;
+      }
+    }
+    __syncthreads();  // the previous chunk's sums have been used
+    if (lane == 31) {
+      s_warp[0][warp] = inc_tok;
+      s_warp[1][warp] = inc_pg;
+    }
+    __syncthreads();
+    int64_t base_tok = tok, base_pg = pg;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) {
+        base_tok += s_warp[0][w];
+        base_pg += s_warp[1][w];
+      }
+      tok += s_warp[0][w];
+      pg += s_warp[1][w];
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      s_tok[tid * kPlanPer + k] = base_tok + inc_tok - sum_tok + my_tok[k];
+      s_pg[tid * kPlanPer + k] = base_pg + inc_pg - sum_pg + my_pg[k];
+    }
+    if (tid == 0) s_tok[kPlanChunk] = tok;
+    __syncthreads();
+
+    // Per sequence: cu_q, kv_len and the fresh table entries.  A single chunk is shared by
+    // sequence among all blocks; one warp per sequence, its lanes over the pages taken.
+    if (rows_mine) {
+      const int first = a.B <= kPlanChunk ? blockIdx.x * (kPlanThreads / 32) + warp : warp;
+      const int step = (a.B <= kPlanChunk ? gridDim.x : 1) * (kPlanThreads / 32);
+      for (int i = first; i < nb; i += step) {
+        bool ignore = false;
+        const PlanSeq s = plan_seq(a, b0 + i, &ignore);
+        if (lane == 0) {
+          a.cu_q[b0 + i] = (int)min(s_tok[i], (int64_t)a.T);
+          a.kv_len[b0 + i] = (int)s.kv;
+        }
+        int32_t* row = a.block_table + (int64_t)(b0 + i) * a.max_pages + s.have;
+        bool none = false;
+        for (int k = lane; k < s.take; k += 32) {
+          const int page = plan_page(a, head, s_pg[i] + k);
+          row[k] = page;
+          none |= page < 0;
+        }
+        if (none) set_status(a.status, MLA_ERR_PAGE);
+      }
+    }
+
+    // Per token: the sequences of this chunk that reach into [t0, t1).
+    const int64_t lo = max(t0, s_tok[0] / kPlanTok * kPlanTok), hi = min(t1, tok);
+    for (int64_t t = lo + (int64_t)tid * kPlanTok; t < hi; t += (int64_t)kPlanThreads * kPlanTok) {
+      int l = 0, r = nb;  // the last sequence of the chunk that starts at or before the token
+      const int64_t tf = max(t, s_tok[0]);
+      while (r - l > 1) {
+        const int m = (l + r) >> 1;
+        if (s_tok[m] <= tf) l = m; else r = m;
+      }
+      PlanSeq s;
+      int64_t end = -1;   // first token past sequence l
+      int page = -1, page_k = -1;
+      int slot[kPlanTok], pos[kPlanTok];
+      int64_t mask[kPlanTok];
+      bool whole = true;  // all tokens of the group belong to this chunk
+      bool bad_tree = false, bad_page = false;
+#pragma unroll
+      for (int e = 0; e < kPlanTok; ++e) {
+        slot[e] = -1; pos[e] = 0; mask[e] = 0;
+        const int64_t te = t + e;
+        if (te < s_tok[0] || te >= hi) {
+          whole = false;
+          continue;
+        }
+        while (te >= end) {  // skips sequences without new tokens
+          if (end >= 0) ++l;
+          end = l + 1 < nb ? s_tok[l + 1] : tok;
+          if (te < end) {
+            bool ignore = false;
+            s = plan_seq(a, b0 + l, &ignore);
+            page_k = -1;
+          }
+        }
+        const int64_t i = te - s_tok[l];
+        const int64_t p = s.ctx + i;
+        if (p < s.kv) {
+          const int k = (int)(p >> a.page_shift);
+          if (k != page_k) {
+            page_k = k;
+            if (k >= s.have) {
+              page = plan_page(a, head, s_pg[l] + k - s.have);
+            } else {
+              page = a.block_table[(int64_t)(b0 + l) * a.max_pages + k];
+              if (page < 0 || page >= a.num_pages) {
+                page = -1;
+                bad_page = true;
+              }
+            }
+          }
+          if (page >= 0) slot[e] = (page << a.page_shift) + (int)(p & (psize - 1));
+        }
+        int64_t depth = i;
+        if (a.parent) {
+          // Up the path to the root; indexes fall at every step, so the walk ends.
+          const int32_t* par = a.parent + s_tok[l];
+          uint64_t m = 0;
+          depth = -1;
+          int at = (int)i;
+          if (i < 64) {
+            for (;;) {
+              m |= 1ull << at;
+              ++depth;
+              const int up = par[at];
+              if (up < 0 || up >= at) {
+                bad_tree |= up != -1;
+                break;
+              }
+              at = up;
+            }
+          } else {
+            depth = 0;
+          }
+          mask[e] = (int64_t)m;
+        }
+        pos[e] = (int)min(s.ctx + depth, last_pos);
+      }
+      if (whole) {
+        *reinterpret_cast<int4*>(a.slots + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        *reinterpret_cast<int4*>(a.positions + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        if (a.parent) {
+          reinterpret_cast<longlong2*>(a.draft_mask + t)[0] = make_longlong2(mask[0], mask[1]);
+          reinterpret_cast<longlong2*>(a.draft_mask + t)[1] = make_longlong2(mask[2], mask[3]);
+        }
+      } else {
+        for (int e = 0; e < kPlanTok; ++e) {
+          if (t + e < s_tok[0] || t + e >= hi) continue;
+          a.slots[t + e] = slot[e];
+          a.positions[t + e] = pos[e];
+          if (a.parent) a.draft_mask[t + e] = mask[e];
+        }
+      }
+      if (bad_tree) set_status(a.status, MLA_ERR_TREE);
+      if (bad_page) set_status(a.status, MLA_ERR_PAGE);
+    }
+  }
+
+  if (blockIdx.x == 0 && tid == 0) {
+    if (tok > a.T) set_status(a.status, MLA_ERR_KVLEN);
+    a.cu_q[a.B] = (int)min(tok, (int64_t)a.T);
+    a.free_next[0] = (int)min(head + pg, (int64_t)a.n_free);
+  }
+  // Rows behind the last sequence.  A block that broke off above has none: its tokens lie
+  // before the running total.
+  for (int64_t t = max(t0, tok) + tid; t < t1; t += kPlanThreads) {
+    a.slots[t] = -1;
+    a.positions[t] = 0;
+    if (a.parent) a.draft_mask[t] = 0;
+  }
+}
+
+// ---- append -----------------------------------------------------------------------------
+// One pass over the new rows, bound by HBM: per token 2304 bytes of latent row and rotary key
+// in and out, and 256 H bytes of query.  A block takes tokens in turn; its threads take the
+// token's 16-byte pieces: 64 of the latent row, 4 pairs (columns c .. c+7 and c+32 .. c+39, so
+// that one thread rotates both and may write over its own input) of the rotary key and of
+// each head's query.
+constexpr int kAppThreads = 256;
+
+__device__ __forceinline__ void rotate_pair(const uint16_t* src, uint16_t* dst, int c,
+                                            const float* cs) {
+  const uint4 lo = *reinterpret_cast<const uint4*>(src + c);
+  const uint4 hi = *reinterpret_cast<const uint4*>(src + c + 32);
+  uint4 ylo = lo, yhi = hi;
+  if (cs) {
+    float cosv[8], sinv[8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      *reinterpret_cast<float4*>(cosv + 4 * k) = *reinterpret_cast<const float4*>(cs + c + 4 * k);
+      *reinterpret_cast<float4*>(sinv + 4 * k) =
+          *reinterpret_cast<const float4*>(cs + 32 + c + 4 * k);
+    }
+    ylo = rope_rotate8(lo, hi, cosv, sinv, false);
+    yhi = rope_rotate8(hi, lo, cosv, sinv, true);
+  }
+  *reinterpret_cast<uint4*>(dst + c) = ylo;
+  *reinterpret_cast<uint4*>(dst + c + 32) = yhi;
+}
+
+__global__ void __launch_bounds__(kAppThreads) latent_append_kernel(const LatentAppendArgs a) {
+  const int pieces = 64 + 4 + 4 * a.H;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int slot = a.slots[t];
+    if (slot < 0) continue;
+    const bool inside = slot < a.rows;
+    if (!inside && threadIdx.x == 0) set_status(a.status, MLA_ERR_PAGE);
+    const float* cs = nullptr;
+    if (a.rope_table) {
+      const int raw = a.positions[t];
+      const int p = min(max(raw, 0), a.table_rows - 1);
+      if (p != raw && threadIdx.x == 0) set_status(a.status, MLA_ERR_KVLEN);
+      cs = a.rope_table + (size_t)p * 64;
+    }
+    for (int i = threadIdx.x; i < pieces; i += kAppThreads) {
+      if (i < 4 * a.H) {
+        const size_t row = ((size_t)t * a.H + (i >> 2)) * 64;
+        rotate_pair(a.q_pe + row, a.q_pe_out + row, (i & 3) * 8, cs);
+      } else if (inside) {
+        const int k = i - 4 * a.H;
+        if (k < 64)
+          reinterpret_cast<uint4*>(a.c_pages + (size_t)slot * 512)[k] =
+              reinterpret_cast<const uint4*>(a.c_new + (size_t)t * 512)[k];
+        else
+          rotate_pair(a.pe_new + (size_t)t * 64, a.pe_pages + (size_t)slot * 64, (k - 64) * 8, cs);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
+  // Enough blocks for one group of tokens per thread, or one warp per sequence, within two
+  // blocks per SM.
+  const int sms = device_sm_count();
+  const int64_t by_tok = ((int64_t)a.T + kPlanThreads * kPlanTok - 1) / (kPlanThreads * kPlanTok);
+  const int64_t by_seq = ((int64_t)std::min(a.B, kPlanChunk) + 7) / 8;
+  const int64_t grid = std::min<int64_t>(std::max(by_tok, by_seq), 2 * (sms > 0 ? sms : 152));
+  paged_plan_kernel<<<(unsigned)grid, kPlanThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  const int grid = std::min(a.T, 8 * (sms > 0 ? sms : 152));
+  latent_append_kernel<<<grid, kAppThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace mla

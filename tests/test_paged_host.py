@@ -1,0 +1,125 @@
+"""What the paged-cache entry points refuse, on the host and before any launch (no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import mla_causal_attention_gb300 as mla
+from mla_causal_attention_gb300 import binding
+from mla_causal_attention_gb300.build import build_library
+
+S = binding.MlaStatus
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_library()
+    return binding.library()
+
+
+@pytest.fixture(scope="module")
+def base():
+    buf = ctypes.create_string_buffer(1 << 16)
+    base.keep = buf
+    return (ctypes.addressof(buf) + 255) & ~255
+
+
+def _no_device():
+    return (S.ERR_CUDA, S.ERR_DEVICE)
+
+
+PLAN = ["ctx_len", "new_len", "B", "block_table", "max_pages", "free_pages", "n_free", "free_head",
+        "page_size", "num_pages", "parent", "T", "cu_q", "kv_len", "slots", "positions",
+        "draft_mask", "free_next", "workspace", "workspace_bytes", "stream"]
+
+
+def _plan_args(base):
+    a = {n: base + 256 * i for i, n in enumerate(PLAN)}
+    a.update(B=2, max_pages=4, n_free=3, page_size=16, num_pages=8, T=5, parent=None,
+             draft_mask=None, workspace_bytes=256, stream=None)
+    return a
+
+
+@pytest.mark.parametrize("change,want", [
+    ({"ctx_len": None}, S.ERR_NULL), ({"new_len": None}, S.ERR_NULL),
+    ({"block_table": None}, S.ERR_NULL), ({"free_pages": None}, S.ERR_NULL),
+    ({"free_head": None}, S.ERR_NULL), ({"cu_q": None}, S.ERR_NULL),
+    ({"kv_len": None}, S.ERR_NULL), ({"slots": None}, S.ERR_NULL),
+    ({"positions": None}, S.ERR_NULL), ({"free_next": None}, S.ERR_NULL),
+    ({"draft_mask": 512}, S.ERR_NULL), ({"parent": 512}, S.ERR_NULL),
+    ({"workspace": None}, S.ERR_WORKSPACE), ({"workspace_bytes": 255}, S.ERR_WORKSPACE),
+    ({"B": 0}, S.ERR_SHAPE), ({"T": 0}, S.ERR_SHAPE), ({"max_pages": 0}, S.ERR_SHAPE),
+    ({"n_free": -1}, S.ERR_SHAPE), ({"page_size": 8}, S.ERR_SHAPE),
+    ({"page_size": 48}, S.ERR_SHAPE), ({"page_size": 2048}, S.ERR_SHAPE),
+    ({"num_pages": 0}, S.ERR_SHAPE), ({"num_pages": 1 << 27}, S.ERR_SHAPE),
+    ({"max_pages": 1 << 27}, S.ERR_SHAPE),
+])
+def test_plan_refuses(lib, base, change, want):
+    a = _plan_args(base)
+    a.update(change)
+    assert lib.mla_paged_plan(*[a[n] for n in PLAN]) == want
+
+
+def test_plan_refuses_alignment_and_alias(lib, base):
+    for name, off in [("slots", 4), ("positions", 8), ("ctx_len", 2), ("block_table", 1),
+                      ("free_next", 2), ("workspace", 4)]:
+        a = _plan_args(base)
+        a[name] += off
+        assert lib.mla_paged_plan(*[a[n] for n in PLAN]) == S.ERR_ALIGN, name
+    a = _plan_args(base)
+    a["free_next"] = a["free_head"]
+    assert lib.mla_paged_plan(*[a[n] for n in PLAN]) == S.ERR_ARG
+    if not torch.cuda.is_available():
+        a = _plan_args(base)
+        assert lib.mla_paged_plan(*[a[n] for n in PLAN]) in _no_device()
+
+
+APPEND = ["c_kv_new", "k_pe_new", "slots", "T", "c_pages", "pe_pages", "num_pages", "page_size",
+          "positions", "rope_table", "table_rows", "q_pe", "H", "q_pe_out", "workspace",
+          "workspace_bytes", "stream"]
+
+
+def _append_args(base):
+    a = {n: base + 256 * i for i, n in enumerate(APPEND)}
+    a.update(T=3, num_pages=2, page_size=16, table_rows=9, H=2, workspace_bytes=256, stream=None)
+    return a
+
+
+@pytest.mark.parametrize("change,want", [
+    ({"c_kv_new": None}, S.ERR_NULL), ({"k_pe_new": None}, S.ERR_NULL),
+    ({"slots": None}, S.ERR_NULL), ({"c_pages": None}, S.ERR_NULL),
+    ({"pe_pages": None}, S.ERR_NULL), ({"positions": None}, S.ERR_NULL),
+    ({"rope_table": None}, S.ERR_NULL),        # q_pe would stay unrotated
+    ({"q_pe": None}, S.ERR_NULL), ({"q_pe_out": None}, S.ERR_NULL),
+    ({"workspace": None}, S.ERR_WORKSPACE), ({"workspace_bytes": 0}, S.ERR_WORKSPACE),
+    ({"T": 0}, S.ERR_SHAPE), ({"H": 0}, S.ERR_SHAPE), ({"table_rows": 0}, S.ERR_SHAPE),
+    ({"page_size": 17}, S.ERR_SHAPE), ({"num_pages": -1}, S.ERR_SHAPE),
+])
+def test_append_refuses(lib, base, change, want):
+    a = _append_args(base)
+    a.update(change)
+    assert lib.mla_latent_append(*[a[n] for n in APPEND]) == want
+
+
+def test_append_refuses_alignment(lib, base):
+    for name in ("c_kv_new", "k_pe_new", "c_pages", "pe_pages", "rope_table", "q_pe", "q_pe_out"):
+        a = _append_args(base)
+        a[name] += 8
+        assert lib.mla_latent_append(*[a[n] for n in APPEND]) == S.ERR_ALIGN, name
+    if not torch.cuda.is_available():
+        a = _append_args(base)
+        assert lib.mla_latent_append(*[a[n] for n in APPEND]) in _no_device()
+
+
+def test_status_names(lib):
+    assert lib.mla_status_string(10).decode().startswith("MLA_ERR_PAGE")
+    assert lib.mla_status_string(11).decode().startswith("MLA_ERR_TREE")
+
+
+def test_binding_refuses_cpu_tensors(lib):
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        mla.mla_paged_plan(i, i, i[None], i, i, 16, 1, 1)
+    x = torch.zeros((1, 16, 512), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mla.mla_latent_append(x[0], x[0], i, x, x)
