@@ -399,6 +399,47 @@ MLA_API mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k
                                      size_t workspace_bytes, void* cuda_stream);
 
 /*
+ * Attention of a step's new tokens over the paged latent cache: drafted token trees
+ * (speculative decoding), runs of tokens in order, or one token per sequence.
+ *
+ * The new tokens' own rows are already in the cache (mla_latent_append), as its last rows:
+ * with n = cu_q[b+1] - cu_q[b] and ctx = kv_len[b] - n, cached token j < ctx of sequence b is
+ * position j and new token i is position ctx + i of the block table's row b.  New token i
+ * attends, per head h, to
+ *   every key j < ctx, and the keys ctx + k (k < n) with
+ *     k <= i                          without draft_mask (tokens in order), or
+ *     bit k of draft_mask[t] set      with it (t = cu_q[b] + i; any bits, so a row may see
+ *                                     nothing: its output is zero; n <= 64)
+ * and the result is that of mla_latent_decode_fwd over those keys:
+ *   s_j = softmax_scale * (W_K[h] c_j . q_nope[t,h] + k_pe_j . q_pe[t,h])
+ *   out[t,h] = W_V[h] sum_j softmax(s)_j c_j,  fp32 softmax
+ * with W_K[h], W_V[h] rows 256 h .. and 256 h + 128 .. of w_kvb.  Cache rows behind kv_len[b]
+ * and other sequences' rows never reach a result, whatever they hold; a new key that the mask
+ * hides from a row takes part with weight zero, so it has to be finite.
+ *
+ *   q_nope [T, H, 128], q_pe [T, H, 64], out [T, H, 128]    bf16; rows from cu_q[B] on of
+ *                                       out are left as they were
+ *   c_pages, pe_pages, block_table [B, max_pages], cu_q [B + 1], kv_len [B]    as above
+ *   draft_mask [T] int64 or NULL        w_kvb [H * 256, 512] bf16
+ * Only the entries of the block table below ceil(kv_len[b] / page_size) are read.
+ * H up to 1024; workspace mla_latent_tree_workspace_bytes(...) bytes, zeroed once.
+ * Device-side problems (the call completes): cu_q not rising within [0, T], kv_len[b] below n
+ * or past max_pages * page_size (MLA_ERR_KVLEN, clamped); a page outside the pool
+ * (MLA_ERR_PAGE, read as zeros); n > 64 with draft_mask (MLA_ERR_TREE: the keys past 64 are
+ * hidden).  The output of such a sequence is not meaningful.
+ */
+MLA_API size_t mla_latent_tree_workspace_bytes(int T, int H, int B, int num_pages,
+                                               int page_size);
+MLA_API mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
+                                       const uint16_t* c_pages, const uint16_t* pe_pages,
+                                       int num_pages, int page_size, const int32_t* block_table,
+                                       int max_pages, const int32_t* kv_len, const int32_t* cu_q,
+                                       const int64_t* draft_mask, const uint16_t* w_kvb, int B,
+                                       int T, int H, float softmax_scale, uint16_t* out,
+                                       void* workspace, size_t workspace_bytes,
+                                       void* cuda_stream);
+
+/*
  * Synchronises cuda_stream, reads the device status word in the workspace, clears it,
  * and returns it (MLA_OK if no kernel recorded a problem since the last read).
  */

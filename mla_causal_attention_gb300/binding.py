@@ -71,7 +71,7 @@ EXPORTED = ("mla_attn_workspace_bytes", "mla_attn_fwd", "mla_attn_fwd_ex",
             "mla_attn_masked_workspace_bytes", "mla_attn_masked_fwd",
             "mla_latent_workspace_bytes", "mla_latent_decode_fwd",
             "mla_oproj_workspace_bytes", "mla_oproj_fwd", "mla_paged_plan",
-            "mla_latent_append")
+            "mla_latent_append", "mla_latent_tree_workspace_bytes", "mla_latent_tree_fwd")
 
 
 def library():
@@ -130,6 +130,11 @@ def library():
                                        sz, p]
         lib.mla_latent_append.restype = i
         lib.mla_latent_append.argtypes = [p, p, p, i, p, p, i, i, p, p, i, p, i, p, p, sz, p]
+        lib.mla_latent_tree_workspace_bytes.restype = sz
+        lib.mla_latent_tree_workspace_bytes.argtypes = [i, i, i, i, i]
+        lib.mla_latent_tree_fwd.restype = i
+        lib.mla_latent_tree_fwd.argtypes = [p, p, p, p, i, i, p, i, p, p, p, p, i, i, i, f, p, p,
+                                            sz, p]
         _lib = lib
         return lib
 
@@ -526,6 +531,45 @@ def mla_latent_append(c_kv_new, k_pe_new, slots, c_pages, pe_pages, positions=No
         pe_pages.data_ptr(), num_pages, page_size, _addr(positions), _addr(rope_table), rows,
         _addr(q_pe), H, _addr(q_pe_out)))
     return q_pe_out
+
+
+def mla_latent_tree_fwd(q_nope, q_pe, c_pages, pe_pages, block_table, kv_len, cu_q, draft_mask,
+                        w_kvb, softmax_scale: float, out=None,
+                        workspace: "Workspace | None" = None, stream=None):
+    """Attention of a step's new tokens over the paged latent cache (their rows appended).
+
+    q_nope [T,H,128], q_pe [T,H,64] packed by sequence; c_pages [num_pages, page_size, 512] /
+    pe_pages [num_pages, page_size, 64]; block_table [B, max_pages], kv_len [B] (with the new
+    tokens), cu_q [B+1] (int32, from mla_paged_plan); draft_mask [T] int64 for token trees, or
+    None for tokens in order (one per sequence: plain decode); w_kvb [H*256,512].  Returns out
+    [T,H,128]; rows from cu_q[B] on are left as they were."""
+    dev = q_nope.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    T, H = q_nope.shape[:2]
+    num_pages, page_size = c_pages.shape[:2]
+    B, max_pages = block_table.shape
+    bf, i32 = torch.bfloat16, torch.int32
+    _check(q_nope, "q_nope", bf, (T, H, 128), dev)
+    _check(q_pe, "q_pe", bf, (T, H, 64), dev)
+    _check(c_pages, "c_pages", bf, (num_pages, page_size, 512), dev)
+    _check(pe_pages, "pe_pages", bf, (num_pages, page_size, 64), dev)
+    _check(block_table, "block_table", i32, (B, max_pages), dev)
+    _check(kv_len, "kv_len", i32, (B,), dev)
+    _check(cu_q, "cu_q", i32, (B + 1,), dev)
+    if draft_mask is not None:
+        _check(draft_mask, "draft_mask", torch.int64, (T,), dev)
+    _check(w_kvb, "w_kvb", bf, (H * 256, 512), dev)
+    if out is None:
+        out = torch.empty((T, H, 128), dtype=bf, device=dev)
+    else:
+        _check(out, "out", bf, (T, H, 128), dev)
+    nbytes = library().mla_latent_tree_workspace_bytes(T, H, B, num_pages, page_size)
+    _enqueue("mla_latent_tree_fwd", dev, stream, workspace, nbytes, (
+        q_nope.data_ptr(), q_pe.data_ptr(), c_pages.data_ptr(), pe_pages.data_ptr(), num_pages,
+        page_size, block_table.data_ptr(), max_pages, kv_len.data_ptr(), cu_q.data_ptr(),
+        _addr(draft_mask), w_kvb.data_ptr(), B, T, H, float(softmax_scale), out.data_ptr()))
+    return out
 
 
 def mla_rope_frequencies(cfg: RopeConfig | None = None):

@@ -98,6 +98,18 @@ size_t latent_workspace(int B, int H, int grid) {
          latent_ml_bytes(B, H, grid) + latent_acc_bytes(B, H, grid);
 }
 
+// Workspace of the tree attention: the status word, then the queries folded into the latent
+// space [T, H, 512] bf16.
+struct TreeLayout {
+  size_t q_lat, total;
+};
+TreeLayout tree_layout(int T, int H, int, int, int, int) {
+  TreeLayout l;
+  l.q_lat = kStatusBytes;
+  l.total = l.q_lat + r256((size_t)T * H * 512 * 2);
+  return l;
+}
+
 // Rotary workspace: rotated queries [B,H,Tq,64] then rotated new rotary keys [B,Tq,64],
 // each on a 256-byte boundary, after the attention call's own workspace.
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -652,6 +664,57 @@ mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k_pe_new,
   a.q_pe_out = q_pe_out; a.status = static_cast<int*>(workspace);
   a.T = T; a.H = q_pe ? H : 0; a.table_rows = table_rows; a.rows = num_pages * page_size;
   return launch_latent_append(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+size_t mla_latent_tree_workspace_bytes(int T, int H, int B, int num_pages, int page_size) {
+  if (T < 1 || H < 1 || H > 1024 || B < 1 || check_pool(num_pages, page_size) != MLA_OK) return 0;
+  int sms = 0;
+  if (check_device(&sms) != MLA_OK || sms <= 0) sms = 152;
+  return tree_layout(T, H, B, num_pages, page_size, sms).total;
+}
+
+mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
+                               const uint16_t* c_pages, const uint16_t* pe_pages, int num_pages,
+                               int page_size, const int32_t* block_table, int max_pages,
+                               const int32_t* kv_len, const int32_t* cu_q,
+                               const int64_t* draft_mask, const uint16_t* w_kvb, int B, int T,
+                               int H, float softmax_scale, uint16_t* out, void* workspace,
+                               size_t workspace_bytes, void* cuda_stream) {
+  if (!q_nope || !q_pe || !c_pages || !pe_pages || !block_table || !kv_len || !cu_q || !w_kvb ||
+      !out)
+    return MLA_ERR_NULL;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  const mla_status ps = check_pool(num_pages, page_size);
+  if (ps != MLA_OK) return ps;
+  if (B < 1 || T < 1 || H < 1 || H > 1024 || max_pages < 1 || B > (1 << 20) ||
+      (int64_t)max_pages * page_size > 0x7fffffff || (int64_t)T * H > (int64_t(1) << 26))
+    return MLA_ERR_SHAPE;
+  if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(c_pages) || !aligned16(pe_pages) ||
+      !aligned16(w_kvb) || !aligned16(out) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(kv_len) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(cu_q) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(draft_mask) & 7u) != 0)
+    return MLA_ERR_ALIGN;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0f)) return MLA_ERR_ARG;
+  int sms = 0;
+  const mla_status st = check_device(&sms);
+  if (st != MLA_OK) return st;
+  const TreeLayout lay = tree_layout(T, H, B, num_pages, page_size, sms);
+  if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  TreeArgs a{};
+  a.q_nope = q_nope; a.q_pe = q_pe; a.c_pages = c_pages; a.pe_pages = pe_pages;
+  a.block_table = block_table; a.kv_len = kv_len; a.cu_q = cu_q; a.draft_mask = draft_mask;
+  a.w_kvb = w_kvb; a.out = out;
+  a.status = reinterpret_cast<int*>(w);
+  a.q_lat = reinterpret_cast<uint16_t*>(w + lay.q_lat);
+  a.num_pages = num_pages; a.page_shift = page_shift(page_size); a.max_pages = max_pages;
+  a.B = B; a.T = T; a.H = H;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  return launch_latent_tree(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }

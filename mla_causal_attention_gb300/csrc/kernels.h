@@ -226,6 +226,28 @@ struct LatentAppendArgs {
 };
 cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream);
 
+// Query folding of the latent paths alone: q_lat [B,H,512] from q_nope [B,H,128] and w_kvb.
+cudaError_t launch_latent_absorb(const LatentArgs& a, cudaStream_t stream);
+
+// Attention of packed new tokens over the paged latent cache (see mla_latent_tree_fwd).
+struct TreeArgs {
+  const uint16_t* q_nope;
+  const uint16_t* q_pe;
+  const uint16_t* c_pages;
+  const uint16_t* pe_pages;
+  const int32_t* block_table;
+  const int32_t* kv_len;
+  const int32_t* cu_q;
+  const int64_t* draft_mask;  // may be null
+  const uint16_t* w_kvb;
+  uint16_t* out;
+  uint16_t* q_lat;  // workspace [T,H,512]
+  int* status;
+  int num_pages, page_shift, max_pages, B, T, H;
+  float scale_log2;
+};
+cudaError_t launch_latent_tree(const TreeArgs& a, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 

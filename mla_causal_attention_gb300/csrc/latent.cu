@@ -883,6 +883,23 @@ bool latent_maps(const LatentArgs& a, LatentParams* p) {
 
 }  // namespace
 
+cudaError_t launch_latent_absorb(const LatentArgs& a, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};  // bit per device: smem attribute set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(latent_absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kAbsorbSmem);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_release);
+  }
+  const unsigned bgroups = (unsigned)((a.B + kPB - 1) / kPB);
+  latent_absorb_kernel<<<dim3(a.H, kLD / kAbN, bgroups), 256, kAbsorbSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_latent(const LatentArgs& a, cudaStream_t stream) {
   LatentParams p;
   if (!latent_maps(a, &p)) return cudaErrorInvalidValue;

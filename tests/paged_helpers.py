@@ -65,3 +65,63 @@ def rotate64(x, table, positions):
     c, s = cs[..., :32], cs[..., 32:]
     lo, hi = x[..., :32].double(), x[..., 32:].double()
     return torch.cat((lo * c - hi * s, hi * c + lo * s), -1)
+
+
+def tree_case(seed, B, H, ctx, new, page, tree, pad=0, dev="cuda"):
+    """Inputs of mla_latent_tree_fwd.  Everything in the pool that no sequence holds is NaN, the
+    rows behind a sequence's last one in its last page too; free table entries are -1."""
+    r, c, n, table, free, num = random_batch(seed, B, ctx, new, page)
+    g = torch.Generator("cpu").manual_seed(seed)
+    mk = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16)  # noqa: E731
+    parents = [random_parents(r, k, roots=True) for k in n]
+    flat = [x for p in parents for x in p]
+    T = sum(n) + pad
+    cu, kv, slots, _, _, mask, table = plan_reference(c, n, table, free, 0, page, T, flat)
+    c_pages = torch.full((num, page, 512), float("nan"), dtype=torch.bfloat16)
+    pe_pages = torch.full((num, page, 64), float("nan"), dtype=torch.bfloat16)
+    for b, k in enumerate(kv):
+        at = torch.tensor([table[b][p // page] * page + p % page for p in range(k)],
+                          dtype=torch.int64)
+        c_pages.view(-1, 512)[at] = mk(k, 512)
+        pe_pages.view(-1, 64)[at] = mk(k, 64)
+    i = lambda x, dt=torch.int32: torch.tensor(x, dtype=dt, device=dev)  # noqa: E731
+    return dict(q_nope=mk(T, H, 128).to(dev), q_pe=mk(T, H, 64).to(dev), c_pages=c_pages.to(dev),
+                pe_pages=pe_pages.to(dev), block_table=i(table), kv_len=i(kv), cu_q=i(cu),
+                draft_mask=i(mask, torch.int64) if tree else None,
+                w_kvb=mk(H * 256, 512).div(512 ** 0.5).to(dev))
+
+
+def tree_reference(d, scale):
+    """(out, spread) in 64 bits from the definition: each head's keys and values spelled out
+    from the latent rows.  spread = sum_j p_j |v_j|, the scale of rounding errors."""
+    T, H = d["q_nope"].shape[:2]
+    page = d["c_pages"].shape[1]
+    cu, kv = d["cu_q"].tolist(), d["kv_len"].tolist()
+    w = d["w_kvb"].double().view(H, 256, 512)
+    out = torch.full((T, H, 128), float("nan"), dtype=torch.float64, device=w.device)
+    spread = out.clone()
+    for b, k in enumerate(kv):
+        lo, hi = cu[b], cu[b + 1]
+        if lo == hi:
+            continue
+        j = torch.arange(k, device=w.device)
+        slot = d["block_table"][b].long()[j // page] * page + j % page
+        c, pe = (d[x].view(-1, n)[slot].double() for x, n in (("c_pages", 512), ("pe_pages", 64)))
+        new = j - (k - (hi - lo))
+        i = torch.arange(hi - lo, device=w.device)
+        if d["draft_mask"] is None:
+            seen = new[None] <= i[:, None]
+        else:
+            seen = (new < 0) | ((d["draft_mask"][lo:hi, None] >> new.clamp(0, 63)) & 1).bool()
+        keys = torch.einsum("jl,hdl->hjd", c, w[:, :128])
+        vals = torch.einsum("jl,hdl->hjd", c, w[:, 128:])
+        x = torch.einsum("ihd,hjd->hij", d["q_nope"][lo:hi].double(), keys)
+        x = (x + torch.einsum("ihd,jd->hij", d["q_pe"][lo:hi].double(), pe)) * scale
+        x = x.masked_fill(~seen, float("-inf"))
+        top = x.amax(-1, keepdim=True).clamp(min=-1e300)
+        e = (x - top).exp()
+        total = e.sum(-1, keepdim=True)
+        p = e / torch.where(total > 0, total, 1.0)
+        out[lo:hi] = torch.einsum("hij,hjd->ihd", p, vals)
+        spread[lo:hi] = torch.einsum("hij,hjd->ihd", p, vals.abs())
+    return out, spread

@@ -123,3 +123,46 @@ def test_binding_refuses_cpu_tensors(lib):
     x = torch.zeros((1, 16, 512), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         mla.mla_latent_append(x[0], x[0], i, x, x)
+
+
+TREE = ["q_nope", "q_pe", "c_pages", "pe_pages", "num_pages", "page_size", "block_table",
+        "max_pages", "kv_len", "cu_q", "draft_mask", "w_kvb", "B", "T", "H", "scale", "out",
+        "workspace", "workspace_bytes", "stream"]
+
+
+def _tree_args(base, lib):
+    a = {n: base + 256 * i for i, n in enumerate(TREE)}
+    a.update(num_pages=4, page_size=16, max_pages=2, B=2, T=3, H=4, scale=0.1, stream=None,
+             workspace_bytes=lib.mla_latent_tree_workspace_bytes(3, 4, 2, 4, 16))
+    return a
+
+
+@pytest.mark.parametrize("change,want", [
+    ({k: None}, S.ERR_NULL) for k in ("q_nope", "q_pe", "c_pages", "pe_pages", "block_table",
+                                      "kv_len", "cu_q", "w_kvb", "out")
+] + [
+    ({"workspace": None}, S.ERR_WORKSPACE), ({"B": 0}, S.ERR_SHAPE), ({"T": 0}, S.ERR_SHAPE),
+    ({"H": 0}, S.ERR_SHAPE), ({"H": 1025}, S.ERR_SHAPE), ({"page_size": 20}, S.ERR_SHAPE),
+    ({"num_pages": 0}, S.ERR_SHAPE), ({"max_pages": 0}, S.ERR_SHAPE),
+    ({"T": 1 << 27}, S.ERR_SHAPE), ({"scale": 0.0}, S.ERR_ARG), ({"scale": float("inf")}, S.ERR_ARG),
+])
+def test_tree_refuses(lib, base, change, want):
+    a = _tree_args(base, lib)
+    a.update(change)
+    assert lib.mla_latent_tree_fwd(*[a[n] for n in TREE]) == want
+
+
+def test_tree_refuses_alignment_and_small_workspaces(lib, base):
+    for name in ("q_nope", "q_pe", "c_pages", "pe_pages", "w_kvb", "out", "workspace"):
+        a = _tree_args(base, lib)
+        a[name] += 8
+        assert lib.mla_latent_tree_fwd(*[a[n] for n in TREE]) == S.ERR_ALIGN, name
+    a = _tree_args(base, lib)
+    a["draft_mask"] += 4
+    assert lib.mla_latent_tree_fwd(*[a[n] for n in TREE]) == S.ERR_ALIGN
+    assert lib.mla_latent_tree_workspace_bytes(0, 4, 2, 4, 16) == 0
+    assert lib.mla_latent_tree_workspace_bytes(3, 4, 2, 4, 24) == 0
+    a = _tree_args(base, lib)
+    a["workspace_bytes"] = 256
+    want = (S.ERR_WORKSPACE,) if torch.cuda.is_available() else _no_device()
+    assert lib.mla_latent_tree_fwd(*[a[n] for n in TREE]) in want

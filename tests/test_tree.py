@@ -1,0 +1,240 @@
+"""Attention of new tokens over the paged latent cache (mla_latent_tree_fwd) against its
+definition in 64 bits.  Every row of the pool that no sequence holds is NaN.
+
+Tolerances.  The kernels round to bf16 four times on the way: the query folded into the latent
+space, the softmax weights, the latent mix, the output.  Each rounding is off by at most half a
+step, 2^-8 of the value, at most 2^-8 / sqrt(3) in the root of the mean square, and they are
+independent: in the 2-norm the result is within 2 * 2^-8 / sqrt(3) = 0.0045 of the reference.
+For one element the scale is spread = sum_j p_j |v_j|: weights and mix err by at most 2^-8 of
+it each, the output by 2^-8 of less, and the folded query moves every score by about 2^-8 of
+itself (scores here are ~N(0, 1): up to five), which is 5 * 2^-8 of the spread: 8 * 2^-8."""
+import pytest
+import torch
+
+import mla_causal_attention_gb300 as mla
+from mla_causal_attention_gb300 import binding
+from mla_causal_attention_gb300.workloads import softmax_scale_192
+from paged_helpers import tree_case, tree_reference
+
+pytestmark = pytest.mark.gpu
+
+S = binding.MlaStatus
+SCALE = softmax_scale_192()
+
+
+def _run(d, **kw):
+    out = mla.mla_latent_tree_fwd(d["q_nope"], d["q_pe"], d["c_pages"], d["pe_pages"],
+                                  d["block_table"], d["kv_len"], d["cu_q"], d["draft_mask"],
+                                  d["w_kvb"], SCALE, **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+def _close(got, d):
+    used = int(d["cu_q"][-1])
+    ref, spread = tree_reference(d, SCALE)
+    err = (got.double() - ref).abs()[:used]
+    if used == 0:
+        return
+    assert bool(torch.isfinite(got[:used]).all())
+    rel = float(err.norm() / ref[:used].norm().clamp(min=1e-30))
+    worst = float((err / (spread[:used] + 1e-30)).max()) if float(spread[:used].max()) else 0.0
+    print(f"[tree] rel {rel:.2e} worst {worst * 256:.2f} * 2^-8")
+    assert rel <= 0.0045 and bool((err <= 8 * 2 ** -8 * spread[:used] + 1e-30).all())
+
+
+CASES = [
+    # B, H, cached, new, page, tree
+    (1, 64, (0, 0), (1, 1), 64, False),         # a single key
+    (1, 64, (1000, 1000), (8, 8), 64, True),
+    (1, 64, (1000, 1000), (1, 1), 64, False),   # plain decode
+    (5, 64, (0, 600), (0, 5), 16, True),        # sequences without new tokens among others
+    (3, 16, (100, 900), (1, 64), 32, True),
+    (2, 64, (0, 0), (64, 64), 64, True),        # no cached keys: the tree alone
+    (2, 64, (63, 65), (63, 64), 64, False),     # tokens in order, tiles and pages end inside
+    (4, 3, (0, 300), (1, 40), 16, True),        # head counts that fill no block of rows
+    (3, 1, (0, 300), (1, 64), 128, True),
+    (2, 5, (127, 129), (1, 3), 1024, False),
+    (2, 128, (200, 300), (1, 3), 64, True),     # more heads than Kimi K2's 64
+    (1, 8, (9000, 9000), (17, 17), 128, True),  # long: split over the keys
+    (2, 64, (0, 10), (300, 400), 64, False),    # a chunk of a prompt, more than 64 tokens
+    (150, 8, (0, 200), (1, 3), 16, True),       # more sequences than there are CTA pairs
+    (40, 64, (1, 700), (1, 20), 64, True),
+]
+
+
+@pytest.mark.parametrize("B,H,ctx,new,page,tree", CASES)
+def test_tree_matches_definition(B, H, ctx, new, page, tree):
+    d = tree_case(B * 7 + H, B, H, ctx, new, page, tree, pad=3)
+    out = torch.full((d["q_nope"].shape[0], H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = _run(d, out=out)
+    assert got is out and mla.mla_attn_get_status() == 0
+    _close(got, d)
+    assert bool((got[int(d["cu_q"][-1]):] == 7.0).all())  # rows behind the last sequence
+
+
+def test_tree_random_sweep():
+    import random
+    r = random.Random(11)
+    for k in range(12):
+        B, H = r.choice((1, 2, 9, 33)), r.choice((2, 7, 16, 48, 64))
+        ctx, new = r.randint(0, 1500), r.randint(1, 64)
+        page, tree = r.choice((16, 32, 64, 128, 256)), r.random() < 0.7
+        d = tree_case(1000 + k, B, H, (0, ctx), (0, new), page, tree, pad=1)
+        print(B, H, ctx, new, page, tree)
+        _close(_run(d), d)
+    assert mla.mla_attn_get_status() == 0
+
+
+def test_any_mask_and_rows_that_see_nothing():
+    """Bits of any kind; with nothing cached and no bit set a row is zero, and its neighbours
+    in the same block of rows are as they would be."""
+    d = tree_case(5, 3, 64, (0, 0), (20, 64), 16, True)
+    g = torch.Generator("cpu").manual_seed(1)
+    m = torch.randint(-2 ** 62, 2 ** 62, d["draft_mask"].shape, generator=g, dtype=torch.int64)
+    m[::3] = 0
+    m[4] = 1 << 40  # past the sequence's last key, or not: hidden either way if it is
+    d["draft_mask"] = m.cuda()
+    got = _run(d)
+    _close(got, d)
+    assert bool((got[::3] == 0).all())
+    # with cached keys a zero mask leaves those
+    d = tree_case(6, 2, 16, (50, 200), (5, 5), 16, True)
+    d["draft_mask"].zero_()
+    _close(_run(d), d)
+
+
+def test_large_scores():
+    """Scores of a few hundred: the running maximum moves by more than the type's range."""
+    d = tree_case(8, 3, 64, (300, 900), (1, 20), 32, True)
+    d["q_nope"] *= 24
+    got = _run(d)
+    ref, spread = tree_reference(d, SCALE)
+    # scores ~N(0, 20^2): the folded query's rounding moves them by up to 100 * 2^-8, so single
+    # weights are off by a factor; what has to hold is that rows stay finite mixes of the values
+    assert bool(torch.isfinite(got).all())
+    assert bool((got.double() - ref).abs().mean() < 0.5 * spread.mean())
+
+
+def test_equal_scores_average_the_values():
+    """q = 0: every visible key has the same weight, and the mix is the mean."""
+    d = tree_case(9, 2, 64, (700, 1500), (3, 9), 64, True)
+    d["q_nope"].zero_()
+    d["q_pe"].zero_()
+    _close(_run(d), d)
+
+
+def test_tree_runs_on_a_side_stream_and_under_a_graph():
+    d = tree_case(10, 6, 64, (0, 900), (1, 12), 64, True, pad=5)
+    e = tree_case(11, 6, 64, (0, 900), (1, 12), 64, True, pad=5)
+    T = max(d["q_nope"].shape[0], e["q_nope"].shape[0])
+    width = max(d["block_table"].shape[1], e["block_table"].shape[1])
+    num = max(d["c_pages"].shape[0], e["c_pages"].shape[0])
+
+    def fit(c):
+        f = dict(c)
+        for k, n in (("q_nope", T), ("q_pe", T), ("draft_mask", T), ("c_pages", num),
+                     ("pe_pages", num)):
+            f[k] = torch.zeros((n,) + c[k].shape[1:], dtype=c[k].dtype, device="cuda")
+            f[k][:c[k].shape[0]] = c[k]
+        f["block_table"] = torch.full((6, width), -1, dtype=torch.int32, device="cuda")
+        f["block_table"][:, :c["block_table"].shape[1]] = c["block_table"]
+        return f
+
+    d, e = fit(d), fit(e)
+    want = {k: _run(x).clone() for k, x in (("d", d), ("e", e))}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    side = _run(d, stream=s, workspace=mla.Workspace())
+    used = int(d["cu_q"][-1])
+    assert torch.equal(side[:used], want["d"][:used])
+    st = {k: v.clone() for k, v in d.items()}
+    out, ws = torch.empty_like(want["d"]), mla.Workspace()
+    _run(st, out=out, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mla.mla_latent_tree_fwd(st["q_nope"], st["q_pe"], st["c_pages"], st["pe_pages"],
+                                st["block_table"], st["kv_len"], st["cu_q"], st["draft_mask"],
+                                st["w_kvb"], SCALE, out=out, workspace=ws)
+    for name, c in (("e", e), ("d", d)):
+        for k, v in c.items():
+            st[k].copy_(v)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        n = int(c["cu_q"][-1])
+        assert torch.equal(out[:n], want[name][:n])
+        assert bool((out[n:] == 0).all())
+    assert mla.mla_attn_get_status() == 0
+
+
+def test_tree_reports_what_only_the_device_sees():
+    mla.mla_attn_get_status()
+    d = tree_case(12, 3, 16, (20, 60), (2, 4), 16, True)
+    good = _run(d)
+    cu = d["cu_q"].tolist()
+
+    def other(**change):
+        e = dict(d)
+        e.update(change)
+        return _run(e)
+
+    kv = d["kv_len"].clone()
+    kv[1] = 1 << 30
+    out = other(kv_len=kv)
+    st = mla.mla_attn_get_status()  # the clamped length may also meet entries that hold no page
+    assert st in (S.ERR_KVLEN, S.ERR_PAGE)
+    assert torch.equal(out[:cu[1]], good[:cu[1]]) and torch.equal(out[cu[2]:], good[cu[2]:])
+    kv[1] = 1
+    out = other(kv_len=kv)
+    assert mla.mla_attn_get_status() == S.ERR_KVLEN
+    assert torch.equal(out[cu[2]:], good[cu[2]:])
+    table = d["block_table"].clone()
+    table[0, 0] = d["c_pages"].shape[0]
+    out = other(block_table=table)
+    assert mla.mla_attn_get_status() == S.ERR_PAGE
+    assert torch.equal(out[cu[1]:], good[cu[1]:])
+    table[0, 0] = -1
+    other(block_table=table)
+    assert mla.mla_attn_get_status() == S.ERR_PAGE
+    wide = tree_case(13, 1, 2, (5, 5), (70, 70), 16, False)
+    wide["draft_mask"] = torch.ones(70, dtype=torch.int64, device="cuda")
+    _run(wide)
+    assert mla.mla_attn_get_status() == S.ERR_TREE
+    cu_bad = d["cu_q"].clone()
+    cu_bad[3] = 1000
+    other(cu_q=cu_bad)
+    assert mla.mla_attn_get_status() == S.ERR_KVLEN
+
+
+def test_tree_agrees_with_the_dense_latent_decode():
+    """One token per sequence is mla_latent_decode_fwd on the same rows laid end to end."""
+    d = tree_case(14, 4, 64, (10, 500), (1, 1), 64, False)
+    kv, page = d["kv_len"].tolist(), 64
+    Tk = max(kv)
+    c = torch.zeros((4, Tk, 512), dtype=torch.bfloat16, device="cuda")
+    pe = torch.zeros((4, Tk, 64), dtype=torch.bfloat16, device="cuda")
+    for b, k in enumerate(kv):
+        j = torch.arange(k, device="cuda")
+        slot = d["block_table"][b].long()[j // page] * page + j % page
+        c[b, :k], pe[b, :k] = d["c_pages"].view(-1, 512)[slot], d["pe_pages"].view(-1, 64)[slot]
+    dense = mla.mla_latent_decode_fwd(d["q_nope"], d["q_pe"], c, pe, d["w_kvb"], d["kv_len"], SCALE)
+    ref, spread = tree_reference(d, SCALE)
+    got = _run(d)
+    for x in (dense, got):
+        assert bool(((x.double() - ref).abs() <= 8 * 2 ** -8 * spread).all())
+
+
+def test_a_pool_past_four_gigabytes():
+    """Pages whose byte offset does not fit 32 bits."""
+    page, num = 1024, 4300
+    d = tree_case(15, 2, 16, (1500, 2500), (4, 9), page, True)
+    big = {k: torch.empty((num, page, n), dtype=torch.bfloat16, device="cuda")
+           for k, n in (("c_pages", 512), ("pe_pages", 64))}
+    n_small = d["c_pages"].shape[0]
+    far = torch.tensor([num - 1 - 7 * k for k in range(n_small)], device="cuda")
+    for k in big:
+        big[k][far] = d[k]
+    table = torch.where(d["block_table"] >= 0, far[d["block_table"].clamp(min=0).long()].int(), -1)
+    e = dict(d, block_table=table.contiguous(), **big)
+    assert torch.equal(_run(e), _run(d))
