@@ -98,15 +98,26 @@ size_t latent_workspace(int B, int H, int grid) {
          latent_ml_bytes(B, H, grid) + latent_acc_bytes(B, H, grid);
 }
 
-// Workspace of the tree attention: the status word, then the queries folded into the latent
-// space [T, H, 512] bf16.
+// Workspace of the tree attention: the status word; the queries folded into the latent space
+// [T, H, 512] bf16; the partition; and two partial results of 128 rows x (512 + 2) floats for
+// each of the ranges the key tiles are cut into.  One range per CTA pair, or several when the
+// pool is larger than what L2 holds of it at a time (the device decides from the lengths).
 struct TreeLayout {
-  size_t q_lat, total;
+  size_t q_lat, tile0, ranges, part_ml, part_acc, total;
+  int pairs, max_ranges;
 };
-TreeLayout tree_layout(int T, int H, int, int, int, int) {
+TreeLayout tree_layout(int T, int H, int B, int num_pages, int page_size, int sms) {
   TreeLayout l;
+  l.pairs = std::max(1, sms / 2);
+  const int64_t pool = (int64_t)num_pages * page_size * 1152;
+  const int64_t rounds = (pool + kTreeRoundBytes - 1) / kTreeRoundBytes;
+  l.max_ranges = l.pairs * (int)std::min<int64_t>(std::max<int64_t>(rounds, 1), kTreeMaxRounds);
   l.q_lat = kStatusBytes;
-  l.total = l.q_lat + r256((size_t)T * H * 512 * 2);
+  l.tile0 = l.q_lat + r256((size_t)T * H * 512 * 2);
+  l.ranges = l.tile0 + r256((size_t)(B + 1) * 8);
+  l.part_ml = l.ranges + 256;
+  l.part_acc = l.part_ml + r256((size_t)2 * l.max_ranges * 128 * 2 * 4);
+  l.total = l.part_acc + r256((size_t)2 * l.max_ranges * 128 * 512 * 4);
   return l;
 }
 
@@ -711,8 +722,12 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
   a.w_kvb = w_kvb; a.out = out;
   a.status = reinterpret_cast<int*>(w);
   a.q_lat = reinterpret_cast<uint16_t*>(w + lay.q_lat);
+  a.tile0 = reinterpret_cast<int64_t*>(w + lay.tile0);
+  a.ranges = reinterpret_cast<int32_t*>(w + lay.ranges);
+  a.part_ml = reinterpret_cast<float*>(w + lay.part_ml);
+  a.part_acc = reinterpret_cast<float*>(w + lay.part_acc);
   a.num_pages = num_pages; a.page_shift = page_shift(page_size); a.max_pages = max_pages;
-  a.B = B; a.T = T; a.H = H;
+  a.B = B; a.T = T; a.H = H; a.pairs = lay.pairs; a.max_ranges = lay.max_ranges;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   return launch_latent_tree(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MLA_OK

@@ -226,9 +226,6 @@ struct LatentAppendArgs {
 };
 cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream);
 
-// Query folding of the latent paths alone: q_lat [B,H,512] from q_nope [B,H,128] and w_kvb.
-cudaError_t launch_latent_absorb(const LatentArgs& a, cudaStream_t stream);
-
 // Attention of packed new tokens over the paged latent cache (see mla_latent_tree_fwd).
 struct TreeArgs {
   const uint16_t* q_nope;
@@ -241,11 +238,19 @@ struct TreeArgs {
   const int64_t* draft_mask;  // may be null
   const uint16_t* w_kvb;
   uint16_t* out;
-  uint16_t* q_lat;  // workspace [T,H,512]
+  uint16_t* q_lat;   // workspace [T,H,512]: folded queries, then the mixes of whole units
+  int64_t* tile0;    // workspace [B+1]: first tile of each sequence, then all tiles (W)
+  int32_t* ranges;   // workspace [1]: ranges the tiles are cut into
+  float* part_ml;    // workspace [2 max_ranges][128][2]
+  float* part_acc;   // workspace [2 max_ranges][128][512]
   int* status;
   int num_pages, page_shift, max_pages, B, T, H;
+  int pairs, max_ranges;
   float scale_log2;
 };
+// Latent rows that the CTA pairs of one round walk through together (see tree.cu).
+constexpr int64_t kTreeRoundBytes = 64 << 20;
+constexpr int kTreeMaxRounds = 5;
 cudaError_t launch_latent_tree(const TreeArgs& a, cudaStream_t stream);
 
 // Number of SMs of the current device (cached per device).

@@ -1,133 +1,856 @@
-// tree.cu -- attention of packed new tokens over the paged latent cache.
+// tree.cu -- attention of packed new tokens over the paged latent cache, on CTA pairs.
 //
 // For new token t of sequence b and head h, over the keys j the token sees,
 //   s_j = scale * (q_lat[t,h] . c_j + q_pe[t,h] . k_pe_j),   q_lat = W_K[h]^T q_nope
 //   out = W_V[h] (sum_j softmax(s)_j c_j)
-// (the up-projection kv_b_proj folded into the query and applied once to the mix).
+// (the up-projection kv_b_proj folded into the query and applied once to the mix).  All tokens
+// and heads of a sequence read the same latent rows, so its n * H rows of queries form one
+// matrix, cut into units of 128 rows, against tiles of 128 keys.
+//
+// Kernels, each a programmatic dependent launch of the one before:
+//   tree_absorb_kernel   q_lat, and the partition of the work (block 0)
+//   tree_split_kernel    the attention over the latent rows, flash style
+//   tree_up_kernel       merges partial mixes, then out = W_V mix
+//
+// What bounds it: per row and key 2 * (576 + 512) operations against 1152 bytes per key, read
+// once for all rows of a sequence: one token per sequence (64 rows) is bound by HBM, from about
+// four tokens on the tensor cores are.  Each unit's mix is 128 rows x 512 columns of fp32, all
+// of an SM's TMEM; a pair of CTAs holds 64 rows each instead (256 of the 512 TMEM columns,
+// tcgen05 cta_group::2 with M = 128), which leaves room for two score tiles, and each CTA
+// stages only its half of the keys (scores) and of the latent columns (mix): 72 KB + 64 KB in
+// shared memory beside the queries' 72 KB.  So the next tile's scores run on the tensor cores
+// while this tile's softmax is computed.
+//
+// Per tile of 128 keys:  S = Q K^T   M128 N128 K576: CTA r stages keys 64 r .. 64 r + 63
+//                        O += P C    M128 N256 K128, twice: CTA r stages latent columns
+//                                    256 n + 128 r .. + 127 of all 128 keys
+// Warps: 0 keys' and queries' TMA, 1 MMA issue (even CTA), 2 latent columns' TMA, 4-7 softmax.
+// TMEM: S tiles at columns 0 and 64, O blocks n at 128 and 256.  Softmax thread (row r, half g)
+// = lane 64 g + r holds the scores of keys 64 g .. 64 g + 63 of its row, and the mix columns
+// 256 n + 128 g + c.
 #include <cuda.h>
 
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "kernels.h"
+#include "latent_proj.cuh"
 #include "ptx.cuh"
+#include "tcgen05.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kWarps = 8;
+using namespace proj;
 
-// The keys of a sequence and the part of them that are new tokens, clamped for safety.
+constexpr int kTile = 128;       // keys per tile
+constexpr int kRows = 128;       // query rows per unit, 64 per CTA
+constexpr int kSubQ = 64 * 128;  // 64 rows x 64 columns, bf16, 128-byte swizzled
+constexpr int kSubV = 128 * 128; // 128 keys x 64 columns
+constexpr int kThreads = 256;
+constexpr int kOffQ = 0;                     // 9 sub-tiles: q_lat columns 0-511, q_pe
+constexpr int kOffK = kOffQ + 9 * kSubQ;     // 9 sub-tiles: latent columns 0-511, rotary key
+constexpr int kOffV = kOffK + 9 * kSubQ;     // 4 sub-tiles: columns 256 n + 128 r + 64 s
+constexpr int kOffP = kOffV + 4 * kSubV;     // weights: 2 sub-tiles of 64 keys
+constexpr int kOffRed = kOffP + 2 * kSubQ;   // [2 tile parities][2 halves][64 rows] floats
+constexpr int kOffBar = kOffRed + 1024;
+constexpr int kSmem = kOffBar + 256 + 1024;  // + barriers + alignment slack
+static_assert(kSmem <= 232448, "shared memory per block");
+constexpr uint32_t kColO = 128;
+constexpr float kRescale = 8.0f;  // log2 units: the mix is rescaled when the maximum grows by more
+
+struct TreeParams {
+  CUtensorMap tm_q;   // q_lat {512, T*H}, boxes {64, 64}
+  CUtensorMap tm_qr;  // q_pe  {64,  T*H}
+  CUtensorMap tm_c;   // c_pages  {512, slots}, boxes {64, min(page, 64)}
+  CUtensorMap tm_kr;  // pe_pages {64,  slots}
+  TreeArgs a;
+};
+
+// Barriers.  "even": used in the even CTA only (both CTAs arrive there).
+struct TBars {
+  uint64_t q_full;      // even: the segment's queries landed in both CTAs
+  uint64_t q_empty;     // the segment's last score MMA has read them
+  uint64_t k_full[3];   // even: sub-tiles 3 g .. 3 g + 2 of the keys landed in both CTAs
+  uint64_t k_empty[3];
+  uint64_t v_full[2];   // even: latent columns of block n landed in both CTAs
+  uint64_t v_empty;     // block 0's columns read (block 1's: mix_done)
+  uint64_t v_tail;      // this CTA's columns of a tile that ends inside, before the zeroing
+  uint64_t s_full[2];   // scores of a tile in TMEM
+  uint64_t p_ready;     // even: weights of a tile written (8 warps)
+  uint64_t mix_done;    // the tile's mix added: weights and columns read, O up to date
+  uint64_t o_free;      // even: O of the segment read out (8 warps)
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(TBars) <= 256, "barrier block");
+
+// ---- the partition -----------------------------------------------------------------------
+// Sequence b has n_b H rows in M_b units and K_b key tiles.  The tiles of all units, laid end
+// to end in the order (sequence, unit, key), are cut into V ranges of equal length (to within
+// one tile), and pair c takes ranges c, c + pairs, ...: V = pairs, or several times that when
+// units share many keys, so that the pairs walk through the keys of few sequences at a time and
+// find them in L2.  A range's tiles of one unit are a segment; a unit within one range is
+// finished there, the others leave a partial mix each: in slot 2 v if it is the first segment
+// of range v, else (the last) in 2 v + 1.
 struct TreeSeq {
   int q0, n, kv, ctx;
+  bool bad;
 };
-__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool* bad) {
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
   const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], k = a.kv_len[b];
   TreeSeq s;
   s.q0 = min(max(c0, 0), a.T);
   s.n = min(max(c1, s.q0), a.T) - s.q0;
   s.kv = (int)min((int64_t)max(k, 0), (int64_t)a.max_pages << a.page_shift);
   s.ctx = max(s.kv - s.n, 0);
-  if (s.q0 != c0 || s.q0 + s.n != c1 || s.kv != k || s.kv < s.n) *bad = true;
+  s.bad = s.q0 != c0 || s.q0 + s.n != c1 || s.kv != k || s.kv < s.n;
   return s;
 }
+__device__ __forceinline__ int seq_units(const TreeArgs& a, const TreeSeq& s) {
+  return (s.n * a.H + kRows - 1) / kRows;
+}
+__device__ __forceinline__ int seq_tiles(const TreeSeq& s) { return (s.kv + kTile - 1) / kTile; }
+__device__ __forceinline__ int64_t range_start(int64_t v, int64_t W, int64_t V) { return v * W / V; }
 
-// One block per (token, head): warps take keys in turn, lane l holds latent columns
-// 16 l .. 16 l + 15 and rotary columns 2 l, 2 l + 1.
-__global__ void __launch_bounds__(kWarps * 32) latent_tree_kernel(const TreeArgs a) {
-  __shared__ float s_acc[kWarps][512];
-  __shared__ float s_m[kWarps], s_l[kWarps];
-  const int t = blockIdx.x, h = blockIdx.y;
+// Prefix sums of M_b K_b over the sequences, by one block; also the choice of V.
+__device__ void tree_partition(const TreeArgs& a) {
+  __shared__ int64_t s_w[8], s_shared[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t total = 0, shared_keys = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 256) {
+    const int b = b0 + tid;
+    int64_t w = 0, again = 0;
+    if (b < a.B) {
+      const TreeSeq s = tree_seq(a, b);
+      if (s.bad) set_status(a.status, MLA_ERR_KVLEN);
+      if (a.draft_mask && s.n > 64) set_status(a.status, MLA_ERR_TREE);
+      const int units = seq_units(a, s);
+      w = (int64_t)units * seq_tiles(s);
+      if (units > 1) again = seq_tiles(s);
+    }
+    int64_t inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) again += __shfl_xor_sync(0xffffffffu, again, o);
+    if (lane == 31) {
+      s_w[warp] = inc;
+      s_shared[warp] = again;
+    }
+    __syncthreads();
+    int64_t before = total;
+    for (int k = 0; k < 8; ++k) {
+      if (k < warp) before += s_w[k];
+      total += s_w[k];
+      shared_keys += s_shared[k];
+    }
+    if (b < a.B) a.tile0[b] = before + inc - w;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.tile0[a.B] = total;
+    const int64_t rounds =
+        max((shared_keys * (kTile * 1152) + kTreeRoundBytes - 1) / kTreeRoundBytes, (int64_t)1);
+    a.ranges[0] = (int)min(min(rounds * a.pairs, (int64_t)a.max_ranges), max(total, (int64_t)1));
+  }
+}
+
+__global__ void __launch_bounds__(256) tree_absorb_kernel(const TreeArgs a) {
+  grid_dep_launch();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) tree_partition(a);
+  absorb_block(a.q_nope, a.w_kvb, a.q_lat, a.T, a.H, blockIdx.x, blockIdx.y * kAbN,
+               blockIdx.z * kPB);
+}
+
+// One segment: rows 128 m .. of sequence b's rows, key tiles [k0, k1).
+struct Seg {
+  int b, m, k0, k1;
+  TreeSeq s;
+  int64_t slot;  // partial slot, or -1: the unit is finished here
+};
+// Walks the segments of a pair's ranges.  Warp-uniform; every role has its own.
+struct SegWalk {
+  int64_t W, V, v, x, x1, first_x, base, next_base;
+  int b, step, K;
+  TreeSeq s;
+  __device__ __forceinline__ SegWalk(const TreeArgs& a, int pair) {
+    W = a.tile0[a.B];
+    V = a.ranges[0];
+    v = (int64_t)pair - a.pairs;
+    step = a.pairs;
+    x = x1 = 0;
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a, Seg& g) {
+    if (x >= x1) {
+      v += step;
+      if (v >= V || W == 0) return false;
+      x = first_x = range_start(v, W, V);
+      x1 = range_start(v + 1, W, V);
+      int lo = 0, hi = a.B;  // the last sequence that starts at or before x
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.tile0[mid] <= x) lo = mid; else hi = mid;
+      }
+      enter(a, lo);
+    }
+    while (x >= next_base) enter(a, b + 1);  // skips sequences without work
+    const int64_t off = x - base;
+    g.b = b;
+    g.m = (int)(off / K);
+    g.k0 = (int)(off - (int64_t)g.m * K);
+    g.k1 = (int)min((int64_t)K, g.k0 + (x1 - x));
+    g.s = s;
+    g.slot = g.k0 == 0 && g.k1 == K ? -1 : x == first_x ? 2 * v : 2 * v + 1;
+    x += g.k1 - g.k0;
+    return true;
+  }
+  __device__ __forceinline__ void enter(const TreeArgs& a, int seq) {
+    b = seq;
+    base = a.tile0[b];
+    next_base = a.tile0[b + 1];
+    s = tree_seq(a, b);
+    K = seq_tiles(s);
+  }
+};
+
+// Page rows of a tile: lane l gets the pool row at which box l of `box` keys from key j on
+// starts, or the pool's end (read as zeros) where the table holds no page.
+__device__ __forceinline__ int box_row(const TreeArgs& a, int b, int kv, int j, int lane, int box) {
+  const int key = j + lane * box;
+  if (key >= kv) return 0;  // not loaded
+  const int page = a.block_table[(int64_t)b * a.max_pages + (key >> a.page_shift)];
+  if (page < 0 || page >= a.num_pages) {
+    set_status(a.status, MLA_ERR_PAGE);
+    return a.num_pages << a.page_shift;
+  }
+  return (page << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+}
+
+// Which of the 64 keys from `key` on a row sees: the bits of the new tokens' mask (or, without
+// one, the tokens up to its own), every cached key, none from kv on.
+__device__ __forceinline__ uint64_t seen_bits(int key, int ctx, int kv, bool masked, uint64_t mask,
+                                              int i) {
+  const int left = kv - key;  // keys that exist
+  const uint64_t exist = left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
+  const int off = key - ctx;  // index of the first key among the new tokens
+  uint64_t w;
+  if (masked) {
+    if (off >= 0)
+      w = off < 64 ? mask >> off : 0ull;
+    else
+      w = off <= -64 ? ~0ull : (mask << -off) | ((1ull << -off) - 1);
+  } else {
+    const int cnt = i + 1 - off;
+    w = cnt >= 64 ? ~0ull : cnt <= 0 ? 0ull : (1ull << cnt) - 1;
+  }
+  return w & exist;
+}
+
+// Barrier over the four softmax warps that ANDs a predicate across them: they leave the loops
+// together when one of them gave up waiting.
+__device__ __forceinline__ bool softmax_and(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n"
+      " bar.red.and.pred po, 1, 128, pi;\n selp.u32 %0, 1, 0, po;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]),
+                 "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    tree_split_kernel(const __grid_constant__ TreeParams p) {
+  namespace tp = tc::pair;
+  grid_dep_launch();
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  uint8_t* sQ = smem + kOffQ;
+  uint8_t* sK = smem + kOffK;
+  uint8_t* sV = smem + kOffV;
+  uint8_t* sP = smem + kOffP;
+  TBars* bars = reinterpret_cast<TBars*>(smem + kOffBar);
+  volatile int* abort_flag = &bars->abort_flag;
+  const TreeArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)tp::cta_rank();
+  const int pair_id = blockIdx.x >> 1;
+  int* status = a.status;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 2);
+    mbar_init(&bars->q_empty, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&bars->k_full[i], 2);
+      mbar_init(&bars->k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->v_full[i], 2);
+      mbar_init(&bars->s_full[i], 1);
+    }
+    mbar_init(&bars->v_empty, 1);
+    mbar_init(&bars->v_tail, 1);
+    mbar_init(&bars->p_ready, 8);
+    mbar_init(&bars->mix_done, 1);
+    mbar_init(&bars->o_free, 8);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tp::tmem_alloc(&bars->tmem_base, 512);
+    tp::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tp::cluster_sync();  // both CTAs' barriers are ready before either signals the other's
+  tc::fence_after_sync();
+  const uint32_t tbase = bars->tmem_base;
+  grid_dep_wait();  // the partition and the folded queries
+  SegWalk walk(a, pair_id);
+  Seg g;
+  const int box = min(1 << a.page_shift, 64);  // keys per TMA box
+  const int boxes = 64 / box;                  // boxes per 64 keys
+
+  if (warp == 0) {
+    // ================= keys and queries =================
+    if (lane == 0) {
+      prefetch_tmap(&p.tm_q);
+      prefetch_tmap(&p.tm_qr);
+      prefetch_tmap(&p.tm_c);
+      prefetch_tmap(&p.tm_kr);
+    }
+    const uint32_t q_full = tp::even_addr(&bars->q_full);
+    uint32_t k_full[3];
+    for (int i = 0; i < 3; ++i) k_full[i] = tp::even_addr(&bars->k_full[i]);
+    uint32_t t = 0;  // tiles over the run
+    int ns = 0;      // segments
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      if (ns > 0) ok = tp::wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        const int row = g.s.q0 * a.H + g.m * kRows + 64 * rank;
+        tp::arrive_expect_tx(q_full, 9 * kSubQ);
+        for (int s = 0; s < 8; ++s) tp::tma_load_3d(sQ + s * kSubQ, &p.tm_q, q_full, 64 * s, row, 0);
+        tp::tma_load_3d(sQ + 8 * kSubQ, &p.tm_qr, q_full, 0, row, 0);
+      }
+      ++ns;
+      int rows_next = box_row(a, g.b, g.s.kv, g.k0 * kTile + 64 * rank, lane & 7, box);
+      for (int k = g.k0; k < g.k1; ++k, ++t) {
+        const int rows = rows_next;
+        const int j = k * kTile + 64 * rank;
+        if (k + 1 < g.k1) rows_next = box_row(a, g.b, g.s.kv, j + kTile, lane & 7, box);
+        const int left = min(max(g.s.kv - j, 0), 64);
+        const int nb = (left + box - 1) / box;  // boxes that hold a key
+        for (int grp = 0; grp < 3; ++grp) {
+          if (t > 0) ok = tp::wait(&bars->k_empty[grp], (t - 1) & 1, status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) tp::arrive_expect_tx(k_full[grp], 3 * nb * box * 128);
+          for (int q = 0; q < nb; ++q) {
+            const int row = __shfl_sync(0xffffffffu, rows, q);
+            if (lane == 0) {
+              uint8_t* dst = sK + 3 * grp * kSubQ + q * box * 128;
+              for (int s = 0; s < 3; ++s) {
+                const int sub = 3 * grp + s;
+                if (sub < 8)
+                  tp::tma_load_3d(dst + s * kSubQ, &p.tm_c, k_full[grp], 64 * sub, row, 0);
+                else
+                  tp::tma_load_3d(dst + s * kSubQ, &p.tm_kr, k_full[grp], 0, row, 0);
+              }
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp == 2) {
+    // ================= latent columns of the mix =================
+    uint32_t v_full[2];
+    for (int i = 0; i < 2; ++i) v_full[i] = tp::even_addr(&bars->v_full[i]);
+    const uint32_t v_tail = smem_u32(&bars->v_tail);
+    uint32_t t = 0, tails = 0;
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      int rows_next = box_row(a, g.b, g.s.kv, g.k0 * kTile, lane & 15, box);
+      for (int k = g.k0; k < g.k1; ++k, ++t) {
+        const int rows = rows_next;
+        const int j = k * kTile;
+        if (k + 1 < g.k1) rows_next = box_row(a, g.b, g.s.kv, j + kTile, lane & 15, box);
+        const int left = min(g.s.kv - j, kTile);  // > 0
+        const int nb = (left + box - 1) / box;
+        const bool tail = left < kTile;
+        if (tail && lane == 0) mbar_arrive_expect_tx(&bars->v_tail, 4 * nb * box * 128);
+        for (int n = 0; n < 2; ++n) {
+          if (t > 0)
+            ok = tp::wait(n ? &bars->mix_done : &bars->v_empty, (t - 1) & 1, status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (!tail && lane == 0) tp::arrive_expect_tx(v_full[n], 2 * kSubV);
+          for (int q = 0; q < nb; ++q) {
+            const int row = __shfl_sync(0xffffffffu, rows, q);
+            if (lane == 0) {
+              uint8_t* dst = sV + 2 * n * kSubV + q * box * 128;
+              for (int s = 0; s < 2; ++s)
+                tp::tma_load_3d(dst + s * kSubV, &p.tm_c, tail ? v_tail : v_full[n],
+                                256 * n + 128 * rank + 64 * s, row, 0);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (tail) {
+          // Rows behind the last key hold whatever the page or an earlier tile held there: their
+          // weight is zero, but zero times an infinity is not, so they are cleared.
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_tail, tails & 1, status, abort_flag));
+          if (!ok) break;
+          ++tails;
+          for (int i = left * 8 + lane; i < kTile * 8; i += 32)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              *reinterpret_cast<uint4*>(sV + s * kSubV + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          asm volatile("fence.proxy.async;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tp::arrive(v_full[0]);
+            tp::arrive(v_full[1]);
+          }
+        }
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ================= MMA issuer =================
+    constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, false);
+    constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, 256, true);
+    const uint64_t d_k = tc::smem_desc_sw128(0, 16, 1024);     // K-major: Q, K, P
+    const uint64_t d_v = tc::smem_desc_sw128(0, kSubV, 1024);  // MN-major: 64-column halves
+    const uint32_t q_lo = smem_u32(sQ) >> 4, k_lo = smem_u32(sK) >> 4;
+    const uint32_t v_lo = smem_u32(sV) >> 4, p_lo = smem_u32(sP) >> 4;
+    uint32_t t = 0;  // tiles over the run
+    int ns = 0;      // segments
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      const int nt = g.k1 - g.k0;
+      ok = __all_sync(0xffffffffu, tp::wait(&bars->q_full, ns & 1, status, abort_flag));
+      for (int j = 0; j <= nt && ok; ++j) {
+        if (j < nt) {
+          // scores of tile t + j
+          const uint32_t tt = t + j;
+          for (int grp = 0; grp < 3; ++grp) {
+            ok = __all_sync(0xffffffffu,
+                            tp::wait(&bars->k_full[grp], tt & 1, status, abort_flag));
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 12; ++kk) {
+                const uint32_t off = (3 * grp + (kk >> 2)) * (kSubQ >> 4) + (kk & 3) * 2;
+                tp::mma_ss(tbase + (tt & 1) * 64, d_k | (uint64_t)(q_lo + off),
+                           d_k | (uint64_t)(k_lo + off), kIdS, (grp | kk) != 0 ? 1u : 0u);
+              }
+              tp::commit_both(&bars->k_empty[grp]);
+              if (grp == 2) {
+                tp::commit_both(&bars->s_full[tt & 1]);
+                if (j == nt - 1) tp::commit_both(&bars->q_empty);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+        if (j > 0) {
+          // mix of tile t + j - 1
+          const uint32_t tt = t + j - 1;
+          ok = tp::wait(&bars->p_ready, tt & 1, status, abort_flag);
+          if (ok && j == 1 && ns > 0)  // the segment before has read its mix out
+            ok = tp::wait(&bars->o_free, (ns - 1) & 1, status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          for (int n = 0; n < 2 && ok; ++n) {
+            ok = __all_sync(0xffffffffu, tp::wait(&bars->v_full[n], tt & 1, status, abort_flag));
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tp::mma_ss(tbase + kColO + 128 * n,
+                           d_k | (uint64_t)(p_lo + (kk >> 2) * (kSubQ >> 4) + (kk & 3) * 2),
+                           d_v | (uint64_t)(v_lo + 2 * n * (kSubV >> 4) + kk * (2048 >> 4)), kIdO,
+                           (j > 1 || kk > 0) ? 1u : 0u);
+              tp::commit_both(n ? &bars->mix_done : &bars->v_empty);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      t += nt;
+      ++ns;
+    }
+  } else if (warp >= 4) {
+    // ================= softmax =================
+    const int q4 = warp & 3;
+    const int half = q4 >> 1;                 // keys 64 half .. of a tile
+    const int r = (q4 & 1) * 32 + lane;       // row of this CTA's 64
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    float* red = reinterpret_cast<float*>(smem + kOffRed);  // [parity][half][64]
+    const uint32_t p_ready = tp::even_addr(&bars->p_ready);
+    const uint32_t o_free = tp::even_addr(&bars->o_free);
+    const float sl2 = a.scale_log2;
+    uint32_t t = 0;
+    bool ok = true, gone = false;  // a wait of this thread's gave up; all four warps leave
+    while (walk.next(a, g)) {
+      const int row = g.m * kRows + 64 * rank + r;  // row of the sequence
+      const bool real = row < g.s.n * a.H;
+      const int i = row / a.H;                      // new token
+      const bool masked = a.draft_mask != nullptr;
+      const uint64_t mask = masked && real ? (uint64_t)a.draft_mask[g.s.q0 + i] : 0ull;
+      float m = -INFINITY, l = 0.f;
+      for (int k = g.k0; k < g.k1; ++k, ++t) {
+        ok = ok && tp::wait(&bars->s_full[t & 1], (t >> 1) & 1, status, abort_flag);
+        __syncwarp();
+        tc::fence_after_sync();
+        uint32_t x[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tc::tmem_ld32(tbase + lane_off + (t & 1) * 64 + c * 32, x[c]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) pin<32>(x[c]);
+        const int key = k * kTile + 64 * half;
+        if ((k + 1) * kTile > g.s.ctx) {  // the tile holds new tokens or ends behind the last
+          const uint64_t seen = seen_bits(key, g.s.ctx, g.s.kv, masked, mask, i);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t w = (uint32_t)(seen >> (32 * c));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((w >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(x[c][e]),
+                                     __uint_as_float(x[c][e + 1]));
+        const float own = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+        float* rd = red + (t & 1) * 128;
+        rd[half * 64 + r] = own;
+        gone = !softmax_and(ok);
+        if (gone) break;
+        const float top = fmaxf(own, rd[(half ^ 1) * 64 + r]) * sl2;
+        // Both threads of a row take the same decisions from the same maxima.
+        const bool need = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2_approx(m - top);
+          m = top;
+          l *= alpha;
+        }
+        const float mb = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights are 2^-inf = 0
+        const uint64_t sl2_2 = f2_pack(sl2, sl2), neg_2 = f2_pack(-mb, -mb);
+        uint64_t sum2[2] = {0ull, 0ull};
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            f2_unpack(ffma2(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sl2_2,
+                            neg_2),
+                      p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum2[(e >> 1) & 1] = fadd2(sum2[(e >> 1) & 1], f2_pack(p0, p1));
+            pk[c * 16 + (e >> 1)] = pack_bf16x2(p0, p1);
+          }
+        float sa, sb;
+        f2_unpack(fadd2(sum2[0], sum2[1]), sa, sb);
+        l += sa + sb;
+        // The weights' buffer and O are free once the tile before has been mixed in.
+        if (t > 0) ok = tp::wait(&bars->mix_done, (t - 1) & 1, status, abort_flag);
+        __syncwarp();
+        if (k > g.k0 && __any_sync(0xffffffffu, need)) {
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < 16; ++c) {
+            uint32_t o[16];
+            tc::tmem_ld16(tbase + lane_off + kColO + c * 16, o);
+            tc::tmem_wait_ld();
+            pin<16>(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st16(tbase + lane_off + kColO + c * 16, o);
+          }
+          tc::tmem_wait_st();
+        }
+        // Weights [64 rows x 64 keys] of this half, 128-byte swizzled like a TMA tile.
+        uint8_t* dst = sP + half * kSubQ + r * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        asm volatile("fence.proxy.async;" ::: "memory");
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tp::arrive(p_ready);
+      }
+      if (gone) break;
+      // The segment's mix, once its last tile has been added.
+      ok = ok && tp::wait(&bars->mix_done, (t - 1) & 1, status, abort_flag);
+      __syncwarp();
+      tc::fence_after_sync();
+      float* rl = red + (t & 1) * 128;  // this parity's maxima are behind a barrier
+      rl[half * 64 + r] = l;
+      gone = !softmax_and(ok);
+      if (gone) break;
+      l += rl[(half ^ 1) * 64 + r];
+      const bool whole = g.slot < 0;
+      const float f = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      uint16_t* fin = a.q_lat + ((size_t)g.s.q0 * a.H + row) * kLD;
+      float* part = a.part_acc + (whole ? 0 : ((size_t)g.slot * kRows + 64 * rank + r) * kLD);
+      if (!whole && half == 0)
+        *reinterpret_cast<float2*>(a.part_ml + ((size_t)g.slot * kRows + 64 * rank + r) * 2) =
+            make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[32];
+        tc::tmem_ld32(tbase + lane_off + kColO + c * 32, o);
+        tc::tmem_wait_ld();
+        pin<32>(o);
+        const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+        if (real && whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * f,
+                                 __uint_as_float(o[8 * e + 2 * k + 1]) * f);
+            *reinterpret_cast<uint4*>(fin + col + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (real) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(part + col + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tp::arrive(o_free);
+      softmax_and(true);  // the sums have been read before the next tile's maxima
+    }
+  }
+
+  // A CTA leaves once neither it nor its peer has anything in flight into its shared memory.
+  // In the regular course every copy and MMA has been waited for by now.  After a wait gave
+  // up, copies may still be landing: they take microseconds.
+  __syncwarp();
+  if (*abort_flag) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tp::cluster_sync();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tp::tmem_dealloc(tbase, 512);
+  }
+}
+
+// ---- merge and up-projection ---------------------------------------------------------------
+// One row (token t, head h) of the mix as bf16, the up-projection's operand: taken as it is from
+// a unit finished by one range, or merged from the partials of the ranges that share the unit:
+// sum 2^(m_s - m) acc_s / sum 2^(m_s - m) l_s.  One warp; lane owns columns 4 lane + 128 k.
+__device__ __forceinline__ void tree_merge_row(const TreeArgs& a, int t, int h, int lane,
+                                               uint16_t* dst) {
   int lo = 0, hi = a.B;  // the last sequence that starts at or before t
   while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (a.cu_q[m] <= t) lo = m; else hi = m;
+    const int mid = (lo + hi) >> 1;
+    if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
   }
-  const int b = lo;
-  bool bad = false;
-  const TreeSeq s = tree_seq(a, b, &bad);
-  if (bad && tid == 0) set_status(a.status, MLA_ERR_KVLEN);
-  if (t < s.q0 || t >= s.q0 + s.n) return;
-  if (a.draft_mask && s.n > 64 && tid == 0) set_status(a.status, MLA_ERR_TREE);
-  const int i = t - s.q0;
-  const uint64_t mask = a.draft_mask ? (uint64_t)a.draft_mask[t] : 0;
-  const size_t row = (size_t)t * a.H + h;
-  float q[16], qr[2], acc[16], m = -INFINITY, l = 0.f;
-  for (int k = 0; k < 16; ++k) {
-    q[k] = __uint_as_float((uint32_t)a.q_lat[row * 512 + lane * 16 + k] << 16);
-    acc[k] = 0.f;
-  }
-  for (int k = 0; k < 2; ++k)
-    qr[k] = __uint_as_float((uint32_t)a.q_pe[row * 64 + lane * 2 + k] << 16);
-  for (int j = warp; j < s.kv; j += kWarps) {
-    if (j >= s.ctx) {
-      const int k = j - s.ctx;
-      if (a.draft_mask ? (k > 63 || !((mask >> k) & 1)) : k > i) continue;
+  const TreeSeq s = tree_seq(a, lo);
+  const int K = seq_tiles(s);
+  const int row = max(t - s.q0, 0) * a.H + h, r = row % kRows;
+  const int64_t W = a.tile0[a.B], V = a.ranges[0];
+  const int64_t x0 = a.tile0[lo] + (int64_t)(row / kRows) * K;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  // Without keys, or in no sequence (a bad length or offset), the row is zero.
+  if (K > 0 && t >= s.q0 && t < s.q0 + s.n) {
+    const int64_t v0 = ((x0 + 1) * V - 1) / W, v1 = ((x0 + K) * V - 1) / W;
+    if (v0 == v1) {
+      const uint2* src = reinterpret_cast<const uint2*>(a.q_lat + ((size_t)t * a.H + h) * kLD);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) = src[lane + 32 * k];
+      return;
     }
-    const int page = a.block_table[(size_t)b * a.max_pages + (j >> a.page_shift)];
-    const bool in = page >= 0 && page < a.num_pages;
-    if (!in && lane == 0) set_status(a.status, MLA_ERR_PAGE);
-    const size_t slot = ((size_t)(in ? page : 0) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
-    float c[16], dot = 0.f;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(a.c_pages + slot * 512 + lane * 16);
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t w = in ? src[k] : 0u;
-      c[2 * k] = bf16lo_to_f32(w);
-      c[2 * k + 1] = bf16hi_to_f32(w);
-      dot += q[2 * k] * c[2 * k] + q[2 * k + 1] * c[2 * k + 1];
+    float m = -INFINITY;
+    for (int64_t v = v0; v <= v1; ++v) {
+      const int64_t slot = v > v0 || range_start(v, W, V) == x0 ? 2 * v : 2 * v + 1;
+      const float2 ml = reinterpret_cast<const float2*>(a.part_ml)[slot * kRows + r];
+      const float4* src = reinterpret_cast<const float4*>(a.part_acc + (slot * kRows + r) * kLD) + lane;
+      const float m2 = fmaxf(m, ml.x);
+      const float base = m2 == -INFINITY ? 0.f : m2;
+      const float f0 = ex2_approx(m - base), f1 = ex2_approx(ml.x - base);
+      m = m2;
+      l = l * f0 + ml.y * f1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 w = src[32 * k];
+        acc[k].x = acc[k].x * f0 + w.x * f1;
+        acc[k].y = acc[k].y * f0 + w.y * f1;
+        acc[k].z = acc[k].z * f0 + w.z * f1;
+        acc[k].w = acc[k].w * f0 + w.w * f1;
+      }
     }
-    const uint32_t pe = in ? reinterpret_cast<const uint32_t*>(a.pe_pages + slot * 64)[lane] : 0u;
-    dot += qr[0] * bf16lo_to_f32(pe) + qr[1] * bf16hi_to_f32(pe);
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    const float x = dot * a.scale_log2;
-    const float m2 = fmaxf(m, x);
-    const float f = ex2_approx(m - m2), p = ex2_approx(x - m2);
-    l = l * f + p;
-    for (int k = 0; k < 16; ++k) acc[k] = acc[k] * f + p * c[k];
-    m = m2;
   }
-  for (int k = 0; k < 16; ++k) s_acc[warp][lane * 16 + k] = acc[k];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) =
+        make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
+                   pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+}
+
+// out[t,h] = W_V[h] mix[t,h] for one head and 32 tokens; the weight is on its way before the
+// split kernel is waited for.  Rows from cu_q[B] on are not written.
+__global__ void __launch_bounds__(512) tree_up_kernel(const TreeArgs a) {
+  extern __shared__ __align__(16) uint8_t up_smem[];
+  uint16_t* sw = reinterpret_cast<uint16_t*>(up_smem);
+  uint16_t* so = sw + 128 * kUpRow;
+  const int h = blockIdx.x;
+  const int t0 = blockIdx.y * kCuB;
+  up_load_weight(sw, a.w_kvb, h);
+  grid_dep_wait();
+  const int nb = min(kCuB, min(max(a.cu_q[a.B], 0), a.T) - t0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = warp; i < kCuB; i += 16) {
+    uint16_t* row = so + i * kUpRow;
+    if (i < nb) {
+      tree_merge_row(a, t0 + i, h, lane, row);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint2*>(row + 4 * lane + 128 * k) = make_uint2(0u, 0u);
+    }
   }
+  cp_async_wait_all();
   __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  const float base = top == -INFINITY ? 0.f : top;
-  for (int w = 0; w < kWarps; ++w) total += s_l[w] * ex2_approx(s_m[w] - base);
-  const float inv = total > 0.f ? 1.f / total : 0.f;
-  float mix[2];
-  for (int k = 0; k < 2; ++k) {
-    mix[k] = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      mix[k] += s_acc[w][tid + 256 * k] * ex2_approx(s_m[w] - base);
+  up_project(so, sw, a.out + ((size_t)t0 * a.H + h) * 128, (size_t)a.H * 128, nb);
+}
+
+// Tensor maps, cached by pointers and sizes (encoding costs microseconds of host time).
+struct MapKey {
+  const void* ptr[4];
+  int T, H, num_pages, page_shift;
+  bool operator==(const MapKey& o) const {
+    for (int i = 0; i < 4; ++i)
+      if (ptr[i] != o.ptr[i]) return false;
+    return T == o.T && H == o.H && num_pages == o.num_pages && page_shift == o.page_shift;
   }
-  __syncthreads();
-  for (int k = 0; k < 2; ++k) s_acc[0][tid + 256 * k] = mix[k] * inv;
-  __syncthreads();
-  if (tid < 128) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(a.w_kvb + ((size_t)h * 256 + 128 + tid) * 512);
-    float y = 0.f;
-    for (int k = 0; k < 256; ++k)
-      y += bf16lo_to_f32(w[k]) * s_acc[0][2 * k] + bf16hi_to_f32(w[k]) * s_acc[0][2 * k + 1];
-    a.out[row * 128 + tid] = (uint16_t)(pack_bf16x2(y, 0.f) & 0xffffu);
+};
+struct MapEntry {
+  MapKey key;
+  CUtensorMap maps[4];
+  bool valid;
+};
+std::mutex g_mu;
+MapEntry g_maps[16];
+int g_next = 0;
+
+bool tree_maps(const TreeArgs& a, TreeParams* p) {
+  const MapKey key = {{a.q_lat, a.q_pe, a.c_pages, a.pe_pages}, a.T, a.H, a.num_pages, a.page_shift};
+  std::lock_guard<std::mutex> lk(g_mu);
+  for (const MapEntry& e : g_maps) {
+    if (e.valid && e.key == key) {
+      p->tm_q = e.maps[0];
+      p->tm_qr = e.maps[1];
+      p->tm_c = e.maps[2];
+      p->tm_kr = e.maps[3];
+      return true;
+    }
   }
+  const uint64_t rows = (uint64_t)a.T * a.H, slots = (uint64_t)a.num_pages << a.page_shift;
+  const uint32_t box = std::min(1 << a.page_shift, 64);
+  if (!encode_bf16_3d(&p->tm_q, a.q_lat, kLD, rows, 1, rows, 64) ||
+      !encode_bf16_3d(&p->tm_qr, a.q_pe, 64, rows, 1, rows, 64) ||
+      !encode_bf16_3d(&p->tm_c, a.c_pages, kLD, slots, 1, slots, box) ||
+      !encode_bf16_3d(&p->tm_kr, a.pe_pages, 64, slots, 1, slots, box))
+    return false;
+  MapEntry& e = g_maps[g_next];
+  g_next = (g_next + 1) % 16;
+  e.key = key;
+  e.maps[0] = p->tm_q;
+  e.maps[1] = p->tm_qr;
+  e.maps[2] = p->tm_c;
+  e.maps[3] = p->tm_kr;
+  e.valid = true;
+  return true;
 }
 
 }  // namespace
 
 cudaError_t launch_latent_tree(const TreeArgs& a, cudaStream_t stream) {
-  LatentArgs l{};
-  l.q_nope = a.q_nope;
-  l.w_kvb = a.w_kvb;
-  l.q_lat = a.q_lat;
-  l.B = a.T;
-  l.H = a.H;
-  const cudaError_t e = launch_latent_absorb(l, stream);
+  TreeParams p;
+  if (!tree_maps(a, &p)) return cudaErrorInvalidValue;
+  p.a = a;
+  static std::atomic<uint64_t> attr_done{0};  // bit per device: smem attributes set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  latent_tree_kernel<<<dim3((unsigned)a.T, (unsigned)a.H), kWarps * 32, 0, stream>>>(a);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(tree_absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kAbsorbSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(tree_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(tree_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCuSmem);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_release);
+  }
+  tree_absorb_kernel<<<dim3(a.H, kLD / kAbN, (unsigned)((a.T + kPB - 1) / kPB)), 256, kAbsorbSmem,
+                       stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2 * a.pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  e = cudaLaunchKernelEx(&cfg, tree_split_kernel, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.H, (unsigned)((a.T + kCuB - 1) / kCuB));
+  cfg.blockDim = dim3(512);
+  cfg.dynamicSmemBytes = kCuSmem;
+  e = cudaLaunchKernelEx(&cfg, tree_up_kernel, a);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

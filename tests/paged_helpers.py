@@ -92,14 +92,15 @@ def tree_case(seed, B, H, ctx, new, page, tree, pad=0, dev="cuda"):
 
 
 def tree_reference(d, scale):
-    """(out, spread) in 64 bits from the definition: each head's keys and values spelled out
-    from the latent rows.  spread = sum_j p_j |v_j|, the scale of rounding errors."""
+    """(out, spread, mixed) in 64 bits from the definition: each head's keys and values spelled
+    out from the latent rows.  The scales of rounding errors: spread = sum_j p_j |v_j|, and for
+    the latent mix, sum_l |W_V[l]| |mix_l|."""
     T, H = d["q_nope"].shape[:2]
     page = d["c_pages"].shape[1]
     cu, kv = d["cu_q"].tolist(), d["kv_len"].tolist()
     w = d["w_kvb"].double().view(H, 256, 512)
     out = torch.full((T, H, 128), float("nan"), dtype=torch.float64, device=w.device)
-    spread = out.clone()
+    spread, mixed = out.clone(), out.clone()
     for b, k in enumerate(kv):
         lo, hi = cu[b], cu[b + 1]
         if lo == hi:
@@ -124,4 +125,6 @@ def tree_reference(d, scale):
         p = e / torch.where(total > 0, total, 1.0)
         out[lo:hi] = torch.einsum("hij,hjd->ihd", p, vals)
         spread[lo:hi] = torch.einsum("hij,hjd->ihd", p, vals.abs())
-    return out, spread
+        mix = torch.einsum("hij,jl->ihl", p, c).abs()
+        mixed[lo:hi] = torch.einsum("ihl,hdl->ihd", mix, w[:, 128:].abs())
+    return out, spread, mixed

@@ -5,9 +5,12 @@ Tolerances.  The kernels round to bf16 four times on the way: the query folded i
 space, the softmax weights, the latent mix, the output.  Each rounding is off by at most half a
 step, 2^-8 of the value, at most 2^-8 / sqrt(3) in the root of the mean square, and they are
 independent: in the 2-norm the result is within 2 * 2^-8 / sqrt(3) = 0.0045 of the reference.
-For one element the scale is spread = sum_j p_j |v_j|: weights and mix err by at most 2^-8 of
-it each, the output by 2^-8 of less, and the folded query moves every score by about 2^-8 of
-itself (scores here are ~N(0, 1): up to five), which is 5 * 2^-8 of the spread: 8 * 2^-8."""
+For one element: the weights err by at most 2^-8 of spread = sum_j p_j |v_j|, the output by 2^-8
+of less, and the folded query moves every score by about 2^-8 of itself (scores here are
+~N(0, 1): up to five), which is 5 * 2^-8 of the spread: 7 * 2^-8.  The mix is rounded in each of
+its 512 latent columns, before the up-projection: column l by at most 2^-8 |mix_l|, so the output
+by at most 2^-8 sum_l |W_V[l]| |mix_l|, which does not shrink where the sum over l cancels (a row
+that sees two keys whose values nearly cancel in one of the 128 columns)."""
 import pytest
 import torch
 
@@ -32,15 +35,16 @@ def _run(d, **kw):
 
 def _close(got, d):
     used = int(d["cu_q"][-1])
-    ref, spread = tree_reference(d, SCALE)
+    ref, spread, mixed = tree_reference(d, SCALE)
     err = (got.double() - ref).abs()[:used]
     if used == 0:
         return
+    most = 2 ** -8 * (7 * spread + mixed)[:used] + 1e-30
     assert bool(torch.isfinite(got[:used]).all())
     rel = float(err.norm() / ref[:used].norm().clamp(min=1e-30))
-    worst = float((err / (spread[:used] + 1e-30)).max()) if float(spread[:used].max()) else 0.0
-    print(f"[tree] rel {rel:.2e} worst {worst * 256:.2f} * 2^-8")
-    assert rel <= 0.0045 and bool((err <= 8 * 2 ** -8 * spread[:used] + 1e-30).all())
+    print(f"[tree] rel {rel:.2e} of the bound {float((err / most).max()):.2f}")
+    assert rel <= 0.0045
+    assert not bool((err > most).any())
 
 
 CASES = [
@@ -109,7 +113,7 @@ def test_large_scores():
     d = tree_case(8, 3, 64, (300, 900), (1, 20), 32, True)
     d["q_nope"] *= 24
     got = _run(d)
-    ref, spread = tree_reference(d, SCALE)
+    ref, spread, _ = tree_reference(d, SCALE)
     # scores ~N(0, 20^2): the folded query's rounding moves them by up to 100 * 2^-8, so single
     # weights are off by a factor; what has to hold is that rows stay finite mixes of the values
     assert bool(torch.isfinite(got).all())
@@ -219,10 +223,8 @@ def test_tree_agrees_with_the_dense_latent_decode():
         slot = d["block_table"][b].long()[j // page] * page + j % page
         c[b, :k], pe[b, :k] = d["c_pages"].view(-1, 512)[slot], d["pe_pages"].view(-1, 64)[slot]
     dense = mla.mla_latent_decode_fwd(d["q_nope"], d["q_pe"], c, pe, d["w_kvb"], d["kv_len"], SCALE)
-    ref, spread = tree_reference(d, SCALE)
-    got = _run(d)
-    for x in (dense, got):
-        assert bool(((x.double() - ref).abs() <= 8 * 2 ** -8 * spread).all())
+    _close(_run(d), d)
+    _close(dense, d)
 
 
 def test_a_pool_past_four_gigabytes():
