@@ -200,16 +200,15 @@ __device__ __forceinline__ uint32_t even_addr(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
   return r;
 }
-// Arrivals on the even CTA's barrier (a cluster address), releasing this thread's writes to
-// the cluster.
+// Arrivals on the even CTA's barrier (a cluster address).  What they announce is data in this
+// CTA's own shared or tensor memory, read there by the tensor core (the writer has run
+// fence.proxy.async, or the tcgen05 fence), so release at CTA scope is enough; at cluster scope
+// an arrival waits for all the thread's outstanding accesses and took about 2000 cycles.
 __device__ __forceinline__ void arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
-                   bar),
-               "r"(bytes)
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
 // Tiled copy into this CTA's shared memory that completes on the even CTA's barrier.
@@ -232,34 +231,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile(
       "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
           : "memory");
-}
-
-// mbar_wait that also acquires what the other CTA released by arriving.
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status,
-                                     volatile int* abort) {
-  const uint32_t a = smem_u32(bar);
-  if (try_wait(a, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    if (try_wait(a, parity)) return true;
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      set_status(status, MLA_ERR_TIMEOUT);
-      *abort = 1;
-      return false;
-    }
-  }
 }
 
 }  // namespace pair

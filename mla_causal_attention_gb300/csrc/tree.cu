@@ -24,7 +24,8 @@
 // Per tile of 128 keys:  S = Q K^T   M128 N128 K576: CTA r stages keys 64 r .. 64 r + 63
 //                        O += P C    M128 N256 K128, twice: CTA r stages latent columns
 //                                    256 n + 128 r .. + 127 of all 128 keys
-// Warps: 0 keys' and queries' TMA, 1 MMA issue (even CTA), 2 latent columns' TMA, 4-7 softmax.
+// Warps: 0 keys' and queries' TMA, 2 latent columns' TMA, 1 and 3 (even CTA) the MMAs of scores
+// and mixes, 4-7 softmax.
 // TMEM: S tiles at columns 0 and 64, O blocks n at 128 and 256.  Softmax thread (row r, half g)
 // = lane 64 g + r holds the scores of keys 64 g .. 64 g + 63 of its row, and the mix columns
 // 256 n + 128 g + c.
@@ -78,6 +79,7 @@ struct TBars {
   uint64_t v_empty;     // block 0's columns read (block 1's: mix_done)
   uint64_t v_tail;      // this CTA's columns of a tile that ends inside, before the zeroing
   uint64_t s_full[2];   // scores of a tile in TMEM
+  uint64_t s_free[2];   // even: the scores have been read (8 warps)
   uint64_t p_ready;     // even: weights of a tile written (8 warps)
   uint64_t mix_done;    // the tile's mix added: weights and columns read, O up to date
   uint64_t o_free;      // even: O of the segment read out (8 warps)
@@ -218,10 +220,8 @@ struct SegWalk {
   }
 };
 
-// Page rows of a tile: lane l gets the pool row at which box l of `box` keys from key j on
-// starts, or the pool's end (read as zeros) where the table holds no page.
-__device__ __forceinline__ int box_row(const TreeArgs& a, int b, int kv, int j, int lane, int box) {
-  const int key = j + lane * box;
+// The pool row that holds a key, or the pool's end (read as zeros) where the table holds no page.
+__device__ __forceinline__ int key_row(const TreeArgs& a, int b, int kv, int key) {
   if (key >= kv) return 0;  // not loaded
   const int page = a.block_table[(int64_t)b * a.max_pages + (key >> a.page_shift)];
   if (page < 0 || page >= a.num_pages) {
@@ -229,6 +229,11 @@ __device__ __forceinline__ int box_row(const TreeArgs& a, int b, int kv, int j, 
     return a.num_pages << a.page_shift;
   }
   return (page << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+}
+
+// Boxes of `box` keys that hold one of the first min(left, 64) keys.
+__device__ __forceinline__ int boxes_of(int left, int box) {
+  return (min(max(left, 0), 64) + box - 1) / box;
 }
 
 // Which of the 64 keys from `key` on a row sees: the bits of the new tokens' mask (or, without
@@ -301,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->v_full[i], 2);
       mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_free[i], 8);
     }
     mbar_init(&bars->v_empty, 1);
     mbar_init(&bars->v_tail, 1);
@@ -327,90 +333,100 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (warp == 0) {
     // ================= keys and queries =================
-    if (lane == 0) {
-      prefetch_tmap(&p.tm_q);
-      prefetch_tmap(&p.tm_qr);
-      prefetch_tmap(&p.tm_c);
-      prefetch_tmap(&p.tm_kr);
-    }
     const uint32_t q_full = tp::even_addr(&bars->q_full);
-    uint32_t k_full[3];
-    for (int i = 0; i < 3; ++i) k_full[i] = tp::even_addr(&bars->k_full[i]);
+    const uint32_t k_full = tp::even_addr(&bars->k_full[0]);
     uint32_t t = 0;  // tiles over the run
     int ns = 0;      // segments
     bool ok = true;
     while (ok && walk.next(a, g)) {
-      if (ns > 0) ok = tp::wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
+      const auto look = [&](int tile) {  // lane q: the row of box q of this CTA's half
+        return lane < boxes
+                   ? key_row(a, g.b, g.s.kv, tile * kTile + 64 * rank + lane * box) : 0;
+      };
+      int rows_next = look(g.k0);
+      if (ns > 0) ok = mbar_wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane == 0) {
-        const int row = g.s.q0 * a.H + g.m * kRows + 64 * rank;
+      const int q_row = g.s.q0 * a.H + g.m * kRows + 64 * rank;
+      if (tc::elect_one()) {
         tp::arrive_expect_tx(q_full, 9 * kSubQ);
-        for (int s = 0; s < 8; ++s) tp::tma_load_3d(sQ + s * kSubQ, &p.tm_q, q_full, 64 * s, row, 0);
-        tp::tma_load_3d(sQ + 8 * kSubQ, &p.tm_qr, q_full, 0, row, 0);
+#pragma unroll 1
+        for (int s = 0; s < 8; ++s)
+          tp::tma_load_3d(sQ + s * kSubQ, &p.tm_q, q_full, 64 * s, q_row, 0);
+        tp::tma_load_3d(sQ + 8 * kSubQ, &p.tm_qr, q_full, 0, q_row, 0);
       }
+      __syncwarp();
       ++ns;
-      int rows_next = box_row(a, g.b, g.s.kv, g.k0 * kTile + 64 * rank, lane & 7, box);
-      for (int k = g.k0; k < g.k1; ++k, ++t) {
+      for (int k = g.k0; k < g.k1 && ok; ++k, ++t) {
         const int rows = rows_next;
-        const int j = k * kTile + 64 * rank;
-        if (k + 1 < g.k1) rows_next = box_row(a, g.b, g.s.kv, j + kTile, lane & 7, box);
-        const int left = min(max(g.s.kv - j, 0), 64);
-        const int nb = (left + box - 1) / box;  // boxes that hold a key
+        if (k + 1 < g.k1) rows_next = look(k + 1);
+        const int nb = boxes_of(g.s.kv - k * kTile - 64 * rank, box);
+        int row[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) row[q] = __shfl_sync(0xffffffffu, rows, q);
+#pragma unroll 1
         for (int grp = 0; grp < 3; ++grp) {
-          if (t > 0) ok = tp::wait(&bars->k_empty[grp], (t - 1) & 1, status, abort_flag);
+          if (t > 0) ok = mbar_wait(&bars->k_empty[grp], (t - 1) & 1, status, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) tp::arrive_expect_tx(k_full[grp], 3 * nb * box * 128);
-          for (int q = 0; q < nb; ++q) {
-            const int row = __shfl_sync(0xffffffffu, rows, q);
-            if (lane == 0) {
-              uint8_t* dst = sK + 3 * grp * kSubQ + q * box * 128;
-              for (int s = 0; s < 3; ++s) {
-                const int sub = 3 * grp + s;
-                if (sub < 8)
-                  tp::tma_load_3d(dst + s * kSubQ, &p.tm_c, k_full[grp], 64 * sub, row, 0);
-                else
-                  tp::tma_load_3d(dst + s * kSubQ, &p.tm_kr, k_full[grp], 0, row, 0);
+          if (tc::elect_one()) {
+            const uint32_t bar = k_full + 8 * grp;
+            uint8_t* dst = sK + 3 * grp * kSubQ;
+            const CUtensorMap* last = grp < 2 ? &p.tm_c : &p.tm_kr;
+            const int col = 192 * grp;
+            tp::arrive_expect_tx(bar, 3 * nb * box * 128);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (q < nb) {
+                uint8_t* to = dst + q * box * 128;
+                tp::tma_load_3d(to, &p.tm_c, bar, col, row[q], 0);
+                tp::tma_load_3d(to + kSubQ, &p.tm_c, bar, col + 64, row[q], 0);
+                tp::tma_load_3d(to + 2 * kSubQ, last, bar, grp < 2 ? col + 128 : 0, row[q], 0);
               }
-            }
           }
           __syncwarp();
         }
-        if (!ok) break;
       }
     }
   } else if (warp == 2) {
     // ================= latent columns of the mix =================
-    uint32_t v_full[2];
-    for (int i = 0; i < 2; ++i) v_full[i] = tp::even_addr(&bars->v_full[i]);
+    const uint32_t v_full = tp::even_addr(&bars->v_full[0]);
     const uint32_t v_tail = smem_u32(&bars->v_tail);
     uint32_t t = 0, tails = 0;
     bool ok = true;
     while (ok && walk.next(a, g)) {
-      int rows_next = box_row(a, g.b, g.s.kv, g.k0 * kTile, lane & 15, box);
+      const auto look = [&](int tile) {  // lane q: the row of box q of the tile
+        return lane < 2 * boxes ? key_row(a, g.b, g.s.kv, tile * kTile + lane * box) : 0;
+      };
+      int rows_next = look(g.k0);
       for (int k = g.k0; k < g.k1; ++k, ++t) {
         const int rows = rows_next;
-        const int j = k * kTile;
-        if (k + 1 < g.k1) rows_next = box_row(a, g.b, g.s.kv, j + kTile, lane & 15, box);
-        const int left = min(g.s.kv - j, kTile);  // > 0
-        const int nb = (left + box - 1) / box;
+        if (k + 1 < g.k1) rows_next = look(k + 1);
+        const int left = min(g.s.kv - k * kTile, kTile);  // > 0
         const bool tail = left < kTile;
-        if (tail && lane == 0) mbar_arrive_expect_tx(&bars->v_tail, 4 * nb * box * 128);
+        if (tail && lane == 0)
+          mbar_arrive_expect_tx(&bars->v_tail, 4 * ((left + box - 1) / box) * box * 128);
+        int row[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) row[q] = __shfl_sync(0xffffffffu, rows, q);
+        const int nb = (left + box - 1) / box;
+#pragma unroll 1
         for (int n = 0; n < 2; ++n) {
           if (t > 0)
-            ok = tp::wait(n ? &bars->mix_done : &bars->v_empty, (t - 1) & 1, status, abort_flag);
+            ok = mbar_wait(n ? &bars->mix_done : &bars->v_empty, (t - 1) & 1, status, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (!tail && lane == 0) tp::arrive_expect_tx(v_full[n], 2 * kSubV);
-          for (int q = 0; q < nb; ++q) {
-            const int row = __shfl_sync(0xffffffffu, rows, q);
-            if (lane == 0) {
-              uint8_t* dst = sV + 2 * n * kSubV + q * box * 128;
-              for (int s = 0; s < 2; ++s)
-                tp::tma_load_3d(dst + s * kSubV, &p.tm_c, tail ? v_tail : v_full[n],
-                                256 * n + 128 * rank + 64 * s, row, 0);
-            }
+          if (tc::elect_one()) {
+            const uint32_t bar = tail ? v_tail : v_full + 8 * n;
+            uint8_t* dst = sV + 2 * n * kSubV;
+            const int col = 256 * n + 128 * rank;
+            if (!tail) tp::arrive_expect_tx(bar, 2 * kSubV);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q < nb) {
+                tp::tma_load_3d(dst + q * box * 128, &p.tm_c, bar, col, row[q], 0);
+                tp::tma_load_3d(dst + kSubV + q * box * 128, &p.tm_c, bar, col + 64, row[q], 0);
+              }
           }
           __syncwarp();
         }
@@ -425,80 +441,90 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
               *reinterpret_cast<uint4*>(sV + s * kSubV + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          asm volatile("fence.proxy.async;" ::: "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            tp::arrive(v_full[0]);
-            tp::arrive(v_full[1]);
+            tp::arrive(v_full);
+            tp::arrive(v_full + 8);
           }
         }
       }
     }
   } else if (warp == 1 && rank == 0) {
-    // ================= MMA issuer =================
+    // ================= score MMAs =================
+    // Scores and mixes are issued by two warps: waiting for a barrier takes about 170 cycles and
+    // issuing an MMA 24, so one warp for both was the slowest part (3600 cycles per tile; the
+    // MMAs themselves take 36 x 33.8 + 16 x 64.2 = 2244).
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, false);
-    constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, 256, true);
-    const uint64_t d_k = tc::smem_desc_sw128(0, 16, 1024);     // K-major: Q, K, P
-    const uint64_t d_v = tc::smem_desc_sw128(0, kSubV, 1024);  // MN-major: 64-column halves
+    const uint64_t d_k = tc::smem_desc_sw128(0, 16, 1024);  // K-major
     const uint32_t q_lo = smem_u32(sQ) >> 4, k_lo = smem_u32(sK) >> 4;
-    const uint32_t v_lo = smem_u32(sV) >> 4, p_lo = smem_u32(sP) >> 4;
     uint32_t t = 0;  // tiles over the run
     int ns = 0;      // segments
     bool ok = true;
     while (ok && walk.next(a, g)) {
-      const int nt = g.k1 - g.k0;
-      ok = __all_sync(0xffffffffu, tp::wait(&bars->q_full, ns & 1, status, abort_flag));
-      for (int j = 0; j <= nt && ok; ++j) {
-        if (j < nt) {
-          // scores of tile t + j
-          const uint32_t tt = t + j;
-          for (int grp = 0; grp < 3; ++grp) {
-            ok = __all_sync(0xffffffffu,
-                            tp::wait(&bars->k_full[grp], tt & 1, status, abort_flag));
-            if (!ok) break;
-            tc::fence_after_sync();
-            if (tc::elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < 12; ++kk) {
-                const uint32_t off = (3 * grp + (kk >> 2)) * (kSubQ >> 4) + (kk & 3) * 2;
-                tp::mma_ss(tbase + (tt & 1) * 64, d_k | (uint64_t)(q_lo + off),
-                           d_k | (uint64_t)(k_lo + off), kIdS, (grp | kk) != 0 ? 1u : 0u);
-              }
-              tp::commit_both(&bars->k_empty[grp]);
-              if (grp == 2) {
-                tp::commit_both(&bars->s_full[tt & 1]);
-                if (j == nt - 1) tp::commit_both(&bars->q_empty);
-              }
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-        }
-        if (j > 0) {
-          // mix of tile t + j - 1
-          const uint32_t tt = t + j - 1;
-          ok = tp::wait(&bars->p_ready, tt & 1, status, abort_flag);
-          if (ok && j == 1 && ns > 0)  // the segment before has read its mix out
-            ok = tp::wait(&bars->o_free, (ns - 1) & 1, status, abort_flag);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, ns & 1, status, abort_flag));
+      for (int k = g.k0; k < g.k1 && ok; ++k, ++t) {
+        // The score tile to be overwritten, that of tile t - 2, has been read.
+        if (t > 1) ok = mbar_wait(&bars->s_free[t & 1], ((t >> 1) - 1) & 1, status, abort_flag);
+        const uint32_t d = tbase + (t & 1) * 64;
+        const bool last = k + 1 == g.k1;
+#pragma unroll 1
+        for (int grp = 0; grp < 3; ++grp) {
+          ok = ok && mbar_wait(&bars->k_full[grp], t & 1, status, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
-          for (int n = 0; n < 2 && ok; ++n) {
-            ok = __all_sync(0xffffffffu, tp::wait(&bars->v_full[n], tt & 1, status, abort_flag));
-            if (!ok) break;
-            tc::fence_after_sync();
-            if (tc::elect_one()) {
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t at = 3 * grp * (kSubQ >> 4);
+          if (tc::elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tp::mma_ss(tbase + kColO + 128 * n,
-                           d_k | (uint64_t)(p_lo + (kk >> 2) * (kSubQ >> 4) + (kk & 3) * 2),
-                           d_v | (uint64_t)(v_lo + 2 * n * (kSubV >> 4) + kk * (2048 >> 4)), kIdO,
-                           (j > 1 || kk > 0) ? 1u : 0u);
-              tp::commit_both(n ? &bars->mix_done : &bars->v_empty);
+            for (int kk = 0; kk < 12; ++kk) {
+              const uint32_t off = at + (kk >> 2) * (kSubQ >> 4) + (kk & 3) * 2;
+              tp::mma_ss(d, d_k | (uint64_t)(q_lo + off), d_k | (uint64_t)(k_lo + off), kIdS,
+                         (grp | kk) != 0 ? 1u : 0u);
             }
-            __syncwarp();
+            tp::commit_both(&bars->k_empty[grp]);
+            if (grp == 2) {
+              tp::commit_both(&bars->s_full[t & 1]);
+              if (last) tp::commit_both(&bars->q_empty);
+            }
           }
+          __syncwarp();
         }
       }
-      t += nt;
+      ++ns;
+    }
+  } else if (warp == 3 && rank == 0) {
+    // ================= mix MMAs =================
+    constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, 256, true);
+    const uint64_t d_p = tc::smem_desc_sw128(0, 16, 1024);     // K-major
+    const uint64_t d_v = tc::smem_desc_sw128(0, kSubV, 1024);  // MN-major: 64-column halves
+    const uint32_t v_lo = smem_u32(sV) >> 4, p_lo = smem_u32(sP) >> 4;
+    uint32_t t = 0;
+    int ns = 0;
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      for (int k = g.k0; k < g.k1 && ok; ++k, ++t) {
+        ok = mbar_wait(&bars->p_ready, t & 1, status, abort_flag);
+        if (ok && k == g.k0 && ns > 0)  // the segment before has read its mix out
+          ok = mbar_wait(&bars->o_free, (ns - 1) & 1, status, abort_flag);
+#pragma unroll 1
+        for (int n = 0; n < 2; ++n) {
+          ok = ok && mbar_wait(&bars->v_full[n], t & 1, status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t d = tbase + kColO + 128 * n, v_at = v_lo + 2 * n * (kSubV >> 4);
+          const uint32_t acc = k > g.k0 ? 1u : 0u;
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tp::mma_ss(d, d_p | (uint64_t)(p_lo + (kk >> 2) * (kSubQ >> 4) + (kk & 3) * 2),
+                         d_v | (uint64_t)(v_at + kk * (2048 >> 4)), kIdO, kk > 0 ? 1u : acc);
+            tp::commit_both(n ? &bars->mix_done : &bars->v_empty);
+          }
+          __syncwarp();
+        }
+      }
       ++ns;
     }
   } else if (warp >= 4) {
@@ -508,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int r = (q4 & 1) * 32 + lane;       // row of this CTA's 64
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     float* red = reinterpret_cast<float*>(smem + kOffRed);  // [parity][half][64]
+    const uint32_t s_free = tp::even_addr(&bars->s_free[0]);
     const uint32_t p_ready = tp::even_addr(&bars->p_ready);
     const uint32_t o_free = tp::even_addr(&bars->o_free);
     const float sl2 = a.scale_log2;
@@ -521,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint64_t mask = masked && real ? (uint64_t)a.draft_mask[g.s.q0 + i] : 0ull;
       float m = -INFINITY, l = 0.f;
       for (int k = g.k0; k < g.k1; ++k, ++t) {
-        ok = ok && tp::wait(&bars->s_full[t & 1], (t >> 1) & 1, status, abort_flag);
+        ok = ok && mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, status, abort_flag);
         __syncwarp();
         tc::fence_after_sync();
         uint32_t x[2][32];
@@ -530,6 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 2; ++c) pin<32>(x[c]);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tp::arrive(s_free + 8 * (t & 1));
         const int key = k * kTile + 64 * half;
         if ((k + 1) * kTile > g.s.ctx) {  // the tile holds new tokens or ends behind the last
           const uint64_t seen = seen_bits(key, g.s.ctx, g.s.kv, masked, mask, i);
@@ -583,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         f2_unpack(fadd2(sum2[0], sum2[1]), sa, sb);
         l += sa + sb;
         // The weights' buffer and O are free once the tile before has been mixed in.
-        if (t > 0) ok = tp::wait(&bars->mix_done, (t - 1) & 1, status, abort_flag);
+        if (t > 0) ok = mbar_wait(&bars->mix_done, (t - 1) & 1, status, abort_flag);
         __syncwarp();
         if (k > g.k0 && __any_sync(0xffffffffu, need)) {
           tc::fence_after_sync();
@@ -605,14 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int c = 0; c < 8; ++c)
           *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        asm volatile("fence.proxy.async;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tp::arrive(p_ready);
       }
       if (gone) break;
       // The segment's mix, once its last tile has been added.
-      ok = ok && tp::wait(&bars->mix_done, (t - 1) & 1, status, abort_flag);
+      ok = ok && mbar_wait(&bars->mix_done, (t - 1) & 1, status, abort_flag);
       __syncwarp();
       tc::fence_after_sync();
       float* rl = red + (t & 1) * 128;  // this parity's maxima are behind a barrier
@@ -622,11 +652,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       l += rl[(half ^ 1) * 64 + r];
       const bool whole = g.slot < 0;
       const float f = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-      uint16_t* fin = a.q_lat + ((size_t)g.s.q0 * a.H + row) * kLD;
-      float* part = a.part_acc + (whole ? 0 : ((size_t)g.slot * kRows + 64 * rank + r) * kLD);
+      const size_t slot_row = (size_t)(whole ? 0 : g.slot) * kRows + 64 * rank;
       if (!whole && half == 0)
-        *reinterpret_cast<float2*>(a.part_ml + ((size_t)g.slot * kRows + 64 * rank + r) * 2) =
-            make_float2(m, l);
+        *reinterpret_cast<float2*>(a.part_ml + (slot_row + r) * 2) = make_float2(m, l);
+      // 32 columns at a time through this warp's quarter of the weights' buffer (free now), so
+      // that eight lanes write a row's 128 (four lanes its 64) bytes: a lane writing its own row
+      // touches 32 lines per instruction, and took 9000 cycles per segment.
+      uint8_t* stage = sP + q4 * 4096;
+      const int row0 = g.m * kRows + 64 * rank + (q4 & 1) * 32;  // the warp's first row
+      const int have = min(max(g.s.n * a.H - row0, 0), 32);      // rows that exist
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint32_t o[32];
@@ -634,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::tmem_wait_ld();
         pin<32>(o);
         const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
-        if (real && whole) {
+        if (whole) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t w[4];
@@ -642,13 +676,38 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int k = 0; k < 4; ++k)
               w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * f,
                                  __uint_as_float(o[8 * e + 2 * k + 1]) * f);
-            *reinterpret_cast<uint4*>(fin + col + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else if (real) {
+        } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(part + col + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
+        __syncwarp();
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2), e = lane & 3;
+            const uint4 w =
+                *reinterpret_cast<const uint4*>(stage + rr * 64 + ((e ^ ((rr >> 1) & 3)) << 4));
+            if (rr < have)
+              *reinterpret_cast<uint4*>(a.q_lat + ((size_t)g.s.q0 * a.H + row0 + rr) * kLD + col +
+                                        8 * e) = w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3), e = lane & 7;
+            const uint4 w =
+                *reinterpret_cast<const uint4*>(stage + rr * 128 + ((e ^ (rr & 7)) << 4));
+            if (rr < have)
+              *reinterpret_cast<uint4*>(a.part_acc + (slot_row + (q4 & 1) * 32 + rr) * kLD + col +
+                                        4 * e) = w;
+          }
+        }
+        __syncwarp();
       }
       tc::fence_before_sync();
       __syncwarp();
