@@ -131,7 +131,7 @@ def library():
         lib.mla_latent_append.restype = i
         lib.mla_latent_append.argtypes = [p, p, p, i, p, p, i, i, p, p, i, p, i, p, p, sz, p]
         lib.mla_latent_tree_workspace_bytes.restype = sz
-        lib.mla_latent_tree_workspace_bytes.argtypes = [i, i, i, i, i]
+        lib.mla_latent_tree_workspace_bytes.argtypes = [i, i, i]
         lib.mla_latent_tree_fwd.restype = i
         lib.mla_latent_tree_fwd.argtypes = [p, p, p, p, i, i, p, i, p, p, p, p, i, i, i, f, p, p,
                                             sz, p]
@@ -564,7 +564,7 @@ def mla_latent_tree_fwd(q_nope, q_pe, c_pages, pe_pages, block_table, kv_len, cu
         out = torch.empty((T, H, 128), dtype=bf, device=dev)
     else:
         _check(out, "out", bf, (T, H, 128), dev)
-    nbytes = library().mla_latent_tree_workspace_bytes(T, H, B, num_pages, page_size)
+    nbytes = library().mla_latent_tree_workspace_bytes(T, H, B)
     _enqueue("mla_latent_tree_fwd", dev, stream, workspace, nbytes, (
         q_nope.data_ptr(), q_pe.data_ptr(), c_pages.data_ptr(), pe_pages.data_ptr(), num_pages,
         page_size, block_table.data_ptr(), max_pages, kv_len.data_ptr(), cu_q.data_ptr(),

@@ -99,25 +99,22 @@ size_t latent_workspace(int B, int H, int grid) {
 }
 
 // Workspace of the tree attention: the status word; the queries folded into the latent space
-// [T, H, 512] bf16; the partition; and two partial results of 128 rows x (512 + 2) floats for
-// each of the ranges the key tiles are cut into.  One range per CTA pair, or several when the
-// pool is larger than what L2 holds of it at a time (the device decides from the lengths).
+// [T, H, 512] bf16; the partition; and two partial results of 128 rows x (512 + 2) floats per CTA
+// pair.
 struct TreeLayout {
-  size_t q_lat, tile0, ranges, part_ml, part_acc, total;
-  int pairs, max_ranges;
+  size_t q_lat, tile0, unit0, range0, part_ml, part_acc, total;
+  int pairs;
 };
-TreeLayout tree_layout(int T, int H, int B, int num_pages, int page_size, int sms) {
+TreeLayout tree_layout(int T, int H, int B, int sms) {
   TreeLayout l;
-  l.pairs = std::max(1, sms / 2);
-  const int64_t pool = (int64_t)num_pages * page_size * 1152;
-  const int64_t rounds = (pool + kTreeRoundBytes - 1) / kTreeRoundBytes;
-  l.max_ranges = l.pairs * (int)std::min<int64_t>(std::max<int64_t>(rounds, 1), kTreeMaxRounds);
+  l.pairs = std::min(std::max(1, sms / 2), 256);  // the partition has a thread per pair
   l.q_lat = kStatusBytes;
   l.tile0 = l.q_lat + r256((size_t)T * H * 512 * 2);
-  l.ranges = l.tile0 + r256((size_t)(B + 1) * 8);
-  l.part_ml = l.ranges + 256;
-  l.part_acc = l.part_ml + r256((size_t)2 * l.max_ranges * 128 * 2 * 4);
-  l.total = l.part_acc + r256((size_t)2 * l.max_ranges * 128 * 512 * 4);
+  l.unit0 = l.tile0 + r256((size_t)(B + 1) * 8);
+  l.range0 = l.unit0 + r256((size_t)(B + 1) * 8);
+  l.part_ml = l.range0 + r256((size_t)(l.pairs + 2) * 8);
+  l.part_acc = l.part_ml + (size_t)2 * l.pairs * 128 * 2 * 4;
+  l.total = l.part_acc + (size_t)2 * l.pairs * 128 * 512 * 4;
   return l;
 }
 
@@ -679,11 +676,11 @@ mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k_pe_new,
              : MLA_ERR_CUDA;
 }
 
-size_t mla_latent_tree_workspace_bytes(int T, int H, int B, int num_pages, int page_size) {
-  if (T < 1 || H < 1 || H > 1024 || B < 1 || check_pool(num_pages, page_size) != MLA_OK) return 0;
+size_t mla_latent_tree_workspace_bytes(int T, int H, int B) {
+  if (T < 1 || H < 1 || H > 1024 || B < 1) return 0;
   int sms = 0;
   if (check_device(&sms) != MLA_OK || sms <= 0) sms = 152;
-  return tree_layout(T, H, B, num_pages, page_size, sms).total;
+  return tree_layout(T, H, B, sms).total;
 }
 
 mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
@@ -713,7 +710,7 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
   int sms = 0;
   const mla_status st = check_device(&sms);
   if (st != MLA_OK) return st;
-  const TreeLayout lay = tree_layout(T, H, B, num_pages, page_size, sms);
+  const TreeLayout lay = tree_layout(T, H, B, sms);
   if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   TreeArgs a{};
@@ -723,11 +720,12 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
   a.status = reinterpret_cast<int*>(w);
   a.q_lat = reinterpret_cast<uint16_t*>(w + lay.q_lat);
   a.tile0 = reinterpret_cast<int64_t*>(w + lay.tile0);
-  a.ranges = reinterpret_cast<int32_t*>(w + lay.ranges);
+  a.unit0 = reinterpret_cast<int64_t*>(w + lay.unit0);
+  a.range0 = reinterpret_cast<int64_t*>(w + lay.range0);
   a.part_ml = reinterpret_cast<float*>(w + lay.part_ml);
   a.part_acc = reinterpret_cast<float*>(w + lay.part_acc);
   a.num_pages = num_pages; a.page_shift = page_shift(page_size); a.max_pages = max_pages;
-  a.B = B; a.T = T; a.H = H; a.pairs = lay.pairs; a.max_ranges = lay.max_ranges;
+  a.B = B; a.T = T; a.H = H; a.pairs = lay.pairs;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   return launch_latent_tree(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MLA_OK

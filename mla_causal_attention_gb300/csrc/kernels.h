@@ -238,19 +238,21 @@ struct TreeArgs {
   const int64_t* draft_mask;  // may be null
   const uint16_t* w_kvb;
   uint16_t* out;
-  uint16_t* q_lat;   // workspace [T,H,512]: folded queries, then the mixes of whole units
-  int64_t* tile0;    // workspace [B+1]: first tile of each sequence, then all tiles (W)
-  int32_t* ranges;   // workspace [1]: ranges the tiles are cut into
-  float* part_ml;    // workspace [2 max_ranges][128][2]
-  float* part_acc;   // workspace [2 max_ranges][128][512]
+  uint16_t* q_lat;   // workspace [T,H,512]: folded queries, then their rows' mixes
+  // workspace, the partition (see tree.cu): first tile and first unit of each sequence and their
+  // totals [B+1]; first tile of each pair's range, all tiles, waves [pairs+2]
+  int64_t* tile0;
+  int64_t* unit0;
+  int64_t* range0;
+  float* part_ml;    // workspace [2 pairs][128][2]
+  float* part_acc;   // workspace [2 pairs][128][512]
   int* status;
   int num_pages, page_shift, max_pages, B, T, H;
-  int pairs, max_ranges;
+  int pairs;
   float scale_log2;
 };
-// Latent rows that the CTA pairs of one round walk through together (see tree.cu).
-constexpr int64_t kTreeRoundBytes = 64 << 20;
-constexpr int kTreeMaxRounds = 5;
+cudaError_t launch_tree_fold(const TreeArgs& a, cudaStream_t stream);  // q_lat, partition
+cudaError_t launch_tree_up(const TreeArgs& a, cudaStream_t stream);    // merge, out
 cudaError_t launch_latent_tree(const TreeArgs& a, cudaStream_t stream);
 
 // Number of SMs of the current device (cached per device).

@@ -8,9 +8,10 @@
 // matrix, cut into units of 128 rows, against tiles of 128 keys.
 //
 // Kernels, each a programmatic dependent launch of the one before:
-//   tree_absorb_kernel   q_lat, and the partition of the work (block 0)
-//   tree_split_kernel    the attention over the latent rows, flash style
-//   tree_up_kernel       merges partial mixes, then out = W_V mix
+//   tree_proj_kernel<fold>  q_lat, and the partition of the work (tree_proj.cu)
+//   tree_split_kernel       the attention over the latent rows, flash style
+//   tree_merge_kernel       partial mixes of the units that several pairs shared (tree_proj.cu)
+//   tree_proj_kernel<up>    out = W_V mix (tree_proj.cu)
 //
 // What bounds it: per row and key 2 * (576 + 512) operations against 1152 bytes per key, read
 // once for all rows of a sequence: one token per sequence (64 rows) is bound by HBM, from about
@@ -36,17 +37,17 @@
 #include <mutex>
 
 #include "kernels.h"
-#include "latent_proj.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
+#include "tree_part.cuh"
 
 namespace mla {
 namespace {
 
-using namespace proj;
+using namespace tree;
 
-constexpr int kTile = 128;       // keys per tile
-constexpr int kRows = 128;       // query rows per unit, 64 per CTA
+constexpr int kLD = 512;         // latent width (kv_lora_rank)
+
 constexpr int kSubQ = 64 * 128;  // 64 rows x 64 columns, bf16, 128-byte swizzled
 constexpr int kSubV = 128 * 128; // 128 keys x 64 columns
 constexpr int kThreads = 256;
@@ -87,138 +88,6 @@ struct TBars {
   int abort_flag;
 };
 static_assert(sizeof(TBars) <= 256, "barrier block");
-
-// ---- the partition -----------------------------------------------------------------------
-// Sequence b has n_b H rows in M_b units and K_b key tiles.  The tiles of all units, laid end
-// to end in the order (sequence, unit, key), are cut into V ranges of equal length (to within
-// one tile), and pair c takes ranges c, c + pairs, ...: V = pairs, or several times that when
-// units share many keys, so that the pairs walk through the keys of few sequences at a time and
-// find them in L2.  A range's tiles of one unit are a segment; a unit within one range is
-// finished there, the others leave a partial mix each: in slot 2 v if it is the first segment
-// of range v, else (the last) in 2 v + 1.
-struct TreeSeq {
-  int q0, n, kv, ctx;
-  bool bad;
-};
-__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
-  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], k = a.kv_len[b];
-  TreeSeq s;
-  s.q0 = min(max(c0, 0), a.T);
-  s.n = min(max(c1, s.q0), a.T) - s.q0;
-  s.kv = (int)min((int64_t)max(k, 0), (int64_t)a.max_pages << a.page_shift);
-  s.ctx = max(s.kv - s.n, 0);
-  s.bad = s.q0 != c0 || s.q0 + s.n != c1 || s.kv != k || s.kv < s.n;
-  return s;
-}
-__device__ __forceinline__ int seq_units(const TreeArgs& a, const TreeSeq& s) {
-  return (s.n * a.H + kRows - 1) / kRows;
-}
-__device__ __forceinline__ int seq_tiles(const TreeSeq& s) { return (s.kv + kTile - 1) / kTile; }
-__device__ __forceinline__ int64_t range_start(int64_t v, int64_t W, int64_t V) { return v * W / V; }
-
-// Prefix sums of M_b K_b over the sequences, by one block; also the choice of V.
-__device__ void tree_partition(const TreeArgs& a) {
-  __shared__ int64_t s_w[8], s_shared[8];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t total = 0, shared_keys = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 256) {
-    const int b = b0 + tid;
-    int64_t w = 0, again = 0;
-    if (b < a.B) {
-      const TreeSeq s = tree_seq(a, b);
-      if (s.bad) set_status(a.status, MLA_ERR_KVLEN);
-      if (a.draft_mask && s.n > 64) set_status(a.status, MLA_ERR_TREE);
-      const int units = seq_units(a, s);
-      w = (int64_t)units * seq_tiles(s);
-      if (units > 1) again = seq_tiles(s);
-    }
-    int64_t inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) again += __shfl_xor_sync(0xffffffffu, again, o);
-    if (lane == 31) {
-      s_w[warp] = inc;
-      s_shared[warp] = again;
-    }
-    __syncthreads();
-    int64_t before = total;
-    for (int k = 0; k < 8; ++k) {
-      if (k < warp) before += s_w[k];
-      total += s_w[k];
-      shared_keys += s_shared[k];
-    }
-    if (b < a.B) a.tile0[b] = before + inc - w;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    a.tile0[a.B] = total;
-    const int64_t rounds =
-        max((shared_keys * (kTile * 1152) + kTreeRoundBytes - 1) / kTreeRoundBytes, (int64_t)1);
-    a.ranges[0] = (int)min(min(rounds * a.pairs, (int64_t)a.max_ranges), max(total, (int64_t)1));
-  }
-}
-
-__global__ void __launch_bounds__(256) tree_absorb_kernel(const TreeArgs a) {
-  grid_dep_launch();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) tree_partition(a);
-  absorb_block(a.q_nope, a.w_kvb, a.q_lat, a.T, a.H, blockIdx.x, blockIdx.y * kAbN,
-               blockIdx.z * kPB);
-}
-
-// One segment: rows 128 m .. of sequence b's rows, key tiles [k0, k1).
-struct Seg {
-  int b, m, k0, k1;
-  TreeSeq s;
-  int64_t slot;  // partial slot, or -1: the unit is finished here
-};
-// Walks the segments of a pair's ranges.  Warp-uniform; every role has its own.
-struct SegWalk {
-  int64_t W, V, v, x, x1, first_x, base, next_base;
-  int b, step, K;
-  TreeSeq s;
-  __device__ __forceinline__ SegWalk(const TreeArgs& a, int pair) {
-    W = a.tile0[a.B];
-    V = a.ranges[0];
-    v = (int64_t)pair - a.pairs;
-    step = a.pairs;
-    x = x1 = 0;
-  }
-  __device__ __forceinline__ bool next(const TreeArgs& a, Seg& g) {
-    if (x >= x1) {
-      v += step;
-      if (v >= V || W == 0) return false;
-      x = first_x = range_start(v, W, V);
-      x1 = range_start(v + 1, W, V);
-      int lo = 0, hi = a.B;  // the last sequence that starts at or before x
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.tile0[mid] <= x) lo = mid; else hi = mid;
-      }
-      enter(a, lo);
-    }
-    while (x >= next_base) enter(a, b + 1);  // skips sequences without work
-    const int64_t off = x - base;
-    g.b = b;
-    g.m = (int)(off / K);
-    g.k0 = (int)(off - (int64_t)g.m * K);
-    g.k1 = (int)min((int64_t)K, g.k0 + (x1 - x));
-    g.s = s;
-    g.slot = g.k0 == 0 && g.k1 == K ? -1 : x == first_x ? 2 * v : 2 * v + 1;
-    x += g.k1 - g.k0;
-    return true;
-  }
-  __device__ __forceinline__ void enter(const TreeArgs& a, int seq) {
-    b = seq;
-    base = a.tile0[b];
-    next_base = a.tile0[b + 1];
-    s = tree_seq(a, b);
-    K = seq_tiles(s);
-  }
-};
 
 // The pool row that holds a key, or the pool's end (read as zeros) where the table holds no page.
 __device__ __forceinline__ int key_row(const TreeArgs& a, int b, int kv, int key) {
@@ -326,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   tc::fence_after_sync();
   const uint32_t tbase = bars->tmem_base;
   grid_dep_wait();  // the partition and the folded queries
-  SegWalk walk(a, pair_id);
-  Seg g;
+  SegWalk walk(a, pair_id, lane);
+  Seg g, after;
+  bool more = walk.next(a, g);
   const int box = min(1 << a.page_shift, 64);  // keys per TMA box
   const int boxes = 64 / box;                  // boxes per 64 keys
 
@@ -338,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t t = 0;  // tiles over the run
     int ns = 0;      // segments
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    for (; ok && more; g = after) {
       const auto look = [&](int tile) {  // lane q: the row of box q of this CTA's half
         return lane < boxes
                    ? key_row(a, g.b, g.s.kv, tile * kTile + 64 * rank + lane * box) : 0;
@@ -360,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (int k = g.k0; k < g.k1 && ok; ++k, ++t) {
         const int rows = rows_next;
         if (k + 1 < g.k1) rows_next = look(k + 1);
+        if (k == g.k0) more = walk.next(a, after);
         const int nb = boxes_of(g.s.kv - k * kTile - 64 * rank, box);
         int row[4];
 #pragma unroll
@@ -394,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t v_tail = smem_u32(&bars->v_tail);
     uint32_t t = 0, tails = 0;
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    for (; ok && more; g = after) {
       const auto look = [&](int tile) {  // lane q: the row of box q of the tile
         return lane < 2 * boxes ? key_row(a, g.b, g.s.kv, tile * kTile + lane * box) : 0;
       };
@@ -402,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (int k = g.k0; k < g.k1; ++k, ++t) {
         const int rows = rows_next;
         if (k + 1 < g.k1) rows_next = look(k + 1);
+        if (k == g.k0) more = walk.next(a, after);
         const int left = min(g.s.kv - k * kTile, kTile);  // > 0
         const bool tail = left < kTile;
         if (tail && lane == 0)
@@ -461,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t t = 0;  // tiles over the run
     int ns = 0;      // segments
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    for (; ok && more; g = after) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, ns & 1, status, abort_flag));
       for (int k = g.k0; k < g.k1 && ok; ++k, ++t) {
         // The score tile to be overwritten, that of tile t - 2, has been read.
@@ -490,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           }
           __syncwarp();
         }
+        if (k == g.k0) more = walk.next(a, after);
       }
       ++ns;
     }
@@ -502,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t t = 0;
     int ns = 0;
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    for (; ok && more; g = after) {
       for (int k = g.k0; k < g.k1 && ok; ++k, ++t) {
         ok = mbar_wait(&bars->p_ready, t & 1, status, abort_flag);
         if (ok && k == g.k0 && ns > 0)  // the segment before has read its mix out
@@ -524,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           }
           __syncwarp();
         }
+        if (k == g.k0) more = walk.next(a, after);
       }
       ++ns;
     }
@@ -540,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const float sl2 = a.scale_log2;
     uint32_t t = 0;
     bool ok = true, gone = false;  // a wait of this thread's gave up; all four warps leave
-    while (walk.next(a, g)) {
+    for (; more; g = after) {
       const int row = g.m * kRows + 64 * rank + r;  // row of the sequence
       const bool real = row < g.s.n * a.H;
       const int i = row / a.H;                      // new token
@@ -641,6 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (lane == 0) tp::arrive(p_ready);
       }
       if (gone) break;
+      more = walk.next(a, after);
       // The segment's mix, once its last tile has been added.
       ok = ok && mbar_wait(&bars->mix_done, (t - 1) & 1, status, abort_flag);
       __syncwarp();
@@ -667,6 +542,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::tmem_ld32(tbase + lane_off + kColO + c * 32, o);
         tc::tmem_wait_ld();
         pin<32>(o);
+        if (c == 7) {  // the mix is out of TMEM: the next segment's may be written
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tp::arrive(o_free);
+        }
         const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
         if (whole) {
 #pragma unroll
@@ -709,9 +589,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         __syncwarp();
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tp::arrive(o_free);
       softmax_and(true);  // the sums have been read before the next tile's maxima
     }
   }
@@ -732,91 +609,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tc::fence_after_sync();
     tp::tmem_dealloc(tbase, 512);
   }
-}
-
-// ---- merge and up-projection ---------------------------------------------------------------
-// One row (token t, head h) of the mix as bf16, the up-projection's operand: taken as it is from
-// a unit finished by one range, or merged from the partials of the ranges that share the unit:
-// sum 2^(m_s - m) acc_s / sum 2^(m_s - m) l_s.  One warp; lane owns columns 4 lane + 128 k.
-__device__ __forceinline__ void tree_merge_row(const TreeArgs& a, int t, int h, int lane,
-                                               uint16_t* dst) {
-  int lo = 0, hi = a.B;  // the last sequence that starts at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
-  }
-  const TreeSeq s = tree_seq(a, lo);
-  const int K = seq_tiles(s);
-  const int row = max(t - s.q0, 0) * a.H + h, r = row % kRows;
-  const int64_t W = a.tile0[a.B], V = a.ranges[0];
-  const int64_t x0 = a.tile0[lo] + (int64_t)(row / kRows) * K;
-  float4 acc[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  // Without keys, or in no sequence (a bad length or offset), the row is zero.
-  if (K > 0 && t >= s.q0 && t < s.q0 + s.n) {
-    const int64_t v0 = ((x0 + 1) * V - 1) / W, v1 = ((x0 + K) * V - 1) / W;
-    if (v0 == v1) {
-      const uint2* src = reinterpret_cast<const uint2*>(a.q_lat + ((size_t)t * a.H + h) * kLD);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) = src[lane + 32 * k];
-      return;
-    }
-    float m = -INFINITY;
-    for (int64_t v = v0; v <= v1; ++v) {
-      const int64_t slot = v > v0 || range_start(v, W, V) == x0 ? 2 * v : 2 * v + 1;
-      const float2 ml = reinterpret_cast<const float2*>(a.part_ml)[slot * kRows + r];
-      const float4* src = reinterpret_cast<const float4*>(a.part_acc + (slot * kRows + r) * kLD) + lane;
-      const float m2 = fmaxf(m, ml.x);
-      const float base = m2 == -INFINITY ? 0.f : m2;
-      const float f0 = ex2_approx(m - base), f1 = ex2_approx(ml.x - base);
-      m = m2;
-      l = l * f0 + ml.y * f1;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 w = src[32 * k];
-        acc[k].x = acc[k].x * f0 + w.x * f1;
-        acc[k].y = acc[k].y * f0 + w.y * f1;
-        acc[k].z = acc[k].z * f0 + w.z * f1;
-        acc[k].w = acc[k].w * f0 + w.w * f1;
-      }
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) =
-        make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
-                   pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-}
-
-// out[t,h] = W_V[h] mix[t,h] for one head and 32 tokens; the weight is on its way before the
-// split kernel is waited for.  Rows from cu_q[B] on are not written.
-__global__ void __launch_bounds__(512) tree_up_kernel(const TreeArgs a) {
-  extern __shared__ __align__(16) uint8_t up_smem[];
-  uint16_t* sw = reinterpret_cast<uint16_t*>(up_smem);
-  uint16_t* so = sw + 128 * kUpRow;
-  const int h = blockIdx.x;
-  const int t0 = blockIdx.y * kCuB;
-  up_load_weight(sw, a.w_kvb, h);
-  grid_dep_wait();
-  const int nb = min(kCuB, min(max(a.cu_q[a.B], 0), a.T) - t0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = warp; i < kCuB; i += 16) {
-    uint16_t* row = so + i * kUpRow;
-    if (i < nb) {
-      tree_merge_row(a, t0 + i, h, lane, row);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint2*>(row + 4 * lane + 128 * k) = make_uint2(0u, 0u);
-    }
-  }
-  cp_async_wait_all();
-  __syncthreads();
-  up_project(so, sw, a.out + ((size_t)t0 * a.H + h) * 128, (size_t)a.H * 128, nb);
 }
 
 // Tensor maps, cached by pointers and sizes (encoding costs microseconds of host time).
@@ -874,24 +666,17 @@ cudaError_t launch_latent_tree(const TreeArgs& a, cudaStream_t stream) {
   TreeParams p;
   if (!tree_maps(a, &p)) return cudaErrorInvalidValue;
   p.a = a;
-  static std::atomic<uint64_t> attr_done{0};  // bit per device: smem attributes set
+  static std::atomic<uint64_t> attr_done{0};  // bit per device: smem attribute set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(tree_absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kAbsorbSmem);
-    if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(tree_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(tree_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCuSmem);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_release);
   }
-  tree_absorb_kernel<<<dim3(a.H, kLD / kAbN, (unsigned)((a.T + kPB - 1) / kPB)), 256, kAbsorbSmem,
-                       stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_tree_fold(a, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -905,12 +690,7 @@ cudaError_t launch_latent_tree(const TreeArgs& a, cudaStream_t stream) {
   cfg.dynamicSmemBytes = kSmem;
   e = cudaLaunchKernelEx(&cfg, tree_split_kernel, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.H, (unsigned)((a.T + kCuB - 1) / kCuB));
-  cfg.blockDim = dim3(512);
-  cfg.dynamicSmemBytes = kCuSmem;
-  e = cudaLaunchKernelEx(&cfg, tree_up_kernel, a);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return launch_tree_up(a, stream);
 }
 
 }  // namespace mla

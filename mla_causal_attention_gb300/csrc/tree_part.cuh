@@ -1,0 +1,227 @@
+// tree_part.cuh -- how the work of the tree attention is shared out between the CTA pairs, for the
+// kernel that makes the partition and those that walk through it.
+#pragma once
+#include <cstdint>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace mla {
+namespace tree {
+
+constexpr int kTile = 128;  // keys per tile
+constexpr int kRows = 128;  // query rows per unit, 64 per CTA
+
+// ---- the partition -----------------------------------------------------------------------
+// Sequence b has n_b H rows in M_b units and K_b key tiles.  Units are numbered, and their tiles
+// laid end to end, in the order (sequence, unit, key).  Pair c does units c, c + P, c + 2 P, ..
+// whole for the first n_w waves of P units: in a wave the pairs walk through the keys of the
+// same few sequences at the same time, and find them in L2.  The tiles of the remaining units
+// are cut into one contiguous range per pair, each as long as brings the pair's work to the
+// common level; n_w is the largest number of waves that leaves every pair at or below it.  A
+// range's tiles of one unit are a segment: a unit within one segment is finished there, the
+// others leave partial mixes, range c's first segment in slot 2 c, its last, if another, in slot
+// 2 c + 1.
+struct TreeSeq {
+  int q0, n, kv, ctx;
+  bool bad;
+};
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
+  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], k = a.kv_len[b];
+  TreeSeq s;
+  s.q0 = min(max(c0, 0), a.T);
+  s.n = min(max(c1, s.q0), a.T) - s.q0;
+  s.kv = (int)min((int64_t)max(k, 0), (int64_t)a.max_pages << a.page_shift);
+  s.ctx = max(s.kv - s.n, 0);
+  s.bad = s.q0 != c0 || s.q0 + s.n != c1 || s.kv != k || s.kv < s.n;
+  return s;
+}
+__device__ __forceinline__ int seq_tiles(const TreeSeq& s) { return (s.kv + kTile - 1) / kTile; }
+// Units of a sequence; without keys (a bad length) it has none, and its rows are zero.
+__device__ __forceinline__ int seq_units(const TreeArgs& a, const TreeSeq& s) {
+  return s.kv > 0 ? (s.n * a.H + kRows - 1) / kRows : 0;
+}
+
+// The last of n ascending values that is <= x (the first is).
+template <typename T>
+__device__ __forceinline__ int find_last(const T* v, int n, T x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+// The same by a whole warp, 32 probes at a time.
+template <typename T>
+__device__ __forceinline__ int find_warp(const T* v, int n, T x, int lane) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, at < hi && v[at] <= x);
+    lo += (31 - __clz(le | 1u)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// By one block of 256 threads: prefix sums of units and tiles, the waves, the ranges.
+static __device__ __noinline__ void tree_partition(const TreeArgs& a) {
+  __shared__ int64_t s_w[8], s_u[8], s_x;
+  __shared__ int s_more;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t W = 0, U = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 256) {
+    const int b = b0 + tid;
+    int64_t w = 0, u = 0;
+    if (b < a.B) {
+      const TreeSeq s = tree_seq(a, b);
+      if (s.bad) set_status(a.status, MLA_ERR_KVLEN);
+      if (a.draft_mask && s.n > 64) set_status(a.status, MLA_ERR_TREE);
+      u = seq_units(a, s);
+      w = u * seq_tiles(s);
+    }
+    int64_t inc_w = w, inc_u = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, inc_w, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc_u, o);
+      if (lane >= o) {
+        inc_w += x;
+        inc_u += y;
+      }
+    }
+    if (lane == 31) {
+      s_w[warp] = inc_w;
+      s_u[warp] = inc_u;
+    }
+    __syncthreads();
+    int64_t before_w = W, before_u = U;
+    for (int k = 0; k < 8; ++k) {
+      if (k < warp) {
+        before_w += s_w[k];
+        before_u += s_u[k];
+      }
+      W += s_w[k];
+      U += s_u[k];
+    }
+    if (b < a.B) {
+      a.tile0[b] = before_w + inc_w - w;
+      a.unit0[b] = before_u + inc_u - u;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.tile0[a.B] = W;
+    a.unit0[a.B] = U;
+  }
+  __syncthreads();  // the block reads these back
+  // Thread c: the tiles of pair c's whole units, for ever fewer waves until no pair is above the
+  // level.
+  const int P = a.pairs;  // at most 256
+  const int64_t level = (W + P - 1) / P;
+  int64_t nw = U / P, load = 0;
+  int at = 0;  // the sequence of the unit looked at last
+  const auto tiles_of = [&](int64_t u) {
+    while (a.unit0[at + 1] <= u) ++at;
+    while (a.unit0[at] > u) --at;
+    return (int64_t)seq_tiles(tree_seq(a, at));
+  };
+  if (tid < P)
+    for (int64_t i = 0; i < nw; ++i) load += tiles_of(i * P + tid);
+  while (nw > 0) {
+    __syncthreads();
+    if (tid == 0) s_more = 0;
+    __syncthreads();
+    if (tid < P && load > level) s_more = 1;
+    __syncthreads();
+    if (s_more == 0) break;
+    --nw;
+    if (tid < P) load -= tiles_of(nw * P + tid);
+  }
+  // Ranges, from the first tile behind the whole units on.
+  const int64_t need = tid < P ? level - load : 0;
+  int64_t inc = need;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) s_w[warp] = inc;
+  if (tid == 0) {
+    const int64_t u = nw * P;
+    s_x = W;
+    if (u < U) {
+      const int b = find_last(a.unit0, a.B, u);
+      s_x = a.tile0[b] + (u - a.unit0[b]) * seq_tiles(tree_seq(a, b));
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < warp; ++k) inc += s_w[k];
+  if (tid < P) a.range0[tid] = min(s_x + inc - need, W);
+  if (tid == 0) {
+    a.range0[P] = W;
+    a.range0[P + 1] = nw;
+  }
+}
+
+// One segment: rows 128 m .. of sequence b's rows, key tiles [k0, k1).
+struct Seg {
+  int b, m, k0, k1;
+  TreeSeq s;
+  int slot;  // partial slot, or -1: the unit is finished here
+};
+// Walks a pair's segments: its whole units, then its range.  Warp-uniform; every role has its own
+// and looks the next segment up while it works on one, since that takes a chain of loads.
+struct SegWalk {
+  int64_t wave, waves, x, x1, base, next_base;
+  int pair, b, K, lane, slot;
+  TreeSeq s;
+  __device__ __forceinline__ SegWalk(const TreeArgs& a, int pair_id, int lane_id) {
+    pair = pair_id;
+    lane = lane_id;
+    wave = 0;
+    waves = a.range0[a.pairs + 1];
+    x = a.range0[pair];
+    x1 = a.range0[pair + 1];
+    b = -1;
+    slot = 2 * pair;
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a, Seg& g) {
+    if (wave < waves) {
+      const int64_t u = wave * a.pairs + pair;
+      ++wave;
+      g.b = find_warp(a.unit0, a.B, u, lane);
+      g.m = (int)(u - a.unit0[g.b]);
+      g.s = tree_seq(a, g.b);
+      g.k0 = 0;
+      g.k1 = seq_tiles(g.s);
+      g.slot = -1;
+      return true;
+    }
+    if (x >= x1) return false;
+    if (b < 0) enter(a, find_warp(a.tile0, a.B, x, lane));
+    while (x >= next_base) enter(a, b + 1);  // skips sequences without work
+    const int64_t off = x - base;
+    g.b = b;
+    g.m = (int)(off / K);
+    g.k0 = (int)(off - (int64_t)g.m * K);
+    g.k1 = (int)min((int64_t)K, g.k0 + (x1 - x));
+    g.s = s;
+    g.slot = g.k0 == 0 && g.k1 == K ? -1 : slot;
+    slot = 2 * pair + 1;
+    x += g.k1 - g.k0;
+    return true;
+  }
+  __device__ __forceinline__ void enter(const TreeArgs& a, int seq) {
+    b = seq;
+    base = a.tile0[b];
+    next_base = a.tile0[b + 1];
+    s = tree_seq(a, b);
+    K = seq_tiles(s);
+  }
+};
+
+}  // namespace tree
+}  // namespace mla

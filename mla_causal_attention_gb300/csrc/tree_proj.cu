@@ -1,0 +1,417 @@
+// tree_proj.cu -- before and after the tree attention's split kernel: the query folded into the
+// latent space (with the partition of the work), the merge of partial mixes, and the mix projected
+// up, out = W_V mix.
+//
+// The two projections are one batched GEMM, a matrix per head:
+//   fold  q_lat[t,h,:] = q_nope[t,h,:] W_K[h]      [T x 128] . [128 x 512]
+//   up    out[t,h,:]   = mix[t,h,:] W_V[h]^T       [T x 512] . [512 x 128]
+// with W_K[h], W_V[h] the first and second 128 rows of head h's 256 of kv_b_proj.  A block keeps
+// its head's 128 KB of weight in shared memory and takes 128 tokens at a time: rows by TMA through
+// a ring, MMAs into one of two TMEM tiles while the epilogue warps read the other.  Bound by the
+// rows' traffic (1280 bytes per token and head for each); with mma.sync, whose fragments come from
+// shared memory over and over, the two took 53 and 106 us for 1024 tokens and 64 heads.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+#include "tree_part.cuh"
+
+namespace mla {
+namespace {
+
+using namespace tree;
+
+constexpr int kLD = 512;
+constexpr int kM = 128;               // tokens per tile
+constexpr int kSub = 128 * 128;       // 128 rows x 64 columns, bf16, 128-byte swizzled
+constexpr int kSlots = 5;             // ring of the rows' sub-tiles
+constexpr int kOffRing = 8 * kSub;    // behind the weight's 8 sub-tiles
+constexpr int kOffBar = kOffRing + kSlots * kSub;
+constexpr int kSmem = kOffBar + 256 + 1024;
+static_assert(kSmem <= 232448, "shared memory per block");
+
+struct ProjParams {
+  CUtensorMap tm_x;  // rows    {K, T, H}, boxes {64, 128, 1}
+  CUtensorMap tm_w;  // w_kvb   {512, H * 256}, boxes {64, 128}
+  TreeArgs a;
+  int blocks_y;      // blocks per head
+};
+struct PBars {
+  uint64_t w_full;
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t d_full[2], d_free[2];  // accumulator tiles (d_free: 4 epilogue warps)
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(PBars) <= 256, "barrier block");
+
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(a, parity))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+}
+
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]),
+                 "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+// kUp: K = 512 in 8 sub-tiles, N = 128, weight K-major.  Fold: K = 128 in 2 sub-tiles, N = 512 in
+// two blocks of 256, weight MN-major (its rows are the contraction).
+// Warps: 0 TMA, 1 MMA, 4-7 epilogue.  The fold launch has one block more, which makes the partition.
+template <bool kUp>
+__global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant__ ProjParams p) {
+  constexpr int kKs = kUp ? 8 : 2, kNb = kUp ? 1 : 2, kN = kUp ? 128 : 256;
+  grid_dep_launch();
+  const TreeArgs& a = p.a;
+  if (!kUp && blockIdx.x == gridDim.x - 1) {
+    tree_partition(a);
+    return;
+  }
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sW = smem;
+  uint8_t* sX = smem + kOffRing;
+  PBars* bars = reinterpret_cast<PBars*>(smem + kOffBar);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x / p.blocks_y, y = blockIdx.x % p.blocks_y;
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->w_full, 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->d_full[i], 1);
+      mbar_init(&bars->d_free[i], 4);
+    }
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&bars->tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = bars->tmem_base;
+  // The weight is no kernel's output: it is on its way before the kernel in front is waited for.
+  if (warp == 0 && lane == 0) {
+    mbar_arrive_expect_tx(&bars->w_full, 8 * kSub);
+    for (int s = 0; s < 8; ++s)
+      tma_load_2d(sW + s * kSub, &p.tm_w, &bars->w_full, 64 * s, h * 256 + (kUp ? 128 : 0));
+  }
+  if (kUp) grid_dep_wait();
+  const int rows = kUp ? min(max(a.cu_q[a.B], 0), a.T) : a.T;
+  const int tiles = (rows + kM - 1) / kM;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t u = 0;
+      bool ok = true;
+      for (int i = y; i < tiles && ok; i += p.blocks_y)
+        for (int s = 0; s < kKs && ok; ++s, ++u) {
+          const uint32_t slot = u % kSlots, n = u / kSlots;
+          if (n > 0) ok = mbar_wait(&bars->empty[slot], (n - 1) & 1, a.status, abort_flag);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars->full[slot], kSub);
+          tma_load_3d_nohint(sX + slot * kSub, &p.tm_x, &bars->full[slot], 64 * s, i * kM, h);
+        }
+      // Every copy has landed before shared memory is given up.
+      drain(&bars->w_full, 0);
+      for (uint32_t k = u > kSlots ? u - kSlots : 0; k < u; ++k)
+        drain(&bars->full[k % kSlots], (k / kSlots) & 1);
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t kId = tc::idesc_bf16_f32(128, kN, !kUp);
+    const uint64_t d_x = tc::smem_desc_sw128(0, 16, 1024);
+    const uint64_t d_w = tc::smem_desc_sw128(0, kUp ? 16 : kSub, 1024);
+    const uint32_t x_lo = smem_u32(sX) >> 4, w_lo = smem_u32(sW) >> 4;
+    uint32_t u = 0, d = 0;  // sub-tiles, accumulator tiles
+    bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->w_full, 0, a.status, abort_flag));
+    for (int i = y; i < tiles && ok; i += p.blocks_y) {
+      for (int nb = 0; nb < kNb && ok; ++nb, ++d) {
+        if (d > 1) ok = mbar_wait(&bars->d_free[d & 1], ((d >> 1) - 1) & 1, a.status, abort_flag);
+#pragma unroll 1
+        for (int s = 0; s < kKs; ++s) {
+          const uint32_t slot = (u + s) % kSlots, n = (u + s) / kSlots;
+          ok = ok && mbar_wait(&bars->full[slot], n & 1, a.status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              // up: sub-tile s of the weight, K-major; fold: rows 64 s + 16 kk .. of the weight,
+              // MN-major, columns 256 nb .. in four sub-tiles
+              const uint32_t w_at =
+                  kUp ? w_lo + s * (kSub >> 4) + 2 * kk
+                      : w_lo + 4 * nb * (kSub >> 4) + (4 * s + kk) * (2048 >> 4);
+              tc::mma_ss(tbase + (d & 1) * 256,
+                         d_x | (uint64_t)(x_lo + slot * (kSub >> 4) + 2 * kk),
+                         d_w | (uint64_t)w_at, kId, (s | kk) != 0 ? 1u : 0u);
+            }
+            if (nb == kNb - 1) tc::commit(&bars->empty[slot]);
+            if (s == kKs - 1) tc::commit(&bars->d_full[d & 1]);
+          }
+          __syncwarp();
+        }
+      }
+      u += kKs;
+    }
+    // No MMA runs on when TMEM is released: the last tiles are waited for.
+    if (ok)
+      for (uint32_t k = d > 2 ? d - 2 : 0; k < d; ++k) drain(&bars->d_full[k & 1], (k >> 1) & 1);
+    else if (tc::elect_one())
+      tc::commit(&bars->w_full), drain(&bars->w_full, 1);
+    __syncwarp();
+  } else if (warp >= 4) {
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int r = (warp & 3) * 32 + lane;
+    uint32_t d = 0;
+    bool ok = true;
+    for (int i = y; i < tiles && ok; i += p.blocks_y)
+      for (int nb = 0; nb < kNb && ok; ++nb, ++d) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&bars->d_full[d & 1], (d >> 1) & 1, a.status, abort_flag));
+        if (!ok) break;
+        tc::fence_after_sync();
+        const int t = i * kM + r;
+        uint16_t* dst = kUp ? a.out + ((size_t)t * a.H + h) * 128
+                            : a.q_lat + ((size_t)t * a.H + h) * kLD + 256 * nb;
+#pragma unroll 1
+        for (int c = 0; c < kN / 32; ++c) {
+          uint32_t o[32];
+          tc::tmem_ld32(tbase + lane_off + (d & 1) * 256 + c * 32, o);
+          tc::tmem_wait_ld();
+          pin<32>(o);
+          if (c == kN / 32 - 1) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->d_free[d & 1]);
+          }
+          if (t < rows) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]),
+                                   __uint_as_float(o[8 * e + 2 * k + 1]));
+              *reinterpret_cast<uint4*>(dst + c * 32 + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, 512);
+  }
+}
+
+// Partial mixes of the units shared by several pairs: sum 2^(m_s - m) acc_s / sum 2^(m_s - m) l_s
+// over the segments, to bf16 (the up-projection's operand type) where the whole units' mixes are.
+// A warp per row, 16 rows of one unit per block and turn; bound by reading the partials.
+__global__ void __launch_bounds__(512) tree_merge_kernel(const TreeArgs a) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t u0 = a.range0[a.pairs + 1] * a.pairs, U = a.unit0[a.B];
+  for (int64_t i = blockIdx.x; i < (U - u0) * 8; i += gridDim.x) {
+    const int64_t u = u0 + (i >> 3);
+    const int b = find_warp(a.unit0, a.B, u, lane);
+    const TreeSeq s = tree_seq(a, b);
+    const int m_unit = (int)(u - a.unit0[b]), K = seq_tiles(s);
+    const int r = (int)(i & 7) * 16 + warp;
+    const int row = m_unit * kRows + r;
+    if (row >= s.n * a.H) continue;
+    const int64_t x0 = a.tile0[b] + (int64_t)m_unit * K;
+    const int c0 = find_warp(a.range0, a.pairs, x0, lane);
+    const int c1 = find_warp(a.range0, a.pairs, x0 + K - 1, lane);
+    if (c0 == c1) continue;  // finished by one pair
+    const bool starts = a.range0[c0] == x0;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    for (int cb = c0; cb <= c1; cb += 32) {  // lane i: the i-th range of this round
+      const int c = cb + lane;
+      const bool in = c <= c1 && a.range0[c] < a.range0[c + 1];
+      const int slot = c > c0 || starts ? 2 * c : 2 * c + 1;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (in) ml = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot * kRows + r];
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float m2 = fmaxf(m, top), base = m2 == -INFINITY ? 0.f : m2;
+      const float f0 = ex2_approx(m - base), f = ex2_approx(ml.x - base);
+      float sum = ml.y * f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l = l * f0 + sum;
+      m = m2;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[k].x *= f0;
+        acc[k].y *= f0;
+        acc[k].z *= f0;
+        acc[k].w *= f0;
+      }
+      uint32_t left = __ballot_sync(0xffffffffu, in);
+      while (left != 0) {  // two partials' rows in flight
+        float4 v[2][4];
+        float fu[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = left ? __ffs(left) - 1 : 0;
+          const float w = __shfl_sync(0xffffffffu, f, at);
+          const int sl = __shfl_sync(0xffffffffu, slot, at);
+          fu[e] = left ? w : 0.f;
+          const float4* src =
+              reinterpret_cast<const float4*>(a.part_acc + ((size_t)sl * kRows + r) * kLD) + lane;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[e][k] = left ? src[32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
+          left &= left - 1;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[k].x = fmaf(fu[e], v[e][k].x, acc[k].x);
+            acc[k].y = fmaf(fu[e], v[e][k].y, acc[k].y);
+            acc[k].z = fmaf(fu[e], v[e][k].z, acc[k].z);
+            acc[k].w = fmaf(fu[e], v[e][k].w, acc[k].w);
+          }
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint16_t* dst = a.q_lat + ((size_t)s.q0 * a.H + row) * kLD;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) =
+          make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
+                     pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+  }
+}
+
+// Tensor maps, cached by pointers and sizes (encoding costs microseconds of host time).
+struct MapKey {
+  const void* x;
+  const void* w;
+  int T, H, up;
+  bool operator==(const MapKey& o) const {
+    return x == o.x && w == o.w && T == o.T && H == o.H && up == o.up;
+  }
+};
+struct MapEntry {
+  MapKey key;
+  CUtensorMap maps[2];
+  bool valid;
+};
+std::mutex g_mu;
+MapEntry g_maps[16];
+int g_next = 0;
+
+bool proj_maps(const TreeArgs& a, bool up, ProjParams* p) {
+  const MapKey key = {up ? a.q_lat : a.q_nope, a.w_kvb, a.T, a.H, up};
+  std::lock_guard<std::mutex> lk(g_mu);
+  for (const MapEntry& e : g_maps)
+    if (e.valid && e.key == key) {
+      p->tm_x = e.maps[0];
+      p->tm_w = e.maps[1];
+      return true;
+    }
+  const uint64_t width = up ? kLD : 128;
+  const uint64_t dims[3] = {width, (uint64_t)a.T, (uint64_t)a.H};
+  const uint64_t strides[2] = {(uint64_t)a.H * width * 2, width * 2};
+  const uint32_t box[3] = {64, kM, 1};
+  const uint64_t wdims[2] = {kLD, (uint64_t)a.H * 256};
+  const uint64_t wstrides[1] = {kLD * 2};
+  const uint32_t wbox[2] = {64, 128};
+  if (!encode_bf16_tiled(&p->tm_x, key.x, 3, dims, strides, box) ||
+      !encode_bf16_tiled(&p->tm_w, key.w, 2, wdims, wstrides, wbox))
+    return false;
+  MapEntry& e = g_maps[g_next];
+  g_next = (g_next + 1) % 16;
+  e.key = key;
+  e.maps[0] = p->tm_x;
+  e.maps[1] = p->tm_w;
+  e.valid = true;
+  return true;
+}
+
+cudaError_t set_attributes() {
+  static std::atomic<uint64_t> attr_done{0};  // bit per device: smem attributes set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (attr_done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(tree_proj_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(tree_proj_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmem);
+  if (e != cudaSuccess) return e;
+  attr_done.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// Blocks per head: as many as there are SMs for, and token tiles.
+int blocks_per_head(const TreeArgs& a) {
+  return std::min((a.T + kM - 1) / kM, std::max(1, 2 * a.pairs / a.H));
+}
+
+}  // namespace
+
+cudaError_t launch_tree_fold(const TreeArgs& a, cudaStream_t stream) {
+  cudaError_t e = set_attributes();
+  if (e != cudaSuccess) return e;
+  ProjParams p;
+  if (!proj_maps(a, false, &p)) return cudaErrorInvalidValue;
+  p.a = a;
+  p.blocks_y = blocks_per_head(a);
+  tree_proj_kernel<false><<<a.H * p.blocks_y + 1, 256, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_up(const TreeArgs& a, cudaStream_t stream) {
+  ProjParams p;
+  if (!proj_maps(a, true, &p)) return cudaErrorInvalidValue;
+  p.a = a;
+  p.blocks_y = blocks_per_head(a);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(4 * a.pairs);
+  cfg.blockDim = dim3(512);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.H * p.blocks_y);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = kSmem;
+  e = cudaLaunchKernelEx(&cfg, tree_proj_kernel<true>, p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace mla

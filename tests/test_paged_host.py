@@ -133,7 +133,7 @@ TREE = ["q_nope", "q_pe", "c_pages", "pe_pages", "num_pages", "page_size", "bloc
 def _tree_args(base, lib):
     a = {n: base + 256 * i for i, n in enumerate(TREE)}
     a.update(num_pages=4, page_size=16, max_pages=2, B=2, T=3, H=4, scale=0.1, stream=None,
-             workspace_bytes=lib.mla_latent_tree_workspace_bytes(3, 4, 2, 4, 16))
+             workspace_bytes=lib.mla_latent_tree_workspace_bytes(3, 4, 2))
     return a
 
 
@@ -160,8 +160,8 @@ def test_tree_refuses_alignment_and_small_workspaces(lib, base):
     a = _tree_args(base, lib)
     a["draft_mask"] += 4
     assert lib.mla_latent_tree_fwd(*[a[n] for n in TREE]) == S.ERR_ALIGN
-    assert lib.mla_latent_tree_workspace_bytes(0, 4, 2, 4, 16) == 0
-    assert lib.mla_latent_tree_workspace_bytes(3, 4, 2, 4, 24) == 0
+    assert lib.mla_latent_tree_workspace_bytes(0, 4, 2) == 0
+    assert lib.mla_latent_tree_workspace_bytes(3, 1025, 2) == 0
     a = _tree_args(base, lib)
     a["workspace_bytes"] = 256
     want = (S.ERR_WORKSPACE,) if torch.cuda.is_available() else _no_device()
