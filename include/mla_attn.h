@@ -323,6 +323,37 @@ MLA_API mla_status mla_attn_rope_append_fwd(const uint16_t* q_nope, const uint16
                                             size_t workspace_bytes, void* cuda_stream);
 
 /*
+ * Causal attention over whole prompts of different lengths, packed one behind the other: rows
+ * cu_seqlens[b] .. cu_seqlens[b+1] - 1 of every tensor are sequence b, and row i of it attends
+ * to its rows j <= i.  Per head the core described at the top of this file; the H query heads
+ * come in groups of H / Hkv that share one key/value head (Hkv = H: a key/value head each), and
+ * all share the rotary key.
+ *
+ *   q_nope [T, H, 128]    q_pe [T, H, 64]    k_nope, v [T, Hkv, 128]    k_pe [T, 64]
+ *   cu_seqlens [B + 1] int32    out [T, H, 128], contiguous
+ *
+ * strides (elements; NULL: contiguous) lets the inputs be slices of larger tensors, such as the
+ * query projection's [T, H, 192] and the key/value projection's [T, Hkv, 256]: the last
+ * dimension is contiguous, the others' strides are positive multiples of 8.  Sequences may be
+ * empty; rows from cu_seqlens[B] on are padding, and out is left as it was there.  Another
+ * sequence's rows never reach a result, whatever they hold.
+ * Offsets that are not rising within [0, T] are clamped (MLA_ERR_KVLEN in the status word; what
+ * their sequences get is not meaningful).  Workspace: mla_attn_varlen_workspace_bytes(T, B),
+ * zeroed once.
+ */
+typedef struct {
+  int64_t q_nope_row, q_nope_head, q_pe_row, q_pe_head;
+  int64_t k_nope_row, k_nope_head, k_pe_row, v_row, v_head;
+} mla_varlen_strides;
+MLA_API size_t mla_attn_varlen_workspace_bytes(int T, int B);
+MLA_API mla_status mla_attn_varlen_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
+                                       const uint16_t* k_nope, const uint16_t* k_pe,
+                                       const uint16_t* v, const mla_varlen_strides* strides,
+                                       const int32_t* cu_seqlens, int B, int T, int H, int Hkv,
+                                       float softmax_scale, uint16_t* out, void* workspace,
+                                       size_t workspace_bytes, void* cuda_stream);
+
+/*
  * ---- Serving over a paged latent cache ---------------------------------------------------
  *
  * The latent cache (512-wide latent row + 64-wide rotary key per token, see

@@ -71,6 +71,7 @@ EXPORTED = ("mla_attn_workspace_bytes", "mla_attn_fwd", "mla_attn_fwd_ex",
             "mla_attn_masked_workspace_bytes", "mla_attn_masked_fwd",
             "mla_latent_workspace_bytes", "mla_latent_decode_fwd",
             "mla_oproj_workspace_bytes", "mla_oproj_fwd", "mla_paged_plan",
+            "mla_attn_varlen_workspace_bytes", "mla_attn_varlen_fwd",
             "mla_latent_append", "mla_latent_tree_workspace_bytes", "mla_latent_tree_fwd")
 
 
@@ -135,6 +136,10 @@ def library():
         lib.mla_latent_tree_fwd.restype = i
         lib.mla_latent_tree_fwd.argtypes = [p, p, p, p, i, i, p, i, p, p, p, p, i, i, i, f, p, p,
                                             sz, p]
+        lib.mla_attn_varlen_workspace_bytes.restype = sz
+        lib.mla_attn_varlen_workspace_bytes.argtypes = [i, i]
+        lib.mla_attn_varlen_fwd.restype = i
+        lib.mla_attn_varlen_fwd.argtypes = [p, p, p, p, p, p, p, i, i, i, i, f, p, p, sz, p]
         _lib = lib
         return lib
 
@@ -569,6 +574,55 @@ def mla_latent_tree_fwd(q_nope, q_pe, c_pages, pe_pages, block_table, kv_len, cu
         q_nope.data_ptr(), q_pe.data_ptr(), c_pages.data_ptr(), pe_pages.data_ptr(), num_pages,
         page_size, block_table.data_ptr(), max_pages, kv_len.data_ptr(), cu_q.data_ptr(),
         _addr(draft_mask), w_kvb.data_ptr(), B, T, H, float(softmax_scale), out.data_ptr()))
+    return out
+
+
+def _slices(t, name, shape, device):
+    """(row, head) strides of a [T, heads, width] tensor that may be a slice of a larger one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    st = t.stride()
+    # a dimension of one element has no stride of its own
+    head = st[-2] if len(shape) == 3 and shape[1] > 1 else shape[-1]
+    row = st[0] if shape[0] > 1 else head * (shape[1] if len(shape) == 3 else 1)
+    if st[-1] != 1 or row % 8 or head % 8 or row < 8 or head < 8:
+        raise ValueError(f"{name}: the last dimension must be contiguous and the other strides "
+                         f"positive multiples of 8, got {st}")
+    return row, head
+
+
+def mla_attn_varlen_fwd(q_nope, q_pe, k_nope, k_pe, v, cu_seqlens, softmax_scale: float, out=None,
+                        workspace: "Workspace | None" = None, stream=None):
+    """Causal attention over packed prompts: sequence b is rows cu_seqlens[b] .. of every tensor.
+
+    q_nope [T,H,128], q_pe [T,H,64], k_nope / v [T,Hkv,128] (Hkv divides H), k_pe [T,64]
+    (bf16; slices of larger tensors are read in place), cu_seqlens [B+1] int32.  Returns out
+    [T,H,128]; rows from cu_seqlens[B] on are left as they were."""
+    dev = q_nope.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    T, H = q_nope.shape[:2]
+    Hkv, B = k_nope.shape[1], cu_seqlens.shape[0] - 1
+    st = (*_slices(q_nope, "q_nope", (T, H, 128), dev), *_slices(q_pe, "q_pe", (T, H, 64), dev),
+          *_slices(k_nope, "k_nope", (T, Hkv, 128), dev), _slices(k_pe, "k_pe", (T, 64), dev)[0],
+          *_slices(v, "v", (T, Hkv, 128), dev))
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    if out is None:
+        out = torch.empty((T, H, 128), dtype=torch.bfloat16, device=dev)
+    else:
+        _check(out, "out", torch.bfloat16, (T, H, 128), dev)
+    strides = (ctypes.c_int64 * 9)(*st)
+    _enqueue("mla_attn_varlen_fwd", dev, stream, workspace,
+             library().mla_attn_varlen_workspace_bytes(T, B), (
+                 q_nope.data_ptr(), q_pe.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(),
+                 v.data_ptr(), ctypes.addressof(strides), cu_seqlens.data_ptr(), B, T, H, Hkv,
+                 float(softmax_scale), out.data_ptr()))
     return out
 
 

@@ -98,6 +98,20 @@ size_t latent_workspace(int B, int H, int grid) {
          latent_ml_bytes(B, H, grid) + latent_acc_bytes(B, H, grid);
 }
 
+// Workspace of the packed prompts: the status word, the number of query tile pairs, the pairs,
+// and a counter per length class.
+struct VarlenLayout {
+  size_t n_pairs, pairs, count, total;
+};
+VarlenLayout varlen_layout(int T, int B) {
+  VarlenLayout l;
+  l.n_pairs = kStatusBytes;
+  l.pairs = l.n_pairs + 256;
+  l.count = l.pairs + r256((size_t)varlen_max_pairs(T, B) * 16);
+  l.total = l.count + r256(((size_t)T + 255) / 256 * 4);
+  return l;
+}
+
 // Workspace of the tree attention: the status word; the queries folded into the latent space
 // [T, H, 512] bf16; the partition; and two partial results of 128 rows x (512 + 2) floats per CTA
 // pair.
@@ -730,6 +744,54 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
   return launch_latent_tree(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
+}
+
+size_t mla_attn_varlen_workspace_bytes(int T, int B) {
+  if (T < 1 || B < 1) return 0;
+  return varlen_layout(T, B).total;
+}
+
+mla_status mla_attn_varlen_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
+                               const uint16_t* k_nope, const uint16_t* k_pe, const uint16_t* v,
+                               const mla_varlen_strides* strides, const int32_t* cu_seqlens,
+                               int B, int T, int H, int Hkv, float softmax_scale, uint16_t* out,
+                               void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  if (!q_nope || !q_pe || !k_nope || !k_pe || !v || !cu_seqlens || !out) return MLA_ERR_NULL;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  if (B < 1 || T < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || B > (1 << 24) || T > (1 << 26) ||
+      (int64_t)T * H * 128 > kMaxElems || varlen_max_pairs(T, B) * H > 0x7fffffff)
+    return MLA_ERR_SHAPE;
+  mla_varlen_strides s = {(int64_t)H * 128, 128, (int64_t)H * 64, 64, (int64_t)Hkv * 128, 128, 64,
+                          (int64_t)Hkv * 128, 128};
+  if (strides) s = *strides;
+  const int64_t all[] = {s.q_nope_row, s.q_nope_head, s.q_pe_row, s.q_pe_head, s.k_nope_row,
+                         s.k_nope_head, s.k_pe_row, s.v_row, s.v_head};
+  for (int64_t x : all)
+    if (x < 8 || x % 8 != 0 || x > kMaxElems / 8) return MLA_ERR_SHAPE;
+  if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(k_nope) || !aligned16(k_pe) ||
+      !aligned16(v) || !aligned16(out) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0)
+    return MLA_ERR_ALIGN;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0f)) return MLA_ERR_ARG;
+  const VarlenLayout lay = varlen_layout(T, B);
+  if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
+  const mla_status st = check_device(nullptr);
+  if (st != MLA_OK) return st;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  VarlenArgs a{};
+  a.q_nope = q_nope; a.q_pe = q_pe; a.k_nope = k_nope; a.k_pe = k_pe; a.v = v;
+  a.q_nope_row = s.q_nope_row; a.q_nope_head = s.q_nope_head; a.q_pe_row = s.q_pe_row;
+  a.q_pe_head = s.q_pe_head; a.k_nope_row = s.k_nope_row; a.k_nope_head = s.k_nope_head;
+  a.k_pe_row = s.k_pe_row; a.v_row = s.v_row; a.v_head = s.v_head;
+  a.cu_seqlens = cu_seqlens; a.out = out;
+  a.status = reinterpret_cast<int*>(w);
+  a.n_pairs = reinterpret_cast<int*>(w + lay.n_pairs);
+  a.pairs = reinterpret_cast<int4*>(w + lay.pairs);
+  a.count = reinterpret_cast<int*>(w + lay.count);
+  a.B = B; a.T = T; a.H = H; a.Hkv = Hkv;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  return launch_varlen(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? MLA_OK
+                                                                                  : MLA_ERR_CUDA;
 }
 
 mla_status mla_attn_fwd(const uint16_t* q_nope, const uint16_t* q_pe, const uint16_t* k_nope,

@@ -255,6 +255,28 @@ cudaError_t launch_tree_fold(const TreeArgs& a, cudaStream_t stream);  // q_lat,
 cudaError_t launch_tree_up(const TreeArgs& a, cudaStream_t stream);    // merge, out
 cudaError_t launch_latent_tree(const TreeArgs& a, cudaStream_t stream);
 
+// Causal attention over packed prompts (see mla_attn_varlen_fwd).  Strides in elements.
+struct VarlenArgs {
+  const uint16_t* q_nope;
+  const uint16_t* q_pe;
+  const uint16_t* k_nope;
+  const uint16_t* k_pe;
+  const uint16_t* v;
+  int64_t q_nope_row, q_nope_head, q_pe_row, q_pe_head, k_nope_row, k_nope_head, k_pe_row, v_row,
+      v_head;
+  const int32_t* cu_seqlens;
+  uint16_t* out;
+  int4* pairs;   // workspace [varlen_max_pairs]: query tile pairs, most keys first
+  int* n_pairs;  // workspace [1]
+  int* count;    // workspace [ceil(T / 256)]
+  int* status;
+  int B, T, H, Hkv;
+  float scale_log2;
+};
+// Pairs of 128-row query tiles that B sequences of T rows in all can have.
+__host__ __device__ inline int64_t varlen_max_pairs(int T, int B) { return (int64_t)T / 256 + (B < T ? B : T); }
+cudaError_t launch_varlen(const VarlenArgs& a, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 

@@ -84,6 +84,12 @@ struct PrefillParams {
   int* status;
   int B, H, Tq, Tk, past_len, n_qb, n_kt;
   float scale_log2;
+  // Packed sequences only (kPacked): the query tile pairs of all sequences, most keys first, as
+  // {first row, length, tile pair, 0}, their number, and query heads per key/value head.  The
+  // maps are {128, T, heads} of the packed rows.
+  const int4* pairs;
+  const int* n_pairs;
+  int group;
 };
 
 // Barriers.  K/V tiles are counted over the CTA's whole run (g = 0, 1, ...) and
@@ -101,6 +107,10 @@ struct Bars {
   uint64_t o_done[2];   // last value mix of tile t of the unit done
   uint64_t o_free[2];   // O_t of the unit read out by the softmax warps (4 warp arrivals)
   uint64_t mma_done;
+  // Packed: V(g) of a tile that ends inside, before its end is cleared.  By tile parity like vfull:
+  // V(g + 1) is asked for once the scores of g are done, when V(g) may still be on its way; V(g + 2)
+  // only after the scores of g + 1, which follow the mix of g.
+  uint64_t v_tail[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -166,41 +176,87 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // decreasing sizes as well as dynamic assignment would, with no shared counter.
 struct Unit {
   int bh, b, r0, kvl, nt0, nt1, n;
+  int row0, kvh;  // packed: the sequence's first row; plane of the keys and values (else 0, bh)
   int js;  // key tiles skipped at the front (hidden by the 2D mask); tile j is key tile j + js
   __device__ __forceinline__ int nt(int t) const { return t ? nt1 : nt0; }
 };
 
-// Unit index of the CTA's i-th unit, or -1 past the end.
-__device__ __forceinline__ int unit_index(const PrefillParams& p, int i) {
-  const int G = gridDim.x;
-  const int64_t k = (int64_t)i * G + ((i & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x);
-  return k < (int64_t)p.B * p.H * p.n_qb ? (int)k : -1;
+// Packed: units in all (elsewhere they follow from the sizes).
+template <bool kPacked>
+__device__ __forceinline__ int64_t unit_count(const PrefillParams& p) {
+  return kPacked ? (int64_t)*p.n_pairs * p.H : 0;
 }
 
-// kv_len of a unit's sequence as stored (unclamped), or Tk without kv_len.  The only
-// global load of a unit's description: each role fetches it one unit ahead.
+// Unit index of the CTA's i-th unit, or -1 past the end.
+template <bool kPacked>
+__device__ __forceinline__ int unit_index(const PrefillParams& p, int64_t n_units, int i) {
+  const int G = gridDim.x;
+  const int64_t k = (int64_t)i * G + ((i & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x);
+  return k < (kPacked ? n_units : (int64_t)p.B * p.H * p.n_qb) ? (int)k : -1;
+}
+
+// The only global load of a unit's description, which each role fetches one unit ahead: kv_len
+// of its sequence as stored (unclamped), or Tk without kv_len; packed: its entry of the pairs.
+template <bool kPacked>
+struct UnitSource {
+  int kv;
+};
+template <>
+struct UnitSource<true> {
+  int4 pair;
+};
 __device__ __forceinline__ int unit_kv(const PrefillParams& p, int unit) {
   if (unit < 0 || !p.kv_len) return p.Tk;
   return p.kv_len[(unit % (p.B * p.H)) / p.H];
 }
+template <bool kPacked>
+__device__ __forceinline__ UnitSource<kPacked> unit_fetch(const PrefillParams& p, int unit) {
+  if constexpr (kPacked) {
+    UnitSource<true> s;
+    s.pair = unit < 0 ? make_int4(0, 0, 0, 0) : p.pairs[unit / p.H];
+    return s;
+  } else {
+    UnitSource<false> s;
+    s.kv = unit_kv(p, unit);
+    return s;
+  }
+}
 
-__device__ __forceinline__ Unit unit_make(const PrefillParams& p, int unit, int kv) {
+template <bool kPacked>
+__device__ __forceinline__ Unit unit_make(const PrefillParams& p, int unit,
+                                          const UnitSource<kPacked>& src) {
   Unit w;
-  const int BH = p.B * p.H;
-  const int qb = p.n_qb - 1 - unit / BH;
-  w.bh = unit % BH;
-  w.b = w.bh / p.H;
-  w.r0 = qb * 2 * kBM;
-  w.kvl = min(max(kv, 1), p.Tk);
+  int rows, past;  // query rows of the sequence, keys before them
+  if constexpr (kPacked) {
+    w.bh = unit % p.H;
+    w.b = 0;
+    w.kvh = w.bh / p.group;
+    w.row0 = src.pair.x;
+    w.kvl = src.pair.y;
+    w.r0 = src.pair.z * 2 * kBM;
+    rows = src.pair.y;
+    past = 0;
+  } else {
+    const int BH = p.B * p.H;
+    const int qb = p.n_qb - 1 - unit / BH;
+    w.bh = unit % BH;
+    w.b = w.bh / p.H;
+    w.kvh = w.bh;
+    w.row0 = 0;
+    w.r0 = qb * 2 * kBM;
+    w.kvl = min(max(src.kv, 1), p.Tk);
+    rows = p.Tq;
+    past = p.past_len;
+  }
   int nt[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int rt = w.r0 + t * kBM;
-    if (rt >= p.Tq) {
+    if (rt >= rows) {
       nt[t] = 0;
     } else {
-      const int qlast = min(rt + kBM - 1, p.Tq - 1);
-      const int lastkey = min(qlast + p.past_len, w.kvl - 1);
+      const int qlast = min(rt + kBM - 1, rows - 1);
+      const int lastkey = min(qlast + past, w.kvl - 1);
       nt[t] = lastkey / kBN + 1;
     }
   }
@@ -233,8 +289,10 @@ __device__ __forceinline__ void unit_skip_hidden(const PrefillParams& p, Unit& w
 }
 
 // kMasked: the 2D padding mask on keys is applied (p.key_bits); a separate instantiation so
-// the unmasked kernel carries none of its per-tile work.
-template <bool kMasked>
+// the unmasked kernel carries none of its per-tile work.  kPacked: whole prompts of different
+// lengths packed in one buffer, heads in groups over fewer key/value heads; a tile's rows past
+// its sequence's end are the next sequence's.
+template <bool kMasked, bool kPacked>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_prefill_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -247,6 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  if (kPacked) grid_dep_wait();  // the pairs are the kernel in front's
+  const int64_t n_units = unit_count<kPacked>(p);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -263,11 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->o_free[i], 4);
     }
     mbar_init(&bars->mma_done, 1);
+    if (kPacked)
+      for (int i = 0; i < 2; ++i) mbar_init(&bars->v_tail[i], 1);
     bars->abort_flag = 0;
     fence_barrier_init();
     // Out-of-range kv_len is reported once per CTA that meets it (and clamped).
-    for (int i = 0;; ++i) {
-      const int u = unit_index(p, i);
+    for (int i = 0; !kPacked; ++i) {
+      const int u = unit_index<kPacked>(p, n_units, i);
       if (u < 0) break;
       const int raw = unit_kv(p, u);
       if (raw < 1 || raw > p.Tk) {
@@ -312,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // Q_t of unit i: sQ_t is free once the previous unit's last score MMA on tile t has
       // run (one q_empty phase per unit).
-      auto load_q = [&](int i, int t, const int r0, const int ntt, const int bh) -> bool {
+      auto load_q = [&](int i, int t, const int r0, const int ntt, const int bh,
+                        const int row0) -> bool {
         if (i > 0 && !mbar_wait(&bars->q_empty[t], (i - 1) & 1, p.status, abort_flag))
           return false;
         if (ntt == 0) {
@@ -320,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         }
         mbar_arrive_expect_tx(&bars->q_full[t], 3 * kSub);
-        const int rt = r0 + t * kBM;
+        const int rt = row0 + r0 + t * kBM;
         uint8_t* dst = sQ + t * 3 * kSub;
         tma_load_3d(dst, &p.tm_qn, &bars->q_full[t], 0, rt, bh, pol_q);
         tma_load_3d(dst + kSub, &p.tm_qn, &bars->q_full[t], 64, rt, bh, pol_q);
@@ -330,21 +393,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t u = 0;   // ring sub-tiles issued over the run
       uint32_t g = 0;   // key tiles issued over the run
       int q_units = 0;  // units whose Q transactions have been posted
+      uint32_t tails[2] = {0, 0};  // packed: tiles that ended inside, by parity
       bool ok = true;
-      int kv_next = unit_kv(p, unit_index(p, 0));
+      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
       for (int i = 0; ok; ++i) {
-        const int unit = unit_index(p, i);
+        const int unit = unit_index<kPacked>(p, n_units, i);
         if (unit < 0) break;
-        Unit w = unit_make(p, unit, kv_next);
+        Unit w = unit_make<kPacked>(p, unit, next);
         unit_skip_hidden<kMasked>(p, w);
-        kv_next = unit_kv(p, unit_index(p, i + 1));  // fetched a unit ahead
-        ok = load_q(i, 0, w.r0, w.nt0, w.bh);
+        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));  // fetched a unit ahead
+        ok = load_q(i, 0, w.r0, w.nt0, w.bh, w.row0);
         q_units = i + 1;
         for (int j = 0; j < w.n && ok; ++j, ++g, u += kSubPerKv) {
           // Key tile j + js; with the fused append the tiles past the cached prefix come from
           // the new rows (row 0 of the new rows is key past_len = 128 n_pre).
           const bool from_new = p.append && j + w.js >= p.n_pre;
-          const int jt = from_new ? (j + w.js - p.n_pre) * kBN : (j + w.js) * kBN;
+          const int jt = w.row0 + (from_new ? (j + w.js - p.n_pre) * kBN : (j + w.js) * kBN);
           const CUtensorMap* m_kn = from_new ? &p.tm_kn_new : &p.tm_kn;
           const CUtensorMap* m_kr = from_new ? &p.tm_kr_new : &p.tm_kr;
           const CUtensorMap* m_v = from_new ? &p.tm_v_new : &p.tm_v;
@@ -356,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (s == 0) mbar_arrive_expect_tx(kb, 3 * kSub);
             uint8_t* dst = sRing + ((u + s) & (kSlots - 1)) * kSub;
             if (s < 2)
-              tma_load_3d_nohint(dst, m_kn, kb, 64 * s, jt, w.bh);
+              tma_load_3d_nohint(dst, m_kn, kb, 64 * s, jt, w.kvh);
             else
               tma_load_3d_nohint(dst, m_kr, kb, 0, jt, w.b);
           }
@@ -364,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Q of the second tile after the first key tile: the first score MMA needs only
           // Q_0 and K(0).
           if (j == 0) {
-            ok = load_q(i, 1, w.r0, w.nt1, w.bh);
+            ok = load_q(i, 1, w.r0, w.nt1, w.bh, w.row0);
             if (!ok) break;
           }
           // V(j): columns 0-63 go to the lower-addressed of its two slots, so one MMA with
@@ -373,9 +437,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sa = (u + 3) & (kSlots - 1), sb = (u + 4) & (kSlots - 1);
           ok = slot_free(u + 3) && slot_free(u + 4);
           if (!ok) break;
+          // A tile that ends inside lands on a barrier of its own: warp 2 clears its end first.
+          if (kPacked && (j + 1) * kBN > w.kvl) {
+            vb = &bars->v_tail[g & 1];
+            ++tails[g & 1];
+          }
           mbar_arrive_expect_tx(vb, 2 * kSub);
-          tma_load_3d_nohint(sRing + min(sa, sb) * kSub, m_v, vb, 0, jt, w.bh);
-          tma_load_3d_nohint(sRing + max(sa, sb) * kSub, m_v, vb, 64, jt, w.bh);
+          tma_load_3d_nohint(sRing + min(sa, sb) * kSub, m_v, vb, 0, jt, w.kvh);
+          tma_load_3d_nohint(sRing + max(sa, sb) * kSub, m_v, vb, 64, jt, w.kvh);
         }
       }
       // Every load this thread issued must land before shared memory is released.  Each
@@ -389,6 +458,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         drain_wait(&bars->kfull[k & 1], (k >> 1) & 1);
         drain_wait(&bars->vfull[k & 1], (k >> 1) & 1);
       }
+      if (kPacked)
+        for (int k = 0; k < 2; ++k)
+          if (tails[k] > 0) drain_wait(&bars->v_tail[k], (tails[k] - 1) & 1);
+    } else if (kPacked && warp == 2) {
+      // ================= ends of sequences =================
+      // The rows of a value tile behind its sequence's last belong to the next sequence: their
+      // weight is zero, but zero times an infinity is not, so they are cleared.
+      uint32_t u = 0, g = 0, tails[2] = {0, 0};
+      bool ok = true;
+      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
+      for (int i = 0; ok; ++i) {
+        const int unit = unit_index<kPacked>(p, n_units, i);
+        if (unit < 0) break;
+        const Unit w = unit_make<kPacked>(p, unit, next);
+        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));
+        if (w.n * kBN > w.kvl) {  // the unit's last tile
+          const uint32_t ul = u + (w.n - 1) * kSubPerKv, gl = g + w.n - 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_tail[gl & 1], tails[gl & 1] & 1,
+                                                 p.status, abort_flag));
+          if (!ok) break;
+          ++tails[gl & 1];
+          const int left = w.kvl - (w.n - 1) * kBN;
+          uint8_t* va = sRing + ((ul + 3) & (kSlots - 1)) * kSub;
+          uint8_t* vb = sRing + ((ul + 4) & (kSlots - 1)) * kSub;
+          for (int k = left * 8 + lane; k < kBN * 8; k += 32) {
+            reinterpret_cast<uint4*>(va)[k] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(vb)[k] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->vfull[gl & 1]);
+        }
+        u += w.n * kSubPerKv;
+        g += w.n;
+      }
     } else if ((warp == 2 || warp == 3) && lane == 0 && p.append) {
       // ================= cache writers (fused append) =================
       // warp 2: the key sub-tiles of every tile (kfull / kempty), warp 3: the value
@@ -401,13 +505,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool keys = warp == 2;
       uint32_t u = 0, g = 0;
       bool ok = true;
-      int kv_next = unit_kv(p, unit_index(p, 0));
+      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
       for (int i = 0; ok; ++i) {
-        const int unit = unit_index(p, i);
+        const int unit = unit_index<kPacked>(p, n_units, i);
         if (unit < 0) break;
-        Unit w = unit_make(p, unit, kv_next);
+        Unit w = unit_make<kPacked>(p, unit, next);
         unit_skip_hidden<kMasked>(p, w);
-        kv_next = unit_kv(p, unit_index(p, i + 1));
+        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));
         const int qt0 = w.r0 / kBM;  // the unit's first query tile
         for (int j = 0; j < w.n && ok; ++j, ++g, u += kSubPerKv) {
           const int kt = j + w.js;          // key tile
@@ -456,13 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;             // key tiles consumed over the run
       uint32_t stp[2] = {0, 0};   // value mixes issued per tile over the run
       bool ok = true;
-      int kv_next = unit_kv(p, unit_index(p, 0));
+      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
       for (int i = 0; ok; ++i) {
-        const int unit = unit_index(p, i);
+        const int unit = unit_index<kPacked>(p, n_units, i);
         if (unit < 0) break;
-        Unit w = unit_make(p, unit, kv_next);
+        Unit w = unit_make<kPacked>(p, unit, next);
         unit_skip_hidden<kMasked>(p, w);
-        kv_next = unit_kv(p, unit_index(p, i + 1));  // fetched a unit ahead
+        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));  // fetched a unit ahead
         for (int j = 0; j <= w.n && ok; ++j) {
           const uint32_t gk = g + (uint32_t)j;           // key tile j of this unit
           const uint32_t uk = gk * kSubPerKv;            // its sub-tiles: uk .. uk+2
@@ -577,16 +681,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = p.scale_log2;
     uint32_t st = 0;  // score steps of this tile over the run
     bool ok = true;
-    int kv_next = unit_kv(p, unit_index(p, 0));
+    auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
     for (int i = 0; ok; ++i) {
-      const int unit = unit_index(p, i);
+      const int unit = unit_index<kPacked>(p, n_units, i);
       if (unit < 0) break;
-      Unit w = unit_make(p, unit, kv_next);
+      Unit w = unit_make<kPacked>(p, unit, next);
       unit_skip_hidden<kMasked>(p, w);
-      kv_next = unit_kv(p, unit_index(p, i + 1));  // fetched a unit ahead
+      next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));  // fetched a unit ahead
       const int ntt = w.nt(t);
       const int qi = w.r0 + t * kBM + tw;  // query row within the sequence
-      const int limit = min(qi + p.past_len + 1, w.kvl);  // keys [0, limit) are visible
+      const int limit = min(qi + (kPacked ? 0 : p.past_len) + 1, w.kvl);  // keys [0, limit) are visible
       float m = -INFINITY;
       float l = 0.f;
       for (int j = 0; j < ntt; ++j, ++st) {
@@ -726,8 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // l = 0 only when the 2D padding mask hides every key of the row; that row is
       // rewritten afterwards as the mean of all value rows.
       const float inv = l > 0.f ? 1.0f / l : 0.f;
-      if (qi < p.Tq) {
-        uint16_t* row = p.out + ((size_t)w.bh * p.Tq + qi) * 128;
+      if (qi < (kPacked ? w.kvl : p.Tq)) {
+        uint16_t* row = kPacked ? p.out + ((size_t)(w.row0 + qi) * p.H + w.bh) * 128
+                                : p.out + ((size_t)w.bh * p.Tq + qi) * 128;
         auto pk = [&](int c, int e) {
           return pack_bf16x2(__uint_as_float(o[c][e]) * inv, __uint_as_float(o[c][e + 1]) * inv);
         };
@@ -973,10 +1078,10 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(mla_prefill_kernel<false>,
+    e = cudaFuncSetAttribute(mla_prefill_kernel<false, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(mla_prefill_kernel<true>,
+    e = cudaFuncSetAttribute(mla_prefill_kernel<true, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_release);
@@ -985,9 +1090,177 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   const int sms = device_sm_count();
   const uint64_t grid = std::min<uint64_t>(units, (uint64_t)(sms > 0 ? sms : 152));
   if (p.key_bits)
-    mla_prefill_kernel<true><<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(p);
+    mla_prefill_kernel<true, false><<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(p);
   else
-    mla_prefill_kernel<false><<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(p);
+    mla_prefill_kernel<false, false><<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// ---- packed sequences ------------------------------------------------------------------
+namespace {
+
+// The query tile pairs of all sequences, those with the most keys first (pair q of a sequence
+// sees 2 q + 2 key tiles): a counting sort over q by one block.  Pairs of one q come in any
+// order, which changes when a unit runs and nothing else.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) packed_pairs_kernel(const VarlenArgs a) {
+  grid_dep_launch();
+  __shared__ int s_warp[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int classes = (a.T + 2 * kBM - 1) / (2 * kBM);
+  for (int q = tid; q < classes; q += kPlanThreads) a.count[q] = 0;
+  __syncthreads();
+  const auto seq = [&](int b, int& row0) {  // offsets clamped to the buffer
+    const int c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1];
+    row0 = min(max(c0, 0), a.T);
+    const int n = min(max(c1, row0), a.T) - row0;
+    if (row0 != c0 || row0 + n != c1) set_status(a.status, MLA_ERR_KVLEN);
+    return n;
+  };
+  // count[q] = sequences whose last pair is q
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    int row0;
+    const int n = seq(b, row0);
+    if (n > 0) atomicAdd(&a.count[(n - 1) / (2 * kBM)], 1);
+  }
+  __syncthreads();
+  // Sequences that have a pair q: the counts from q on; places: the pairs of all higher q.  Both
+  // are sums from the top, a block scan per 1024 classes.
+  int have = 0, place = 0;  // totals above this chunk
+  for (int top = classes; top > 0; top -= kPlanThreads) {
+    const int q = top - 1 - tid;
+    const int own = q >= 0 ? a.count[q] : 0;
+    const auto scan = [&](int x, int& total) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_warp[warp] = x;
+      __syncthreads();
+      int before = 0;
+      total = 0;
+      for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+      }
+      return x + before;
+    };
+    int t1, t2;
+    const int from = scan(own, t1) + have;
+    const int seqs = q >= 0 ? from : 0;
+    const int upto = scan(seqs, t2) + place;  // pairs of q and above
+    if (q >= 0) a.count[q] = upto - seqs;     // the first place of class q
+    have += t1;
+    place += t2;
+  }
+  // Offsets that fall can make sequences overlap, and more pairs than there is room for.
+  const int most = (int)min(varlen_max_pairs(a.T, a.B), (int64_t)0x7fffffff);
+  if (tid == 0) *a.n_pairs = min(place, most);
+  __syncthreads();
+  // A warp per sequence, lanes over its pairs.
+  for (int b = warp; b < a.B; b += kPlanThreads / 32) {
+    int row0;
+    const int n = seq(b, row0);
+    for (int q = lane; q * 2 * kBM < n; q += 32) {
+      const int at = atomicAdd(&a.count[q], 1);
+      if (at < most) a.pairs[at] = make_int4(row0, n, q, 0);
+    }
+  }
+}
+
+struct PackedKey {
+  const void* ptr[5];
+  int64_t stride[9];
+  int T, H, Hkv;
+  bool operator==(const PackedKey& o) const {
+    for (int i = 0; i < 5; ++i)
+      if (ptr[i] != o.ptr[i]) return false;
+    for (int i = 0; i < 9; ++i)
+      if (stride[i] != o.stride[i]) return false;
+    return T == o.T && H == o.H && Hkv == o.Hkv;
+  }
+};
+struct PackedEntry {
+  PackedKey key;
+  CUtensorMap maps[5];
+  bool valid;
+};
+PackedEntry g_packed_cache[kMapCacheSize];
+int g_packed_next = 0;
+
+bool packed_maps(const VarlenArgs& a, PrefillParams* p) {
+  const PackedKey key = {{a.q_nope, a.q_pe, a.k_nope, a.k_pe, a.v},
+                         {a.q_nope_row, a.q_nope_head, a.q_pe_row, a.q_pe_head, a.k_nope_row,
+                          a.k_nope_head, a.k_pe_row, a.v_row, a.v_head},
+                         a.T, a.H, a.Hkv};
+  CUtensorMap* dst[5] = {&p->tm_qn, &p->tm_qr, &p->tm_kn, &p->tm_kr, &p->tm_v};
+  std::lock_guard<std::mutex> lk(g_map_mu);
+  for (const PackedEntry& e : g_packed_cache)
+    if (e.valid && e.key == key) {
+      for (int k = 0; k < 5; ++k) *dst[k] = e.maps[k];
+      return true;
+    }
+  const int heads[5] = {a.H, a.H, a.Hkv, 1, a.Hkv};
+  const uint64_t width[5] = {128, 64, 128, 64, 128};
+  const int64_t row[5] = {a.q_nope_row, a.q_pe_row, a.k_nope_row, a.k_pe_row, a.v_row};
+  const int64_t head[5] = {a.q_nope_head, a.q_pe_head, a.k_nope_head, 64, a.v_head};
+  const uint32_t box[3] = {64, 128, 1};
+  for (int k = 0; k < 5; ++k) {
+    const uint64_t dims[3] = {width[k], (uint64_t)a.T, (uint64_t)heads[k]};
+    const uint64_t strides[2] = {(uint64_t)row[k] * 2, (uint64_t)head[k] * 2};
+    if (!encode_bf16_tiled(dst[k], key.ptr[k], 3, dims, strides, box)) return false;
+  }
+  PackedEntry& e = g_packed_cache[g_packed_next];
+  g_packed_next = (g_packed_next + 1) % kMapCacheSize;
+  e.key = key;
+  for (int k = 0; k < 5; ++k) e.maps[k] = *dst[k];
+  e.valid = true;
+  return true;
+}
+
+}  // namespace
+
+cudaError_t launch_varlen(const VarlenArgs& a, cudaStream_t stream) {
+  PrefillParams p{};
+  if (!packed_maps(a, &p)) return cudaErrorInvalidValue;
+  p.pairs = a.pairs;
+  p.n_pairs = a.n_pairs;
+  p.group = a.H / a.Hkv;
+  p.out = a.out;
+  p.status = a.status;
+  p.B = 1;
+  p.H = a.H;
+  p.scale_log2 = a.scale_log2;
+  static std::atomic<uint64_t> attr_done{0};  // bit per device: smem attribute set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(mla_prefill_kernel<false, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_release);
+  }
+  packed_pairs_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int sms = device_sm_count();
+  const int64_t units = varlen_max_pairs(a.T, a.B) * a.H;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, sms > 0 ? sms : 152));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  e = cudaLaunchKernelEx(&cfg, mla_prefill_kernel<false, true>, p);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

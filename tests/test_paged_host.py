@@ -166,3 +166,47 @@ def test_tree_refuses_alignment_and_small_workspaces(lib, base):
     a["workspace_bytes"] = 256
     want = (S.ERR_WORKSPACE,) if torch.cuda.is_available() else _no_device()
     assert lib.mla_latent_tree_fwd(*[a[n] for n in TREE]) in want
+
+
+VARLEN = ["q_nope", "q_pe", "k_nope", "k_pe", "v", "strides", "cu_seqlens", "B", "T", "H", "Hkv",
+          "scale", "out", "workspace", "workspace_bytes", "stream"]
+
+
+def _varlen_args(base, lib, strides=None):
+    a = {n: base + 256 * i for i, n in enumerate(VARLEN)}
+    a.update(B=2, T=3, H=4, Hkv=2, scale=0.1, stream=None, strides=None,
+             workspace_bytes=lib.mla_attn_varlen_workspace_bytes(3, 2))
+    if strides is not None:
+        a["strides"] = ctypes.addressof((ctypes.c_int64 * 9)(*strides))
+    return a
+
+
+@pytest.mark.parametrize("change,want", [
+    ({k: None}, S.ERR_NULL) for k in ("q_nope", "q_pe", "k_nope", "k_pe", "v", "cu_seqlens", "out")
+] + [
+    ({"workspace": None}, S.ERR_WORKSPACE), ({"workspace_bytes": 256}, S.ERR_WORKSPACE),
+    ({"B": 0}, S.ERR_SHAPE), ({"T": 0}, S.ERR_SHAPE), ({"H": 0}, S.ERR_SHAPE),
+    ({"Hkv": 0}, S.ERR_SHAPE), ({"Hkv": 3}, S.ERR_SHAPE), ({"Hkv": 8}, S.ERR_SHAPE),
+    ({"T": 1 << 27}, S.ERR_SHAPE), ({"scale": -1.0}, S.ERR_ARG),
+])
+def test_varlen_refuses(lib, base, change, want):
+    a = _varlen_args(base, lib)
+    a.update(change)
+    assert lib.mla_attn_varlen_fwd(*[a[n] for n in VARLEN]) == want
+
+
+def test_varlen_refuses_strides_and_alignment(lib, base):
+    good = [4 * 192, 192, 4 * 192, 192, 512, 256, 64, 512, 256]
+    for i in range(9):
+        for bad in (0, 4, -8, good[i] + 1):
+            keep = (ctypes.c_int64 * 9)(*(good[:i] + [bad] + good[i + 1:]))
+            a = _varlen_args(base, lib)
+            a["strides"] = ctypes.addressof(keep)
+            assert lib.mla_attn_varlen_fwd(*[a[n] for n in VARLEN]) == S.ERR_SHAPE
+    for name in ("q_nope", "q_pe", "k_nope", "k_pe", "v", "out", "workspace"):
+        a = _varlen_args(base, lib)
+        a[name] += 8
+        assert lib.mla_attn_varlen_fwd(*[a[n] for n in VARLEN]) == S.ERR_ALIGN
+    if not torch.cuda.is_available():
+        a = _varlen_args(base, lib)
+        assert lib.mla_attn_varlen_fwd(*[a[n] for n in VARLEN]) in _no_device()
