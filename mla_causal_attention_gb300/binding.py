@@ -78,6 +78,8 @@ EXPORTED = ("mla_attn_workspace_bytes", "mla_attn_fwd", "mla_attn_fwd_ex",
 def library():
     """Load libmla_attn.so (built in-tree by build.py); raise if it is not there."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -214,20 +216,33 @@ def _enqueue(name, dev, stream, workspace, ws_bytes, args):
     """Calls entry point `name` with args, then workspace, its size and the stream, with `dev`
     current.  For calls of a few microseconds the host side counts: no device context unless
     the device changes, and the stream's address without a Stream object."""
-    fn = getattr(library(), name)
-    index = dev.index if dev.index is not None else torch.cuda.current_device()
-    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    fn = getattr(_lib or library(), name)
+    index = dev.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     ws = workspace or _default_workspace(dev)
     buf = ws.buf
     if buf is None or buf.numel() < ws_bytes:
         buf = ws.get(ws_bytes, stream=stream or torch.cuda.current_stream(dev))
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, buf.data_ptr(), buf.numel(), s)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, buf.data_ptr(), buf.numel(), s)
     if rc != 0:
         raise MlaAttnError(rc, name + ": ")
+
+
+def _check_all(dev, dtype, named):
+    """_check of several tensors of one type, (name, tensor, shape) each."""
+    index = dev.index
+    for name, t, shape in named:
+        try:
+            if (t.dtype is dtype and t.get_device() == index and t.shape == shape
+                    and t.is_contiguous()):
+                continue
+        except AttributeError:
+            pass
+        _check(t, name, dtype, shape, dev)
 
 
 class PreparedCall:
@@ -466,35 +481,29 @@ def mla_paged_plan(ctx_len, new_len, block_table, free_pages, free_head, page_si
     if dev.type != "cuda":
         raise ValueError("inputs must be CUDA tensors")
     B, T, i32 = ctx_len.shape[0], int(num_tokens), torch.int32
-    _check(ctx_len, "ctx_len", i32, (B,), dev)
-    _check(new_len, "new_len", i32, (B,), dev)
-    _check(block_table, "block_table", i32, (B, block_table.shape[-1]), dev)
-    _check(free_pages, "free_pages", i32, (free_pages.shape[0],), dev)
-    _check(free_head, "free_head", i32, (1,), dev)
-    if parent is not None:
-        _check(parent, "parent", i32, (T,), dev)
+    max_pages, n_free = block_table.shape[-1], free_pages.shape[0]
     if out is None:
         new = lambda n, dt=i32: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
         out = PagedPlan(new(B + 1), new(B), new(T), new(T), new(1),
                         None if parent is None else new(T, torch.int64))
     elif not isinstance(out, PagedPlan):
         out = PagedPlan(*out)
-    _check(out.cu_q, "cu_q", i32, (B + 1,), dev)
-    _check(out.kv_len, "kv_len", i32, (B,), dev)
-    _check(out.slots, "slots", i32, (T,), dev)
-    _check(out.positions, "positions", i32, (T,), dev)
-    _check(out.free_next, "free_next", i32, (1,), dev)
-    if parent is None:
-        if out.draft_mask is not None:
-            raise ValueError("draft_mask is listed with parent only")
-    else:
-        _check(out.draft_mask, "draft_mask", torch.int64, (T,), dev)
+    cu_q, kv_len, slots, positions, free_next, draft_mask = out
+    _check_all(dev, i32, (
+        ("ctx_len", ctx_len, (B,)), ("new_len", new_len, (B,)),
+        ("block_table", block_table, (B, max_pages)), ("free_pages", free_pages, (n_free,)),
+        ("free_head", free_head, (1,)), ("cu_q", cu_q, (B + 1,)), ("kv_len", kv_len, (B,)),
+        ("slots", slots, (T,)), ("positions", positions, (T,)), ("free_next", free_next, (1,))))
+    if parent is not None:
+        _check(parent, "parent", i32, (T,), dev)
+        _check(draft_mask, "draft_mask", torch.int64, (T,), dev)
+    elif draft_mask is not None:
+        raise ValueError("draft_mask is listed with parent only")
     _enqueue("mla_paged_plan", dev, stream, workspace, 256, (
-        ctx_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(),
-        block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(),
-        int(page_size), int(num_pages), _addr(parent), T, out.cu_q.data_ptr(),
-        out.kv_len.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
-        _addr(out.draft_mask), out.free_next.data_ptr()))
+        ctx_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(), max_pages,
+        free_pages.data_ptr(), n_free, free_head.data_ptr(), int(page_size), int(num_pages),
+        _addr(parent), T, cu_q.data_ptr(), kv_len.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), _addr(draft_mask), free_next.data_ptr()))
     return out
 
 
@@ -511,11 +520,11 @@ def mla_latent_append(c_kv_new, k_pe_new, slots, c_pages, pe_pages, positions=No
         raise ValueError("inputs must be CUDA tensors")
     T, bf, i32 = c_kv_new.shape[0], torch.bfloat16, torch.int32
     num_pages, page_size = c_pages.shape[:2]
-    _check(c_kv_new, "c_kv_new", bf, (T, 512), dev)
-    _check(k_pe_new, "k_pe_new", bf, (T, 64), dev)
+    _check_all(dev, bf, (
+        ("c_kv_new", c_kv_new, (T, 512)), ("k_pe_new", k_pe_new, (T, 64)),
+        ("c_pages", c_pages, (num_pages, page_size, 512)),
+        ("pe_pages", pe_pages, (num_pages, page_size, 64))))
     _check(slots, "slots", i32, (T,), dev)
-    _check(c_pages, "c_pages", bf, (num_pages, page_size, 512), dev)
-    _check(pe_pages, "pe_pages", bf, (num_pages, page_size, 64), dev)
     rows, H = 0, 0
     if rope_table is not None:
         rows = rope_table.shape[0]
@@ -555,20 +564,17 @@ def mla_latent_tree_fwd(q_nope, q_pe, c_pages, pe_pages, block_table, kv_len, cu
     num_pages, page_size = c_pages.shape[:2]
     B, max_pages = block_table.shape
     bf, i32 = torch.bfloat16, torch.int32
-    _check(q_nope, "q_nope", bf, (T, H, 128), dev)
-    _check(q_pe, "q_pe", bf, (T, H, 64), dev)
-    _check(c_pages, "c_pages", bf, (num_pages, page_size, 512), dev)
-    _check(pe_pages, "pe_pages", bf, (num_pages, page_size, 64), dev)
-    _check(block_table, "block_table", i32, (B, max_pages), dev)
-    _check(kv_len, "kv_len", i32, (B,), dev)
-    _check(cu_q, "cu_q", i32, (B + 1,), dev)
-    if draft_mask is not None:
-        _check(draft_mask, "draft_mask", torch.int64, (T,), dev)
-    _check(w_kvb, "w_kvb", bf, (H * 256, 512), dev)
     if out is None:
         out = torch.empty((T, H, 128), dtype=bf, device=dev)
-    else:
-        _check(out, "out", bf, (T, H, 128), dev)
+    _check_all(dev, bf, (
+        ("q_nope", q_nope, (T, H, 128)), ("q_pe", q_pe, (T, H, 64)),
+        ("c_pages", c_pages, (num_pages, page_size, 512)),
+        ("pe_pages", pe_pages, (num_pages, page_size, 64)),
+        ("w_kvb", w_kvb, (H * 256, 512)), ("out", out, (T, H, 128))))
+    _check_all(dev, i32, (("block_table", block_table, (B, max_pages)),
+                          ("kv_len", kv_len, (B,)), ("cu_q", cu_q, (B + 1,))))
+    if draft_mask is not None:
+        _check(draft_mask, "draft_mask", torch.int64, (T,), dev)
     nbytes = library().mla_latent_tree_workspace_bytes(T, H, B)
     _enqueue("mla_latent_tree_fwd", dev, stream, workspace, nbytes, (
         q_nope.data_ptr(), q_pe.data_ptr(), c_pages.data_ptr(), pe_pages.data_ptr(), num_pages,

@@ -116,7 +116,7 @@ VarlenLayout varlen_layout(int T, int B) {
 // [T, H, 512] bf16; the partition; and two partial results of 128 rows x (512 + 2) floats per CTA
 // pair.
 struct TreeLayout {
-  size_t q_lat, tile0, unit0, range0, part_ml, part_acc, total;
+  size_t q_lat, tile0, unit0, range0, first, part_note, part_ml, part_acc, total;
   int pairs;
 };
 TreeLayout tree_layout(int T, int H, int B, int sms) {
@@ -126,7 +126,9 @@ TreeLayout tree_layout(int T, int H, int B, int sms) {
   l.tile0 = l.q_lat + r256((size_t)T * H * 512 * 2);
   l.unit0 = l.tile0 + r256((size_t)(B + 1) * 8);
   l.range0 = l.unit0 + r256((size_t)(B + 1) * 8);
-  l.part_ml = l.range0 + r256((size_t)(l.pairs + 2) * 8);
+  l.first = l.range0 + r256((size_t)(l.pairs + 2) * 8);
+  l.part_note = l.first + r256((size_t)l.pairs * 48);
+  l.part_ml = l.part_note + r256((size_t)l.pairs * 32);
   l.part_acc = l.part_ml + (size_t)2 * l.pairs * 128 * 2 * 4;
   l.total = l.part_acc + (size_t)2 * l.pairs * 128 * 512 * 4;
   return l;
@@ -736,6 +738,8 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
   a.tile0 = reinterpret_cast<int64_t*>(w + lay.tile0);
   a.unit0 = reinterpret_cast<int64_t*>(w + lay.unit0);
   a.range0 = reinterpret_cast<int64_t*>(w + lay.range0);
+  a.first = reinterpret_cast<int4*>(w + lay.first);
+  a.part_note = reinterpret_cast<int4*>(w + lay.part_note);
   a.part_ml = reinterpret_cast<float*>(w + lay.part_ml);
   a.part_acc = reinterpret_cast<float*>(w + lay.part_acc);
   a.num_pages = num_pages; a.page_shift = page_shift(page_size); a.max_pages = max_pages;

@@ -43,6 +43,10 @@ __device__ __forceinline__ PlanSeq plan_seq(const PagedPlanArgs& a, int b, bool*
   return s;
 }
 
+__device__ __forceinline__ int pages_of(const PagedPlanArgs& a, int tokens) {
+  return (int)(((int64_t)tokens + (1 << a.page_shift) - 1) >> a.page_shift);
+}
+
 // The k-th page a step takes, or -1 where the free list has run out or holds no page.
 __device__ __forceinline__ int plan_page(const PagedPlanArgs& a, int64_t head, int64_t k) {
   const int64_t at = head + k;
@@ -54,6 +58,8 @@ __device__ __forceinline__ int plan_page(const PagedPlanArgs& a, int64_t head, i
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPlanArgs a) {
   __shared__ int64_t s_tok[kPlanChunk + 1];  // first token of each sequence of the chunk
   __shared__ int64_t s_pg[kPlanChunk + 1];   // first page taken
+  __shared__ int s_ctx[kPlanChunk], s_kv[kPlanChunk];
+  __shared__ int s_par[64 + kPlanThreads * kPlanTok];  // parents of a turn's tokens, and before
   __shared__ int64_t s_warp[2][kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t head0 = a.free_head[0];
@@ -80,6 +86,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
     }
     const int nb = min(kPlanChunk, a.B - b0);
     int64_t my_tok[kPlanPer], my_pg[kPlanPer], sum_tok = 0, sum_pg = 0;
+    int ctx_of[kPlanPer] = {}, kv_of[kPlanPer] = {};
     bool bad = false;
 #pragma unroll
     for (int k = 0; k < kPlanPer; ++k) {
@@ -90,6 +97,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
         const PlanSeq s = plan_seq(a, b0 + i, &bad);
         sum_tok += s.n;
         sum_pg += s.take;
+        ctx_of[k] = (int)s.ctx;
+        kv_of[k] = (int)s.kv;
         if (a.parent && s.n > 64 && blockIdx.x == 0) set_status(a.status, MLA_ERR_TREE);
       }
     }
@@ -124,6 +133,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
     for (int k = 0; k < kPlanPer; ++k) {
       s_tok[tid * kPlanPer + k] = base_tok + inc_tok - sum_tok + my_tok[k];
       s_pg[tid * kPlanPer + k] = base_pg + inc_pg - sum_pg + my_pg[k];
+      s_ctx[tid * kPlanPer + k] = ctx_of[k];
+      s_kv[tid * kPlanPer + k] = kv_of[k];
     }
     if (tid == 0) s_tok[kPlanChunk] = tok;
     __syncthreads();
@@ -134,15 +145,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
       const int first = a.B <= kPlanChunk ? blockIdx.x * (kPlanThreads / 32) + warp : warp;
       const int step = (a.B <= kPlanChunk ? gridDim.x : 1) * (kPlanThreads / 32);
       for (int i = first; i < nb; i += step) {
-        bool ignore = false;
-        const PlanSeq s = plan_seq(a, b0 + i, &ignore);
+        const int have = pages_of(a, s_ctx[i]), take = pages_of(a, s_kv[i]) - have;
         if (lane == 0) {
           a.cu_q[b0 + i] = (int)min(s_tok[i], (int64_t)a.T);
-          a.kv_len[b0 + i] = (int)s.kv;
+          a.kv_len[b0 + i] = s_kv[i];
         }
-        int32_t* row = a.block_table + (int64_t)(b0 + i) * a.max_pages + s.have;
+        int32_t* row = a.block_table + (int64_t)(b0 + i) * a.max_pages + have;
         bool none = false;
-        for (int k = lane; k < s.take; k += 32) {
+        for (int k = lane; k < take; k += 32) {
           const int page = plan_page(a, head, s_pg[i] + k);
           row[k] = page;
           none |= page < 0;
@@ -153,14 +163,24 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
 
     // Per token: the sequences of this chunk that reach into [t0, t1).
     const int64_t lo = max(t0, s_tok[0] / kPlanTok * kPlanTok), hi = min(t1, tok);
-    for (int64_t t = lo + (int64_t)tid * kPlanTok; t < hi; t += (int64_t)kPlanThreads * kPlanTok) {
+    for (int64_t turn = lo; turn < hi; turn += kPlanThreads * kPlanTok) {
+      if (a.parent) {  // a path lies within the 64 tokens before its end
+        __syncthreads();
+        for (int i = tid; i < 64 + kPlanThreads * kPlanTok; i += kPlanThreads) {
+          const int64_t at = turn - 64 + i;
+          s_par[i] = at >= 0 && at < hi ? a.parent[at] : -1;
+        }
+        __syncthreads();
+      }
+      const int64_t t = turn + tid * kPlanTok;
+      if (t >= hi) continue;
       int l = 0, r = nb;  // the last sequence of the chunk that starts at or before the token
       const int64_t tf = max(t, s_tok[0]);
       while (r - l > 1) {
         const int m = (l + r) >> 1;
         if (s_tok[m] <= tf) l = m; else r = m;
       }
-      PlanSeq s;
+      int ctx = 0, kv = 0, have = 0;
       int64_t end = -1;   // first token past sequence l
       int page = -1, page_k = -1;
       int slot[kPlanTok], pos[kPlanTok];
@@ -179,19 +199,20 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
           if (end >= 0) ++l;
           end = l + 1 < nb ? s_tok[l + 1] : tok;
           if (te < end) {
-            bool ignore = false;
-            s = plan_seq(a, b0 + l, &ignore);
+            ctx = s_ctx[l];
+            kv = s_kv[l];
+            have = pages_of(a, ctx);
             page_k = -1;
           }
         }
         const int64_t i = te - s_tok[l];
-        const int64_t p = s.ctx + i;
-        if (p < s.kv) {
+        const int64_t p = ctx + i;
+        if (p < kv) {
           const int k = (int)(p >> a.page_shift);
           if (k != page_k) {
             page_k = k;
-            if (k >= s.have) {
-              page = plan_page(a, head, s_pg[l] + k - s.have);
+            if (k >= have) {
+              page = plan_page(a, head, s_pg[l] + k - have);
             } else {
               page = a.block_table[(int64_t)(b0 + l) * a.max_pages + k];
               if (page < 0 || page >= a.num_pages) {
@@ -205,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
         int64_t depth = i;
         if (a.parent) {
           // Up the path to the root; indexes fall at every step, so the walk ends.
-          const int32_t* par = a.parent + s_tok[l];
+          const int first = (int)(s_tok[l] - (turn - 64));  // >= 1 where i < 64
           uint64_t m = 0;
           depth = -1;
           int at = (int)i;
@@ -213,7 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
             for (;;) {
               m |= 1ull << at;
               ++depth;
-              const int up = par[at];
+              const int up = s_par[first + at];
               if (up < 0 || up >= at) {
                 bad_tree |= up != -1;
                 break;
@@ -225,7 +246,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
           }
           mask[e] = (int64_t)m;
         }
-        pos[e] = (int)min(s.ctx + depth, last_pos);
+        pos[e] = (int)min(ctx + depth, last_pos);
       }
       if (whole) {
         *reinterpret_cast<int4*>(a.slots + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
@@ -322,12 +343,12 @@ __global__ void __launch_bounds__(kAppThreads) latent_append_kernel(const Latent
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
-  // Enough blocks for one group of tokens per thread, or one warp per sequence, within two
-  // blocks per SM.
+  // Enough blocks for one group of tokens per thread, or one warp per sequence, within four
+  // blocks per SM (each repeats the scan).
   const int sms = device_sm_count();
   const int64_t by_tok = ((int64_t)a.T + kPlanThreads * kPlanTok - 1) / (kPlanThreads * kPlanTok);
   const int64_t by_seq = ((int64_t)std::min(a.B, kPlanChunk) + 7) / 8;
-  const int64_t grid = std::min<int64_t>(std::max(by_tok, by_seq), 2 * (sms > 0 ? sms : 152));
+  const int64_t grid = std::min<int64_t>(std::max(by_tok, by_seq), 4 * (sms > 0 ? sms : 152));
   paged_plan_kernel<<<(unsigned)grid, kPlanThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -59,6 +59,7 @@ constexpr int kOffRed = kOffP + 2 * kSubQ;   // [2 tile parities][2 halves][64 r
 constexpr int kOffBar = kOffRed + 1024;
 constexpr int kSmem = kOffBar + 256 + 1024;  // + barriers + alignment slack
 static_assert(kSmem <= 232448, "shared memory per block");
+constexpr int kAhead = 2;        // tiles between a tile's L2 prefetch and its loads
 constexpr uint32_t kColO = 128;
 constexpr float kRescale = 8.0f;  // log2 units: the mix is rescaled when the maximum grows by more
 
@@ -67,6 +68,8 @@ struct TreeParams {
   CUtensorMap tm_qr;  // q_pe  {64,  T*H}
   CUtensorMap tm_c;   // c_pages  {512, slots}, boxes {64, min(page, 64)}
   CUtensorMap tm_kr;  // pe_pages {64,  slots}
+  CUtensorMap tm_o;   // q_lat again, boxes {64, 32}: the mixes of whole units
+  CUtensorMap tm_pa;  // part_acc {512, rows} fp32, boxes {32, 32}
   TreeArgs a;
 };
 
@@ -195,11 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   tc::fence_after_sync();
   const uint32_t tbase = bars->tmem_base;
   grid_dep_wait();  // the partition and the folded queries
-  SegWalk walk(a, pair_id, lane);
+  SegWalk walk;
   Seg g, after;
-  bool more = walk.next(a, g);
+  bool more = walk.start(a, pair_id, lane, g);
   const int box = min(1 << a.page_shift, 64);  // keys per TMA box
   const int boxes = 64 / box;                  // boxes per 64 keys
+  const int pool = a.num_pages << a.page_shift;
 
   if (warp == 0) {
     // ================= keys and queries =================
@@ -214,6 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                    ? key_row(a, g.b, g.s.kv, tile * kTile + 64 * rank + lane * box) : 0;
       };
       int rows_next = look(g.k0);
+      // Where a sequence is a single unit its keys come from HBM, and are asked into L2 two tiles
+      // before their loads (ragged decode batch 69.5 -> 65.7 us; 4 tiles 73, 8 tiles 83).  Where
+      // several units share them most loads hit L2 anyway, and asking costs more than it
+      // brings (64-token trees 1.20 -> 1.30 ms), even if only one of the units asks.
+      const bool alone = g.s.n * a.H <= kRows;
+      int ahead = alone && g.k0 + kAhead < g.k1 ? look(g.k0 + kAhead) : 0;
       if (ns > 0) ok = mbar_wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -256,6 +266,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               }
           }
           __syncwarp();
+        }
+        if (alone && k + kAhead < g.k1) {
+          if (lane < boxes_of(g.s.kv - (k + kAhead) * kTile - 64 * rank, box) && ahead < pool) {
+            bulk_prefetch_l2(a.c_pages + (size_t)ahead * kLD, box * kLD * 2);
+            bulk_prefetch_l2(a.pe_pages + (size_t)ahead * 64, box * 128);
+          }
+          if (k + 1 + kAhead < g.k1) ahead = look(k + 1 + kAhead);
         }
       }
     }
@@ -412,6 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t p_ready = tp::even_addr(&bars->p_ready);
     const uint32_t o_free = tp::even_addr(&bars->o_free);
     const float sl2 = a.scale_log2;
+    // What a slot holds, for the merge: first row, rows, whether it is its unit's first segment
+    // and its last.  One thread clears the pair's two notes and fills in those of its segments.
+    const bool notes = rank == 0 && threadIdx.x == 128;
+    if (notes) {
+      a.part_note[2 * pair_id] = make_int4(0, 0, 0, 0);
+      a.part_note[2 * pair_id + 1] = make_int4(0, 0, 0, 0);
+    }
     uint32_t t = 0;
     bool ok = true, gone = false;  // a wait of this thread's gave up; all four warps leave
     for (; more; g = after) {
@@ -527,25 +551,40 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       l += rl[(half ^ 1) * 64 + r];
       const bool whole = g.slot < 0;
       const float f = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      if (!whole && notes)
+        a.part_note[g.slot] = make_int4(g.s.q0 * a.H + g.m * kRows,
+                                        min(kRows, g.s.n * a.H - g.m * kRows), g.k0 == 0,
+                                        g.k1 == seq_tiles(g.s));
       const size_t slot_row = (size_t)(whole ? 0 : g.slot) * kRows + 64 * rank;
       if (!whole && half == 0)
         *reinterpret_cast<float2*>(a.part_ml + (slot_row + r) * 2) = make_float2(m, l);
-      // 32 columns at a time through this warp's quarter of the weights' buffer (free now), so
-      // that eight lanes write a row's 128 (four lanes its 64) bytes: a lane writing its own row
-      // touches 32 lines per instruction, and took 9000 cycles per segment.
+      // 128 bytes per row at a time (32 fp32 columns, or 64 as bf16) through this warp's quarter of
+      // the weights' buffer, free now, and a tensor store: a lane writing its own row touches
+      // 32 lines per instruction, which took 9000 cycles per segment.  Rows of a partial slot
+      // that do not exist are written too (nothing reads them); those of a whole unit would be
+      // another sequence's, so the last rows of a sequence are written by hand.
       uint8_t* stage = sP + q4 * 4096;
       const int row0 = g.m * kRows + 64 * rank + (q4 & 1) * 32;  // the warp's first row
       const int have = min(max(g.s.n * a.H - row0, 0), 32);      // rows that exist
+      uint32_t nx[32];
+      tc::tmem_ld32(tbase + lane_off + kColO, nx);
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint32_t o[32];
-        tc::tmem_ld32(tbase + lane_off + kColO + c * 32, o);
         tc::tmem_wait_ld();
-        pin<32>(o);
-        if (c == 7) {  // the mix is out of TMEM: the next segment's may be written
+        pin<32>(nx);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = nx[e];
+        if (c < 7) {
+          tc::tmem_ld32(tbase + lane_off + kColO + (c + 1) * 32, nx);
+        } else {  // the mix is out of TMEM: the next segment's may be written
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tp::arrive(o_free);
+        }
+        if (!whole || (c & 1) == 0) {  // the store before has read the stage
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
         }
         const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
         if (whole) {
@@ -556,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int k = 0; k < 4; ++k)
               w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * f,
                                  __uint_as_float(o[8 * e + 2 * k + 1]) * f);
-            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+            *reinterpret_cast<uint4*>(stage + lane * 128 +
+                                      (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
@@ -565,34 +605,34 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
                 make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
+        if (whole && (c & 1) == 0) continue;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (whole) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2), e = lane & 3;
-            const uint4 w =
-                *reinterpret_cast<const uint4*>(stage + rr * 64 + ((e ^ ((rr >> 1) & 3)) << 4));
-            if (rr < have)
-              *reinterpret_cast<uint4*>(a.q_lat + ((size_t)g.s.q0 * a.H + row0 + rr) * kLD + col +
-                                        8 * e) = w;
-          }
+        if (!whole) {
+          if (lane == 0 && have > 0)
+            tma_store_3d(&p.tm_pa, stage, col, (int)slot_row + (q4 & 1) * 32, 0);
+        } else if (have == 32) {
+          if (lane == 0) tma_store_3d(&p.tm_o, stage, col - 32, g.s.q0 * a.H + row0, 0);
         } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3), e = lane & 7;
-            const uint4 w =
-                *reinterpret_cast<const uint4*>(stage + rr * 128 + ((e ^ (rr & 7)) << 4));
+#pragma unroll 1
+          for (int i = 0; i < have; i += 4) {
+            const int rr = i + (lane >> 3), e = lane & 7;
             if (rr < have)
-              *reinterpret_cast<uint4*>(a.part_acc + (slot_row + (q4 & 1) * 32 + rr) * kLD + col +
-                                        4 * e) = w;
+              *reinterpret_cast<uint4*>(a.q_lat + ((size_t)g.s.q0 * a.H + row0 + rr) * kLD + col -
+                                        32 + 8 * e) =
+                  *reinterpret_cast<const uint4*>(stage + rr * 128 + ((e ^ (rr & 7)) << 4));
           }
+          __syncwarp();
         }
-        __syncwarp();
+        if (lane == 0) bulk_commit_group();
       }
+      if (lane == 0) bulk_wait_read_all();  // before weights are written there again
+      __syncwarp();
       softmax_and(true);  // the sums have been read before the next tile's maxima
     }
   }
 
+  if (warp >= 4 && lane == 0) bulk_wait_all();  // the mixes are written
   // A CTA leaves once neither it nor its peer has anything in flight into its shared memory.
   // In the regular course every copy and MMA has been waited for by now.  After a wait gave
   // up, copies may still be landing: they take microseconds.
@@ -613,17 +653,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
 // Tensor maps, cached by pointers and sizes (encoding costs microseconds of host time).
 struct MapKey {
-  const void* ptr[4];
+  const void* ptr[5];
   int T, H, num_pages, page_shift;
   bool operator==(const MapKey& o) const {
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 5; ++i)
       if (ptr[i] != o.ptr[i]) return false;
     return T == o.T && H == o.H && num_pages == o.num_pages && page_shift == o.page_shift;
   }
 };
 struct MapEntry {
   MapKey key;
-  CUtensorMap maps[4];
+  CUtensorMap maps[6];
   bool valid;
 };
 std::mutex g_mu;
@@ -631,7 +671,7 @@ MapEntry g_maps[16];
 int g_next = 0;
 
 bool tree_maps(const TreeArgs& a, TreeParams* p) {
-  const MapKey key = {{a.q_lat, a.q_pe, a.c_pages, a.pe_pages}, a.T, a.H, a.num_pages, a.page_shift};
+  const MapKey key = {{a.q_lat, a.q_pe, a.c_pages, a.pe_pages, a.part_acc}, a.T, a.H, a.num_pages, a.page_shift};
   std::lock_guard<std::mutex> lk(g_mu);
   for (const MapEntry& e : g_maps) {
     if (e.valid && e.key == key) {
@@ -639,6 +679,8 @@ bool tree_maps(const TreeArgs& a, TreeParams* p) {
       p->tm_qr = e.maps[1];
       p->tm_c = e.maps[2];
       p->tm_kr = e.maps[3];
+      p->tm_o = e.maps[4];
+      p->tm_pa = e.maps[5];
       return true;
     }
   }
@@ -647,7 +689,9 @@ bool tree_maps(const TreeArgs& a, TreeParams* p) {
   if (!encode_bf16_3d(&p->tm_q, a.q_lat, kLD, rows, 1, rows, 64) ||
       !encode_bf16_3d(&p->tm_qr, a.q_pe, 64, rows, 1, rows, 64) ||
       !encode_bf16_3d(&p->tm_c, a.c_pages, kLD, slots, 1, slots, box) ||
-      !encode_bf16_3d(&p->tm_kr, a.pe_pages, 64, slots, 1, slots, box))
+      !encode_bf16_3d(&p->tm_kr, a.pe_pages, 64, slots, 1, slots, box) ||
+      !encode_bf16_3d(&p->tm_o, a.q_lat, kLD, rows, 1, rows, 32) ||
+      !encode_f32_2d(&p->tm_pa, a.part_acc, kLD, (uint64_t)2 * a.pairs * kRows, 32, 32))
     return false;
   MapEntry& e = g_maps[g_next];
   g_next = (g_next + 1) % 16;
@@ -656,6 +700,8 @@ bool tree_maps(const TreeArgs& a, TreeParams* p) {
   e.maps[1] = p->tm_qr;
   e.maps[2] = p->tm_c;
   e.maps[3] = p->tm_kr;
+  e.maps[4] = p->tm_o;
+  e.maps[5] = p->tm_pa;
   e.valid = true;
   return true;
 }

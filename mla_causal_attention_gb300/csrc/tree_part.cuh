@@ -66,6 +66,13 @@ __device__ __forceinline__ int find_warp(const T* v, int n, T x, int lane) {
   return lo;
 }
 
+// One segment: rows 128 m .. of sequence b's rows, key tiles [k0, k1).
+struct Seg {
+  int b, m, k0, k1;
+  TreeSeq s;
+  int slot;  // partial slot, or -1: the unit is finished here
+};
+
 // By one block of 256 threads: prefix sums of units and tiles, the waves, the ranges.
 static __device__ __noinline__ void tree_partition(const TreeArgs& a) {
   __shared__ int64_t s_w[8], s_u[8], s_x;
@@ -159,34 +166,72 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a) {
   }
   __syncthreads();
   for (int k = 0; k < warp; ++k) inc += s_w[k];
-  if (tid < P) a.range0[tid] = min(s_x + inc - need, W);
   if (tid == 0) {
     a.range0[P] = W;
     a.range0[P + 1] = nw;
   }
+  // Each pair's first segment, spelled out: every role of the split kernel starts with one load
+  // instead of a search.
+  if (tid < P) {
+    const int64_t x = min(s_x + inc - need, W), x1 = min(s_x + inc, W);
+    a.range0[tid] = x;
+    Seg g = {};
+    g.b = -1;
+    if (nw > 0) {
+      g.b = find_last(a.unit0, a.B, (int64_t)tid);
+      g.s = tree_seq(a, g.b);
+      g.m = (int)(tid - a.unit0[g.b]);
+      g.k1 = seq_tiles(g.s);
+      g.slot = -1;
+    } else if (x < x1) {
+      g.b = find_last(a.tile0, a.B, x);
+      g.s = tree_seq(a, g.b);
+      const int K = seq_tiles(g.s);
+      const int64_t off = x - a.tile0[g.b];
+      g.m = (int)(off / K);
+      g.k0 = (int)(off - (int64_t)g.m * K);
+      g.k1 = (int)min((int64_t)K, g.k0 + (x1 - x));
+      g.slot = g.k0 == 0 && g.k1 == K ? -1 : 2 * tid;
+    }
+    int4* rec = a.first + 3 * tid;
+    rec[0] = make_int4(g.b, g.m, g.k0, g.k1);
+    rec[1] = make_int4(g.s.q0, g.s.n, g.s.kv, g.s.ctx);
+    rec[2] = make_int4(g.slot, 0, 0, 0);
+  }
 }
 
-// One segment: rows 128 m .. of sequence b's rows, key tiles [k0, k1).
-struct Seg {
-  int b, m, k0, k1;
-  TreeSeq s;
-  int slot;  // partial slot, or -1: the unit is finished here
-};
 // Walks a pair's segments: its whole units, then its range.  Warp-uniform; every role has its own
 // and looks the next segment up while it works on one, since that takes a chain of loads.
 struct SegWalk {
   int64_t wave, waves, x, x1, base, next_base;
   int pair, b, K, lane, slot;
   TreeSeq s;
-  __device__ __forceinline__ SegWalk(const TreeArgs& a, int pair_id, int lane_id) {
+  // The pair's first segment; false if it has none.
+  __device__ __forceinline__ bool start(const TreeArgs& a, int pair_id, int lane_id, Seg& g) {
+    const int4* rec = a.first + 3 * pair_id;
+    const int4 r0 = rec[0], r1 = rec[1], r2 = rec[2];
     pair = pair_id;
     lane = lane_id;
-    wave = 0;
     waves = a.range0[a.pairs + 1];
     x = a.range0[pair];
     x1 = a.range0[pair + 1];
     b = -1;
+    g.b = r0.x;
+    g.m = r0.y;
+    g.k0 = r0.z;
+    g.k1 = r0.w;
+    g.s.q0 = r1.x;
+    g.s.n = r1.y;
+    g.s.kv = r1.z;
+    g.s.ctx = r1.w;
+    g.slot = r2.x;
+    wave = 1;
     slot = 2 * pair;
+    if (waves == 0) {
+      x += g.k1 - g.k0;
+      slot = 2 * pair + 1;
+    }
+    return g.b >= 0;
   }
   __device__ __forceinline__ bool next(const TreeArgs& a, Seg& g) {
     if (wave < waves) {

@@ -29,21 +29,22 @@ using namespace tree;
 constexpr int kLD = 512;
 constexpr int kM = 128;               // tokens per tile
 constexpr int kSub = 128 * 128;       // 128 rows x 64 columns, bf16, 128-byte swizzled
-constexpr int kSlots = 5;             // ring of the rows' sub-tiles
-constexpr int kOffRing = 8 * kSub;    // behind the weight's 8 sub-tiles
-constexpr int kOffBar = kOffRing + kSlots * kSub;
+constexpr int kMaxSlots = 5;          // ring of the rows' sub-tiles: 5, or 3 with 32 KB of output
+constexpr int kOffRing = 8 * kSub;    // staging behind it; behind the weight's 8 sub-tiles
+constexpr int kOffBar = kOffRing + kMaxSlots * kSub;
 constexpr int kSmem = kOffBar + 256 + 1024;
 static_assert(kSmem <= 232448, "shared memory per block");
 
 struct ProjParams {
   CUtensorMap tm_x;  // rows    {K, T, H}, boxes {64, 128, 1}
   CUtensorMap tm_w;  // w_kvb   {512, H * 256}, boxes {64, 128}
+  CUtensorMap tm_y;  // fold: q_lat {512, T, H}, boxes {64, 32, 1}
   TreeArgs a;
   int blocks_y;      // blocks per head
 };
 struct PBars {
   uint64_t w_full;
-  uint64_t full[kSlots], empty[kSlots];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t d_full[2], d_free[2];  // accumulator tiles (d_free: 4 epilogue warps)
   uint32_t tmem_base;
   int abort_flag;
@@ -71,6 +72,7 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 template <bool kUp>
 __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant__ ProjParams p) {
   constexpr int kKs = kUp ? 8 : 2, kNb = kUp ? 1 : 2, kN = kUp ? 128 : 256;
+  constexpr uint32_t kSlots = kUp ? 5 : 3;
   grid_dep_launch();
   const TreeArgs& a = p.a;
   if (!kUp && blockIdx.x == gridDim.x - 1) {
@@ -187,33 +189,63 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
                         mbar_wait(&bars->d_full[d & 1], (d >> 1) & 1, a.status, abort_flag));
         if (!ok) break;
         tc::fence_after_sync();
-        const int t = i * kM + r;
-        uint16_t* dst = kUp ? a.out + ((size_t)t * a.H + h) * 128
-                            : a.q_lat + ((size_t)t * a.H + h) * kLD + 256 * nb;
-#pragma unroll 1
-        for (int c = 0; c < kN / 32; ++c) {
-          uint32_t o[32];
+        const auto take = [&](int c, uint32_t (&o)[32], bool last) {  // columns 32 c ..
           tc::tmem_ld32(tbase + lane_off + (d & 1) * 256 + c * 32, o);
           tc::tmem_wait_ld();
           pin<32>(o);
-          if (c == kN / 32 - 1) {
+          if (last) {
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->d_free[d & 1]);
           }
-          if (t < rows) {
+        };
+        const auto pack8 = [](const uint32_t (&o)[32], int e) {  // columns 8 e .. of the 32
+          uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]),
+                               __uint_as_float(o[8 * e + 2 * k + 1]));
+          return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        if constexpr (kUp) {
+          const int t = i * kM + r;
+          uint16_t* dst = a.out + ((size_t)t * a.H + h) * 128;
+#pragma unroll 1
+          for (int c = 0; c < kN / 32; ++c) {
+            uint32_t o[32];
+            take(c, o, c == kN / 32 - 1);
+            if (t < rows)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]),
-                                   __uint_as_float(o[8 * e + 2 * k + 1]));
-              *reinterpret_cast<uint4*>(dst + c * 32 + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(dst + c * 32 + 8 * e) = pack8(o, e);
+          }
+        } else {
+          // 64 columns of this warp's 32 rows at a time through one of its two 4 KB stages and a
+          // tensor store (lanes writing their own rows touch 32 lines per instruction).
+#pragma unroll 1
+          for (int c = 0; c < kN / 64; ++c) {
+            uint8_t* stage = smem + kOffRing + kSlots * kSub + ((warp & 3) * 2 + (c & 1)) * 4096;
+            if (lane == 0) bulk_wait_read_but_one();  // the stage's last store has read it
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t o[32];
+              take(2 * c + q, o, c == kN / 64 - 1 && q == 1);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + e) ^ (lane & 7)) << 4)) =
+                    pack8(o, e);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && i * kM + (warp & 3) * 32 < a.T) {
+              tma_store_3d(&p.tm_y, stage, 256 * nb + 64 * c, i * kM + (warp & 3) * 32, h);
+              bulk_commit_group();
             }
           }
         }
       }
+    if (!kUp && lane == 0) bulk_wait_all();
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -225,35 +257,39 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
 
 // Partial mixes of the units shared by several pairs: sum 2^(m_s - m) acc_s / sum 2^(m_s - m) l_s
 // over the segments, to bf16 (the up-projection's operand type) where the whole units' mixes are.
-// A warp per row, 16 rows of one unit per block and turn; bound by reading the partials.
-__global__ void __launch_bounds__(512) tree_merge_kernel(const TreeArgs a) {
+// A unit's segments lie in the slots of successive pairs: from the one marked first, each next
+// pair's first slot (pairs without work have empty ones) to the one marked last.  A block per slot
+// and 8 rows, a warp per row; blocks of slots that no unit begins in end at once.  Bound by reading
+// the partials, and for small batches by the chain notes, sums, rows.
+constexpr int kMergeRows = 8;
+__global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeArgs a) {
   grid_dep_launch();
+  __shared__ int4 note[512];
   grid_dep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t u0 = a.range0[a.pairs + 1] * a.pairs, U = a.unit0[a.B];
-  for (int64_t i = blockIdx.x; i < (U - u0) * 8; i += gridDim.x) {
-    const int64_t u = u0 + (i >> 3);
-    const int b = find_warp(a.unit0, a.B, u, lane);
-    const TreeSeq s = tree_seq(a, b);
-    const int m_unit = (int)(u - a.unit0[b]), K = seq_tiles(s);
-    const int r = (int)(i & 7) * 16 + warp;
-    const int row = m_unit * kRows + r;
-    if (row >= s.n * a.H) continue;
-    const int64_t x0 = a.tile0[b] + (int64_t)m_unit * K;
-    const int c0 = find_warp(a.range0, a.pairs, x0, lane);
-    const int c1 = find_warp(a.range0, a.pairs, x0 + K - 1, lane);
-    if (c0 == c1) continue;  // finished by one pair
-    const bool starts = a.range0[c0] == x0;
+  const int slots = 2 * a.pairs;
+  const int s0 = blockIdx.x / (kRows / kMergeRows);
+  const int r0 = (blockIdx.x % (kRows / kMergeRows)) * kMergeRows, r = r0 + warp;
+  const int4 n0 = a.part_note[s0];
+  if (n0.z == 0 || r0 >= n0.y) return;  // empty, no unit's first segment, or fewer rows
+  for (int i = threadIdx.x; i < slots; i += 32 * kMergeRows) note[i] = a.part_note[i];
+  __syncthreads();
+  if (r < n0.y) {
     float4 acc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
-    for (int cb = c0; cb <= c1; cb += 32) {  // lane i: the i-th range of this round
-      const int c = cb + lane;
-      const bool in = c <= c1 && a.range0[c] < a.range0[c + 1];
-      const int slot = c > c0 || starts ? 2 * c : 2 * c + 1;
+    bool last = false;
+    for (int s = s0; !last && s < slots;) {  // up to 32 segments a round, lane i the i-th
+      int slot = -1;
+      for (int k = 0; k < 32 && !last && s < slots; s = (s | 1) + 1) {
+        if (note[s].y == 0) continue;
+        if (lane == k) slot = s;
+        last = note[s].w != 0;
+        ++k;
+      }
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (in) ml = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot * kRows + r];
+      if (slot >= 0) ml = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot * kRows + r];
       float top = ml.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -271,25 +307,24 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const TreeArgs a) {
         acc[k].z *= f0;
         acc[k].w *= f0;
       }
-      uint32_t left = __ballot_sync(0xffffffffu, in);
-      while (left != 0) {  // two partials' rows in flight
-        float4 v[2][4];
-        float fu[2];
+      const int have = __popc(__ballot_sync(0xffffffffu, slot >= 0));
+      for (int k0 = 0; k0 < have; k0 += 4) {  // four partials' rows in flight
+        float4 v[4][4];
+        float fu[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int at = left ? __ffs(left) - 1 : 0;
+        for (int e = 0; e < 4; ++e) {
+          const int at = min(k0 + e, have - 1);
           const float w = __shfl_sync(0xffffffffu, f, at);
           const int sl = __shfl_sync(0xffffffffu, slot, at);
-          fu[e] = left ? w : 0.f;
+          fu[e] = k0 + e < have ? w : 0.f;
           const float4* src =
               reinterpret_cast<const float4*>(a.part_acc + ((size_t)sl * kRows + r) * kLD) + lane;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            v[e][k] = left ? src[32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
-          left &= left - 1;
+            v[e][k] = k0 + e < have ? src[32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             acc[k].x = fmaf(fu[e], v[e][k].x, acc[k].x);
@@ -300,7 +335,7 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const TreeArgs a) {
       }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* dst = a.q_lat + ((size_t)s.q0 * a.H + row) * kLD;
+    uint16_t* dst = a.q_lat + ((size_t)n0.x + r) * kLD;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) =
@@ -313,14 +348,15 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const TreeArgs a) {
 struct MapKey {
   const void* x;
   const void* w;
+  const void* y;
   int T, H, up;
   bool operator==(const MapKey& o) const {
-    return x == o.x && w == o.w && T == o.T && H == o.H && up == o.up;
+    return x == o.x && w == o.w && y == o.y && T == o.T && H == o.H && up == o.up;
   }
 };
 struct MapEntry {
   MapKey key;
-  CUtensorMap maps[2];
+  CUtensorMap maps[3];
   bool valid;
 };
 std::mutex g_mu;
@@ -328,12 +364,13 @@ MapEntry g_maps[16];
 int g_next = 0;
 
 bool proj_maps(const TreeArgs& a, bool up, ProjParams* p) {
-  const MapKey key = {up ? a.q_lat : a.q_nope, a.w_kvb, a.T, a.H, up};
+  const MapKey key = {up ? a.q_lat : a.q_nope, a.w_kvb, a.q_lat, a.T, a.H, up};
   std::lock_guard<std::mutex> lk(g_mu);
   for (const MapEntry& e : g_maps)
     if (e.valid && e.key == key) {
       p->tm_x = e.maps[0];
       p->tm_w = e.maps[1];
+      p->tm_y = e.maps[2];
       return true;
     }
   const uint64_t width = up ? kLD : 128;
@@ -343,14 +380,19 @@ bool proj_maps(const TreeArgs& a, bool up, ProjParams* p) {
   const uint64_t wdims[2] = {kLD, (uint64_t)a.H * 256};
   const uint64_t wstrides[1] = {kLD * 2};
   const uint32_t wbox[2] = {64, 128};
+  const uint64_t ydims[3] = {kLD, (uint64_t)a.T, (uint64_t)a.H};
+  const uint64_t ystrides[2] = {(uint64_t)a.H * kLD * 2, kLD * 2};
+  const uint32_t ybox[3] = {64, 32, 1};
   if (!encode_bf16_tiled(&p->tm_x, key.x, 3, dims, strides, box) ||
-      !encode_bf16_tiled(&p->tm_w, key.w, 2, wdims, wstrides, wbox))
+      !encode_bf16_tiled(&p->tm_w, key.w, 2, wdims, wstrides, wbox) ||
+      !encode_bf16_tiled(&p->tm_y, a.q_lat, 3, ydims, ystrides, ybox))
     return false;
   MapEntry& e = g_maps[g_next];
   g_next = (g_next + 1) % 16;
   e.key = key;
   e.maps[0] = p->tm_x;
   e.maps[1] = p->tm_w;
+  e.maps[2] = p->tm_y;
   e.valid = true;
   return true;
 }
@@ -402,8 +444,8 @@ cudaError_t launch_tree_up(const TreeArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(4 * a.pairs);
-  cfg.blockDim = dim3(512);
+  cfg.gridDim = dim3(2 * a.pairs * (kRows / kMergeRows));
+  cfg.blockDim = dim3(32 * kMergeRows);
   cudaError_t e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, a);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(a.H * p.blocks_y);
