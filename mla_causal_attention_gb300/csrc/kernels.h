@@ -227,6 +227,7 @@ struct LatentAppendArgs {
   uint16_t* q_pe_out;
   int* status;
   int T, H, table_rows, rows;  // H = 0 without q_pe; rows = slots of the pool
+  unsigned q_blocks;           // set by the launcher
 };
 cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream);
 
