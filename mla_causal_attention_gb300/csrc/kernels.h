@@ -156,10 +156,6 @@ bool encode_bf16_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t r
 bool encode_bf16_tiled(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                        const uint64_t* strides_bytes, const uint32_t* box);
 
-// fp32 tensor {inner, rows} with 128-byte swizzled boxes {box_cols (32), box_rows}.
-bool encode_f32_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
-                   uint32_t box_cols, uint32_t box_rows);
-
 // Output projection (o_proj) of the attention output: y [B,T,N] = W [N,H*128] applied to
 // each (b, i) row of attn [B,H,T,128] with the heads concatenated in head order.
 struct OprojArgs {

@@ -68,8 +68,6 @@ struct TreeParams {
   CUtensorMap tm_qr;  // q_pe  {64,  T*H}
   CUtensorMap tm_c;   // c_pages  {512, slots}, boxes {64, min(page, 64)}
   CUtensorMap tm_kr;  // pe_pages {64,  slots}
-  CUtensorMap tm_o;   // q_lat again, boxes {64, 32}: the mixes of whole units
-  CUtensorMap tm_pa;  // part_acc {512, rows} fp32, boxes {32, 32}
   TreeArgs a;
 };
 
@@ -141,6 +139,20 @@ __device__ __forceinline__ bool softmax_and(bool v) {
   return r != 0;
 }
 
+// Eight words w[at ..] to p, in one store if the workspace is 32-byte aligned.
+template <int N>
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[N], int at, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[at]),
+                 "r"(w[at + 1]), "r"(w[at + 2]), "r"(w[at + 3]), "r"(w[at + 4]), "r"(w[at + 5]),
+                 "r"(w[at + 6]), "r"(w[at + 7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[at], w[at + 1], w[at + 2], w[at + 3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[at + 4], w[at + 5], w[at + 6], w[at + 7]);
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 #pragma unroll
@@ -191,6 +203,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (warp == 1) {
     tp::tmem_alloc(&bars->tmem_base, 512);
     tp::tmem_relinquish();
+  }
+  if (warp == 2 && lane == 0) {
+    prefetch_tmap(&p.tm_q);
+    prefetch_tmap(&p.tm_qr);
+    prefetch_tmap(&p.tm_c);
+    prefetch_tmap(&p.tm_kr);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -429,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t p_ready = tp::even_addr(&bars->p_ready);
     const uint32_t o_free = tp::even_addr(&bars->o_free);
     const float sl2 = a.scale_log2;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.q_lat) & 31u) == 0;  // part_acc alike
     // What a slot holds, for the merge: first row, rows, whether it is its unit's first segment
     // and its last.  One thread clears the pair's two notes and fills in those of its segments.
     const bool notes = rank == 0 && threadIdx.x == 128;
@@ -558,14 +577,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const size_t slot_row = (size_t)(whole ? 0 : g.slot) * kRows + 64 * rank;
       if (!whole && half == 0)
         *reinterpret_cast<float2*>(a.part_ml + (slot_row + r) * 2) = make_float2(m, l);
-      // 128 bytes per row at a time (32 fp32 columns, or 64 as bf16) through this warp's quarter of
-      // the weights' buffer, free now, and a tensor store: a lane writing its own row touches
-      // 32 lines per instruction, which took 9000 cycles per segment.  Rows of a partial slot
-      // that do not exist are written too (nothing reads them); those of a whole unit would be
-      // another sequence's, so the last rows of a sequence are written by hand.
-      uint8_t* stage = sP + q4 * 4096;
-      const int row0 = g.m * kRows + 64 * rank + (q4 & 1) * 32;  // the warp's first row
-      const int have = min(max(g.s.n * a.H - row0, 0), 32);      // rows that exist
+      // Each lane writes its own row, 32 columns at a time, the next ones on their way from TMEM.
+      // 32-byte stores, a whole sector each: a store instruction takes a cycle per row, so a
+      // segment's 64 KB per warp take about 4100 cycles (9000 with 16-byte stores, 6400 through
+      // shared memory and tensor stores, whose only free buffer is one stage).
+      uint16_t* fin = a.q_lat + ((size_t)g.s.q0 * a.H + row) * kLD;
+      float* part = a.part_acc + (slot_row + r) * kLD;
       uint32_t nx[32];
       tc::tmem_ld32(tbase + lane_off + kColO, nx);
 #pragma unroll 1
@@ -582,57 +599,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           __syncwarp();
           if (lane == 0) tp::arrive(o_free);
         }
-        if (!whole || (c & 1) == 0) {  // the store before has read the stage
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-        }
         const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+        if (!real) continue;
         if (whole) {
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * f,
-                                 __uint_as_float(o[8 * e + 2 * k + 1]) * f);
-            *reinterpret_cast<uint4*>(stage + lane * 128 +
-                                      (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int k = 0; k < 16; ++k)
+            w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
+          store32(fin + col, w, 0, wide);
+          store32(fin + col + 16, w, 8, wide);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 32; e += 8) store32(part + col + e, o, e, wide);
         }
-        if (whole && (c & 1) == 0) continue;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (!whole) {
-          if (lane == 0 && have > 0)
-            tma_store_3d(&p.tm_pa, stage, col, (int)slot_row + (q4 & 1) * 32, 0);
-        } else if (have == 32) {
-          if (lane == 0) tma_store_3d(&p.tm_o, stage, col - 32, g.s.q0 * a.H + row0, 0);
-        } else {
-#pragma unroll 1
-          for (int i = 0; i < have; i += 4) {
-            const int rr = i + (lane >> 3), e = lane & 7;
-            if (rr < have)
-              *reinterpret_cast<uint4*>(a.q_lat + ((size_t)g.s.q0 * a.H + row0 + rr) * kLD + col -
-                                        32 + 8 * e) =
-                  *reinterpret_cast<const uint4*>(stage + rr * 128 + ((e ^ (rr & 7)) << 4));
-          }
-          __syncwarp();
-        }
-        if (lane == 0) bulk_commit_group();
       }
-      if (lane == 0) bulk_wait_read_all();  // before weights are written there again
-      __syncwarp();
       softmax_and(true);  // the sums have been read before the next tile's maxima
     }
   }
 
-  if (warp >= 4 && lane == 0) bulk_wait_all();  // the mixes are written
   // A CTA leaves once neither it nor its peer has anything in flight into its shared memory.
   // In the regular course every copy and MMA has been waited for by now.  After a wait gave
   // up, copies may still be landing: they take microseconds.
@@ -653,17 +637,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
 // Tensor maps, cached by pointers and sizes (encoding costs microseconds of host time).
 struct MapKey {
-  const void* ptr[5];
+  const void* ptr[4];
   int T, H, num_pages, page_shift;
   bool operator==(const MapKey& o) const {
-    for (int i = 0; i < 5; ++i)
+    for (int i = 0; i < 4; ++i)
       if (ptr[i] != o.ptr[i]) return false;
     return T == o.T && H == o.H && num_pages == o.num_pages && page_shift == o.page_shift;
   }
 };
 struct MapEntry {
   MapKey key;
-  CUtensorMap maps[6];
+  CUtensorMap maps[4];
   bool valid;
 };
 std::mutex g_mu;
@@ -671,7 +655,7 @@ MapEntry g_maps[16];
 int g_next = 0;
 
 bool tree_maps(const TreeArgs& a, TreeParams* p) {
-  const MapKey key = {{a.q_lat, a.q_pe, a.c_pages, a.pe_pages, a.part_acc}, a.T, a.H, a.num_pages, a.page_shift};
+  const MapKey key = {{a.q_lat, a.q_pe, a.c_pages, a.pe_pages}, a.T, a.H, a.num_pages, a.page_shift};
   std::lock_guard<std::mutex> lk(g_mu);
   for (const MapEntry& e : g_maps) {
     if (e.valid && e.key == key) {
@@ -679,8 +663,6 @@ bool tree_maps(const TreeArgs& a, TreeParams* p) {
       p->tm_qr = e.maps[1];
       p->tm_c = e.maps[2];
       p->tm_kr = e.maps[3];
-      p->tm_o = e.maps[4];
-      p->tm_pa = e.maps[5];
       return true;
     }
   }
@@ -689,9 +671,7 @@ bool tree_maps(const TreeArgs& a, TreeParams* p) {
   if (!encode_bf16_3d(&p->tm_q, a.q_lat, kLD, rows, 1, rows, 64) ||
       !encode_bf16_3d(&p->tm_qr, a.q_pe, 64, rows, 1, rows, 64) ||
       !encode_bf16_3d(&p->tm_c, a.c_pages, kLD, slots, 1, slots, box) ||
-      !encode_bf16_3d(&p->tm_kr, a.pe_pages, 64, slots, 1, slots, box) ||
-      !encode_bf16_3d(&p->tm_o, a.q_lat, kLD, rows, 1, rows, 32) ||
-      !encode_f32_2d(&p->tm_pa, a.part_acc, kLD, (uint64_t)2 * a.pairs * kRows, 32, 32))
+      !encode_bf16_3d(&p->tm_kr, a.pe_pages, 64, slots, 1, slots, box))
     return false;
   MapEntry& e = g_maps[g_next];
   g_next = (g_next + 1) % 16;
@@ -700,8 +680,6 @@ bool tree_maps(const TreeArgs& a, TreeParams* p) {
   e.maps[1] = p->tm_qr;
   e.maps[2] = p->tm_c;
   e.maps[3] = p->tm_kr;
-  e.maps[4] = p->tm_o;
-  e.maps[5] = p->tm_pa;
   e.valid = true;
   return true;
 }

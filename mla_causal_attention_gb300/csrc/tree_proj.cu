@@ -29,6 +29,10 @@ using namespace tree;
 constexpr int kLD = 512;
 constexpr int kM = 128;               // tokens per tile
 constexpr int kSub = 128 * 128;       // 128 rows x 64 columns, bf16, 128-byte swizzled
+// Up to this many tokens the up-projection's blocks merge the partial mixes of their rows
+// themselves, two rows per warp, which saves a kernel between two others (8 drafted tokens on 1000
+// keys: 27.9 -> 23.0 us); with more, the merge's blocks all over the GPU are faster.
+constexpr int kMergeTokens = 16;
 constexpr int kMaxSlots = 5;          // ring of the rows' sub-tiles: 5, or 3 with 32 KB of output
 constexpr int kOffRing = 8 * kSub;    // staging behind it; behind the weight's 8 sub-tiles
 constexpr int kOffBar = kOffRing + kMaxSlots * kSub;
@@ -40,7 +44,9 @@ struct ProjParams {
   CUtensorMap tm_w;  // w_kvb   {512, H * 256}, boxes {64, 128}
   CUtensorMap tm_y;  // fold: q_lat {512, T, H}, boxes {64, 32, 1}
   TreeArgs a;
-  int blocks_y;      // blocks per head
+  int blocks_y;      // blocks per head and part along the tokens
+  int parts;         // parts of the output columns, a block each: 1, or (few tokens) 2
+  int merge;         // up: the blocks merge their rows themselves (up to kMergeTokens tokens)
 };
 struct PBars {
   uint64_t w_full;
@@ -66,8 +72,83 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
                  "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+// Merges row r of the unit that begins in slot s0: sum 2^(m_s - m) acc_s / sum 2^(m_s - m) l_s over
+// its segments, to bf16, the up-projection's operand type.  A unit's segments lie in the slots of
+// successive pairs: from the one marked first, each next pair's first slot (pairs without work
+// have empty ones) to the one marked last.  One warp; lane owns columns 4 lane + 128 k.
+__device__ __forceinline__ void merge_row(const TreeArgs& a, const int4* note, int s0, int r,
+                                          int lane, uint2 (&w)[4]) {
+  const int slots = 2 * a.pairs;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+  bool last = false;
+  for (int s = s0; !last && s < slots;) {  // up to 32 segments a round, lane i the i-th
+    int slot = -1;
+    for (int k = 0; k < 32 && !last && s < slots; s = (s | 1) + 1) {
+      if (note[s].y == 0) continue;
+      if (lane == k) slot = s;
+      last = note[s].w != 0;
+      ++k;
+    }
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (slot >= 0) ml = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot * kRows + r];
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float m2 = fmaxf(m, top), base = m2 == -INFINITY ? 0.f : m2;
+    const float f0 = ex2_approx(m - base), f = ex2_approx(ml.x - base);
+    float sum = ml.y * f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * f0 + sum;
+    m = m2;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[k].x *= f0;
+      acc[k].y *= f0;
+      acc[k].z *= f0;
+      acc[k].w *= f0;
+    }
+    const int have = __popc(__ballot_sync(0xffffffffu, slot >= 0));
+    for (int k0 = 0; k0 < have; k0 += 4) {  // four partials' rows in flight
+      float4 v[4][4];
+      float fu[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = min(k0 + e, have - 1);
+        const float x = __shfl_sync(0xffffffffu, f, at);
+        const int sl = __shfl_sync(0xffffffffu, slot, at);
+        fu[e] = k0 + e < have ? x : 0.f;
+        const float4* src =
+            reinterpret_cast<const float4*>(a.part_acc + ((size_t)sl * kRows + r) * kLD) + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[e][k] = k0 + e < have ? src[32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc[k].x = fmaf(fu[e], v[e][k].x, acc[k].x);
+          acc[k].y = fmaf(fu[e], v[e][k].y, acc[k].y);
+          acc[k].z = fmaf(fu[e], v[e][k].z, acc[k].z);
+          acc[k].w = fmaf(fu[e], v[e][k].w, acc[k].w);
+        }
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    w[k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
+                      pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+}
+
 // kUp: K = 512 in 8 sub-tiles, N = 128, weight K-major.  Fold: K = 128 in 2 sub-tiles, N = 512 in
-// two blocks of 256, weight MN-major (its rows are the contraction).
+// two blocks of 256, weight MN-major (its rows are the contraction).  Up to 128 tokens there is
+// one block per head, most SMs are idle and the weight's load is the critical path: the fold's
+// two column blocks then go to two blocks.
 // Warps: 0 TMA, 1 MMA, 4-7 epilogue.  The fold launch has one block more, which makes the partition.
 template <bool kUp>
 __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant__ ProjParams p) {
@@ -86,7 +167,9 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
   PBars* bars = reinterpret_cast<PBars*>(smem + kOffBar);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x / p.blocks_y, y = blockIdx.x % p.blocks_y;
+  const int part = blockIdx.x % p.parts;
+  const int h = blockIdx.x / p.parts / p.blocks_y, y = blockIdx.x / p.parts % p.blocks_y;
+  const int nb0 = p.parts == 2 ? part : 0, nb1 = p.parts == 2 ? part + 1 : kNb;
   if (threadIdx.x == 0) {
     mbar_init(&bars->w_full, 1);
     for (int i = 0; i < kSlots; ++i) {
@@ -110,16 +193,50 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
   const uint32_t tbase = bars->tmem_base;
   // The weight is no kernel's output: it is on its way before the kernel in front is waited for.
   if (warp == 0 && lane == 0) {
-    mbar_arrive_expect_tx(&bars->w_full, 8 * kSub);
-    for (int s = 0; s < 8; ++s)
+    prefetch_tmap(&p.tm_x);
+    if (!kUp) prefetch_tmap(&p.tm_y);
+    const int s0 = kUp ? 0 : 4 * nb0, s1 = kUp ? 8 : 4 * nb1;
+    mbar_arrive_expect_tx(&bars->w_full, (s1 - s0) * kSub);
+    for (int s = s0; s < s1; ++s)
       tma_load_2d(sW + s * kSub, &p.tm_w, &bars->w_full, 64 * s, h * 256 + (kUp ? 128 : 0));
   }
   if (kUp) grid_dep_wait();
   const int rows = kUp ? min(max(a.cu_q[a.B], 0), a.T) : a.T;
   const int tiles = (rows + kM - 1) / kM;
+  const bool merge = kUp && p.merge;
+  // Rows merged by this block lie 2 KB per sub-tile: what an MMA reads behind row 16 is another
+  // sub-tile's, and goes into rows of the result that do not exist.
+  constexpr int kMergeSub = kMergeTokens * 128;
+  if (merge) {
+    int4* note = reinterpret_cast<int4*>(sX + 4 * kSub);
+    for (int i = threadIdx.x; i < 2 * a.pairs; i += 256) note[i] = a.part_note[i];
+    __syncthreads();
+    for (int t = warp; t < rows; t += 8) {
+      const int row = t * a.H + h;
+      int s0 = -1;  // the slot that begins the row's unit, if it was shared
+      for (int i = lane; i < 2 * a.pairs; i += 32)
+        if (note[i].z != 0 && row >= note[i].x && row < note[i].x + note[i].y) s0 = i;
+      s0 = __reduce_max_sync(0xffffffffu, s0);
+      uint2 w[4];
+      if (s0 >= 0) {
+        merge_row(a, note, s0, row - note[s0].x, lane, w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = *reinterpret_cast<const uint2*>(a.q_lat + (size_t)row * kLD + 4 * lane + 128 * k);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint2*>(sX + (2 * k + (lane >> 4)) * kMergeSub + t * 128 +
+                                  ((((lane & 15) >> 1) ^ (t & 7)) << 4) + 8 * (lane & 1)) = w[k];
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+  }
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (lane == 0 && merge) drain(&bars->w_full, 0);
+    if (lane == 0 && !merge) {
       uint32_t u = 0;
       bool ok = true;
       for (int i = y; i < tiles && ok; i += p.blocks_y)
@@ -143,12 +260,12 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
     uint32_t u = 0, d = 0;  // sub-tiles, accumulator tiles
     bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->w_full, 0, a.status, abort_flag));
     for (int i = y; i < tiles && ok; i += p.blocks_y) {
-      for (int nb = 0; nb < kNb && ok; ++nb, ++d) {
+      for (int nb = nb0; nb < nb1 && ok; ++nb, ++d) {
         if (d > 1) ok = mbar_wait(&bars->d_free[d & 1], ((d >> 1) - 1) & 1, a.status, abort_flag);
 #pragma unroll 1
         for (int s = 0; s < kKs; ++s) {
           const uint32_t slot = (u + s) % kSlots, n = (u + s) / kSlots;
-          ok = ok && mbar_wait(&bars->full[slot], n & 1, a.status, abort_flag);
+          if (!merge) ok = ok && mbar_wait(&bars->full[slot], n & 1, a.status, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc::fence_after_sync();
@@ -160,11 +277,11 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
               const uint32_t w_at =
                   kUp ? w_lo + s * (kSub >> 4) + 2 * kk
                       : w_lo + 4 * nb * (kSub >> 4) + (4 * s + kk) * (2048 >> 4);
-              tc::mma_ss(tbase + (d & 1) * 256,
-                         d_x | (uint64_t)(x_lo + slot * (kSub >> 4) + 2 * kk),
+              const uint32_t x_at = merge ? s * (kMergeSub >> 4) : slot * (kSub >> 4);
+              tc::mma_ss(tbase + (d & 1) * 256, d_x | (uint64_t)(x_lo + x_at + 2 * kk),
                          d_w | (uint64_t)w_at, kId, (s | kk) != 0 ? 1u : 0u);
             }
-            if (nb == kNb - 1) tc::commit(&bars->empty[slot]);
+            if (nb == nb1 - 1) tc::commit(&bars->empty[slot]);
             if (s == kKs - 1) tc::commit(&bars->d_full[d & 1]);
           }
           __syncwarp();
@@ -184,7 +301,7 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
     uint32_t d = 0;
     bool ok = true;
     for (int i = y; i < tiles && ok; i += p.blocks_y)
-      for (int nb = 0; nb < kNb && ok; ++nb, ++d) {
+      for (int nb = nb0; nb < nb1 && ok; ++nb, ++d) {
         ok = __all_sync(0xffffffffu,
                         mbar_wait(&bars->d_full[d & 1], (d >> 1) & 1, a.status, abort_flag));
         if (!ok) break;
@@ -255,12 +372,8 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
   }
 }
 
-// Partial mixes of the units shared by several pairs: sum 2^(m_s - m) acc_s / sum 2^(m_s - m) l_s
-// over the segments, to bf16 (the up-projection's operand type) where the whole units' mixes are.
-// A unit's segments lie in the slots of successive pairs: from the one marked first, each next
-// pair's first slot (pairs without work have empty ones) to the one marked last.  A block per slot
-// and 8 rows, a warp per row; blocks of slots that no unit begins in end at once.  Bound by reading
-// the partials, and for small batches by the chain notes, sums, rows.
+// The merge as a kernel of its own: a block per slot and 8 rows, a warp per row; blocks of slots
+// that no unit begins in end at once.  Bound by reading the partials.
 constexpr int kMergeRows = 8;
 __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeArgs a) {
   grid_dep_launch();
@@ -274,74 +387,12 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeA
   if (n0.z == 0 || r0 >= n0.y) return;  // empty, no unit's first segment, or fewer rows
   for (int i = threadIdx.x; i < slots; i += 32 * kMergeRows) note[i] = a.part_note[i];
   __syncthreads();
-  if (r < n0.y) {
-    float4 acc[4];
+  if (r >= n0.y) return;
+  uint2 w[4];
+  merge_row(a, note, s0, r, lane, w);
+  uint16_t* dst = a.q_lat + ((size_t)n0.x + r) * kLD;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    bool last = false;
-    for (int s = s0; !last && s < slots;) {  // up to 32 segments a round, lane i the i-th
-      int slot = -1;
-      for (int k = 0; k < 32 && !last && s < slots; s = (s | 1) + 1) {
-        if (note[s].y == 0) continue;
-        if (lane == k) slot = s;
-        last = note[s].w != 0;
-        ++k;
-      }
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (slot >= 0) ml = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot * kRows + r];
-      float top = ml.x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float m2 = fmaxf(m, top), base = m2 == -INFINITY ? 0.f : m2;
-      const float f0 = ex2_approx(m - base), f = ex2_approx(ml.x - base);
-      float sum = ml.y * f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l = l * f0 + sum;
-      m = m2;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[k].x *= f0;
-        acc[k].y *= f0;
-        acc[k].z *= f0;
-        acc[k].w *= f0;
-      }
-      const int have = __popc(__ballot_sync(0xffffffffu, slot >= 0));
-      for (int k0 = 0; k0 < have; k0 += 4) {  // four partials' rows in flight
-        float4 v[4][4];
-        float fu[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = min(k0 + e, have - 1);
-          const float w = __shfl_sync(0xffffffffu, f, at);
-          const int sl = __shfl_sync(0xffffffffu, slot, at);
-          fu[e] = k0 + e < have ? w : 0.f;
-          const float4* src =
-              reinterpret_cast<const float4*>(a.part_acc + ((size_t)sl * kRows + r) * kLD) + lane;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            v[e][k] = k0 + e < have ? src[32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            acc[k].x = fmaf(fu[e], v[e][k].x, acc[k].x);
-            acc[k].y = fmaf(fu[e], v[e][k].y, acc[k].y);
-            acc[k].z = fmaf(fu[e], v[e][k].z, acc[k].z);
-            acc[k].w = fmaf(fu[e], v[e][k].w, acc[k].w);
-          }
-      }
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* dst = a.q_lat + ((size_t)n0.x + r) * kLD;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) =
-          make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
-                     pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-  }
+  for (int k = 0; k < 4; ++k) *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) = w[k];
 }
 
 // Tensor maps, cached by pointers and sizes (encoding costs microseconds of host time).
@@ -428,7 +479,9 @@ cudaError_t launch_tree_fold(const TreeArgs& a, cudaStream_t stream) {
   if (!proj_maps(a, false, &p)) return cudaErrorInvalidValue;
   p.a = a;
   p.blocks_y = blocks_per_head(a);
-  tree_proj_kernel<false><<<a.H * p.blocks_y + 1, 256, kSmem, stream>>>(p);
+  p.parts = a.T <= kM && a.H <= a.pairs ? 2 : 1;
+  p.merge = 0;
+  tree_proj_kernel<false><<<a.H * p.blocks_y * p.parts + 1, 256, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -437,6 +490,8 @@ cudaError_t launch_tree_up(const TreeArgs& a, cudaStream_t stream) {
   if (!proj_maps(a, true, &p)) return cudaErrorInvalidValue;
   p.a = a;
   p.blocks_y = blocks_per_head(a);
+  p.parts = 1;
+  p.merge = a.T <= kMergeTokens;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -444,10 +499,13 @@ cudaError_t launch_tree_up(const TreeArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(2 * a.pairs * (kRows / kMergeRows));
-  cfg.blockDim = dim3(32 * kMergeRows);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, a);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if (!p.merge) {
+    cfg.gridDim = dim3(2 * a.pairs * (kRows / kMergeRows));
+    cfg.blockDim = dim3(32 * kMergeRows);
+    e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, a);
+    if (e != cudaSuccess) return e;
+  }
   cfg.gridDim = dim3(a.H * p.blocks_y);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = kSmem;
