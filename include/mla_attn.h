@@ -392,7 +392,9 @@ MLA_API mla_status mla_attn_varlen_fwd(const uint16_t* q_nope, const uint16_t* q
  *               mla_latent_tree_fwd takes.  At most 64 new tokens per sequence then.
  * Rows t from cu_q[B] to T - 1: slots -1, positions 0, draft_mask 0.
  *
- * free_next must not be free_head (every block reads one while one block writes the other).
+ * free_next must not be free_head, nor kv_len a length that is read (blocks read the one while
+ * others write the other; MLA_ERR_ARG).  Entries of the table at or past ceil(ctx / page_size) are
+ * taken to be free: a server that drops drafted tokens puts their pages back on its list first.
  * Problems only the device sees go to the status word, and the call completes: lengths below
  * zero or past max_pages * page_size, or more than T new tokens in all (MLA_ERR_KVLEN:
  * lengths are clamped, tokens past the table get slot -1); a free list that runs out, or an
@@ -453,7 +455,7 @@ MLA_API mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k
  *   c_pages, pe_pages, block_table [B, max_pages], cu_q [B + 1], kv_len [B]    as above
  *   draft_mask [T] int64 or NULL        w_kvb [H * 256, 512] bf16
  * Only the entries of the block table below ceil(kv_len[b] / page_size) are read.
- * H up to 1024; workspace mla_latent_tree_workspace_bytes(T, H, B) bytes, zeroed once.
+ * H up to 1024, T * H up to 2^26, max_pages * page_size up to 2^30; workspace mla_latent_tree_workspace_bytes(T, H, B) bytes, zeroed once.
  * Device-side problems (the call completes): cu_q not rising within [0, T], kv_len[b] below n
  * or past max_pages * page_size (MLA_ERR_KVLEN, clamped); a page outside the pool
  * (MLA_ERR_PAGE, read as zeros); n > 64 with draft_mask (MLA_ERR_TREE: the keys past 64 are

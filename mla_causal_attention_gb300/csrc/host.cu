@@ -642,7 +642,8 @@ mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int B,
   if (!aligned16(slots) || !aligned16(positions) || !aligned16(draft_mask) ||
       !aligned16(workspace))
     return MLA_ERR_ALIGN;
-  if (free_next == free_head) return MLA_ERR_ARG;
+  // Blocks read these while others write.
+  if (free_next == free_head || kv_len == ctx_len || kv_len == new_len) return MLA_ERR_ARG;
   if (workspace_bytes < kStatusBytes) return MLA_ERR_WORKSPACE;
   const mla_status st = check_device(nullptr);
   if (st != MLA_OK) return st;
@@ -713,7 +714,7 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
   const mla_status ps = check_pool(num_pages, page_size);
   if (ps != MLA_OK) return ps;
   if (B < 1 || T < 1 || H < 1 || H > 1024 || max_pages < 1 || B > (1 << 20) ||
-      (int64_t)max_pages * page_size > 0x7fffffff || (int64_t)T * H > (int64_t(1) << 26))
+      (int64_t)max_pages * page_size > (1 << 30) || (int64_t)T * H > (int64_t(1) << 26))
     return MLA_ERR_SHAPE;
   if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(c_pages) || !aligned16(pe_pages) ||
       !aligned16(w_kvb) || !aligned16(out) || !aligned16(workspace) ||

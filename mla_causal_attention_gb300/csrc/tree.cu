@@ -555,7 +555,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tp::arrive(p_ready);
+#ifdef MLA_TEST_DROP_P_READY
+        // Test build only: a softmax warp of the first pair withholds the arrival for its second
+        // tile.  The mix warp's bounded wait for it then gives up, which exercises the timeout
+        // report and the unwinding of both CTAs.
+        const bool withhold = blockIdx.x == 0 && warp == 4 && t == 1;
+#else
+        constexpr bool withhold = false;
+#endif
+        if (lane == 0 && !withhold) tp::arrive(p_ready);
       }
       if (gone) break;
       more = walk.next(a, after);
@@ -577,40 +585,43 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const size_t slot_row = (size_t)(whole ? 0 : g.slot) * kRows + 64 * rank;
       if (!whole && half == 0)
         *reinterpret_cast<float2*>(a.part_ml + (slot_row + r) * 2) = make_float2(m, l);
-      // Each lane writes its own row, 32 columns at a time, the next ones on their way from TMEM.
-      // 32-byte stores, a whole sector each: a store instruction takes a cycle per row, so a
-      // segment's 64 KB per warp take about 4100 cycles (9000 with 16-byte stores, 6400 through
-      // shared memory and tensor stores, whose only free buffer is one stage).
+      // Each lane writes its own row, 64 columns at a time, in 32-byte stores, a whole sector each:
+      // a store instruction takes a cycle per row, so a segment's 64 KB per warp take about 4100
+      // cycles (9000 with 16-byte stores, 6400 through shared memory and tensor stores, whose
+      // only free buffer is one stage).  The TMEM loads are waited for where they are issued:
+      // a register that is still being loaded must not be carried around the loop, the compiler
+      // may move it.
       uint16_t* fin = a.q_lat + ((size_t)g.s.q0 * a.H + row) * kLD;
       float* part = a.part_acc + (slot_row + r) * kLD;
-      uint32_t nx[32];
-      tc::tmem_ld32(tbase + lane_off + kColO, nx);
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t o[32];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[2][32];
+        tc::tmem_ld32(tbase + lane_off + kColO + c * 64, o[0]);
+        tc::tmem_ld32(tbase + lane_off + kColO + c * 64 + 32, o[1]);
         tc::tmem_wait_ld();
-        pin<32>(nx);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = nx[e];
-        if (c < 7) {
-          tc::tmem_ld32(tbase + lane_off + kColO + (c + 1) * 32, nx);
-        } else {  // the mix is out of TMEM: the next segment's may be written
+        pin<32>(o[0]);
+        pin<32>(o[1]);
+        if (c == 3) {  // the mix is out of TMEM: the next segment's may be written
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tp::arrive(o_free);
         }
-        const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
         if (!real) continue;
-        if (whole) {
-          uint32_t w[16];
+        const int col = 256 * (c >> 1) + 128 * half + 64 * (c & 1);
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
-          store32(fin + col, w, 0, wide);
-          store32(fin + col + 16, w, 8, wide);
-        } else {
+        for (int q = 0; q < 2; ++q) {
+          if (whole) {
+            uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) store32(part + col + e, o, e, wide);
+            for (int k = 0; k < 16; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(o[q][2 * k]) * f,
+                                 __uint_as_float(o[q][2 * k + 1]) * f);
+            store32(fin + col + 32 * q, w, 0, wide);
+            store32(fin + col + 32 * q + 16, w, 8, wide);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store32(part + col + 32 * q + e, o[q], e, wide);
+          }
         }
       }
       softmax_and(true);  // the sums have been read before the next tile's maxima

@@ -246,8 +246,7 @@ struct SegWalk {
       return true;
     }
     if (x >= x1) return false;
-    if (b < 0) enter(a, find_warp(a.tile0, a.B, x, lane));
-    while (x >= next_base) enter(a, b + 1);  // skips sequences without work
+    if (b < 0 || x >= next_base) enter(a, find_warp(a.tile0, a.B, x, lane));
     const int64_t off = x - base;
     g.b = b;
     g.m = (int)(off / K);

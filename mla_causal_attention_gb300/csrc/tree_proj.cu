@@ -355,8 +355,11 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0 && i * kM + (warp & 3) * 32 < a.T) {
-              tma_store_3d(&p.tm_y, stage, 256 * nb + 64 * c, i * kM + (warp & 3) * 32, h);
+            if (lane == 0) {
+              // A group for every stage, also where all its rows lie behind T: the wait above
+              // counts groups.
+              if (i * kM + (warp & 3) * 32 < a.T)
+                tma_store_3d(&p.tm_y, stage, 256 * nb + 64 * c, i * kM + (warp & 3) * 32, h);
               bulk_commit_group();
             }
           }

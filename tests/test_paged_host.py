@@ -66,9 +66,10 @@ def test_plan_refuses_alignment_and_alias(lib, base):
         a = _plan_args(base)
         a[name] += off
         assert lib.mla_paged_plan(*[a[n] for n in PLAN]) == S.ERR_ALIGN, name
-    a = _plan_args(base)
-    a["free_next"] = a["free_head"]
-    assert lib.mla_paged_plan(*[a[n] for n in PLAN]) == S.ERR_ARG
+    for out, read in (("free_next", "free_head"), ("kv_len", "ctx_len"), ("kv_len", "new_len")):
+        a = _plan_args(base)
+        a[out] = a[read]
+        assert lib.mla_paged_plan(*[a[n] for n in PLAN]) == S.ERR_ARG
     if not torch.cuda.is_available():
         a = _plan_args(base)
         assert lib.mla_paged_plan(*[a[n] for n in PLAN]) in _no_device()
@@ -145,6 +146,7 @@ def _tree_args(base, lib):
     ({"H": 0}, S.ERR_SHAPE), ({"H": 1025}, S.ERR_SHAPE), ({"page_size": 20}, S.ERR_SHAPE),
     ({"num_pages": 0}, S.ERR_SHAPE), ({"max_pages": 0}, S.ERR_SHAPE),
     ({"T": 1 << 27}, S.ERR_SHAPE), ({"scale": 0.0}, S.ERR_ARG), ({"scale": float("inf")}, S.ERR_ARG),
+    ({"max_pages": (1 << 26) + 1}, S.ERR_SHAPE),
 ])
 def test_tree_refuses(lib, base, change, want):
     a = _tree_args(base, lib)

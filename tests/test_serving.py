@@ -125,3 +125,31 @@ def test_prompts_then_drafted_trees(H, seed):
             s.table[b, held:had] = -1
         s.free, s.head = free + s.free[s.head:], 0
     assert sorted(s.free + [q for row in s.table.tolist() for q in row if q >= 0]) == list(range(POOL))
+
+
+def test_two_streams_at_once():
+    """Two servers' steps in flight at the same time, each on a stream and a workspace of its own."""
+    from paged_helpers import tree_case
+    cases = [tree_case(60, 20, 64, (0, 900), (1, 30), 32, True),
+             tree_case(61, 5, 64, (2000, 3000), (1, 5), 64, False)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [mla.Workspace() for _ in cases]
+
+    def call(d, out, **kw):
+        return mla.mla_latent_tree_fwd(d["q_nope"], d["q_pe"], d["c_pages"], d["pe_pages"],
+                                       d["block_table"], d["kv_len"], d["cu_q"], d["draft_mask"],
+                                       d["w_kvb"], SCALE, out=out, **kw)
+
+    want = [call(d, None, workspace=w).clone() for d, w in zip(cases, spaces)]
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(w) for w in want]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(60):
+        for d, o, s, w in zip(cases, outs, streams, spaces):
+            call(d, o, stream=s, workspace=w)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    for w in spaces:
+        assert mla.mla_attn_get_status(workspace=w) == 0

@@ -240,3 +240,71 @@ def test_a_pool_past_four_gigabytes():
     table = torch.where(d["block_table"] >= 0, far[d["block_table"].clamp(min=0).long()].int(), -1)
     e = dict(d, block_table=table.contiguous(), **big)
     assert torch.equal(_run(e), _run(d))
+
+
+def test_many_empty_sequences():
+    """Tokens in the first and the last of 3000 sequences only."""
+    d = tree_case(16, 2, 64, (200, 700), (3, 9), 64, True)
+    B, width = 3000, d["block_table"].shape[1]
+    n0 = int(d["cu_q"][1])
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    table[0], table[-1] = d["block_table"][0], d["block_table"][1]
+    kv = torch.zeros(B, dtype=torch.int32, device="cuda")
+    kv[0], kv[-1] = d["kv_len"][0], d["kv_len"][1]
+    cu = torch.full((B + 1,), n0, dtype=torch.int32, device="cuda")
+    cu[0], cu[-1] = 0, int(d["cu_q"][2])
+    want = _run(d)
+    assert torch.equal(_run(dict(d, block_table=table, kv_len=kv, cu_q=cu)), want)
+    assert mla.mla_attn_get_status() == 0
+
+
+def test_sequences_may_share_pages():
+    """A common prefix held once: two sequences whose first pages are the same."""
+    d = tree_case(17, 2, 16, (640, 640), (4, 4), 64, True)
+    d["block_table"][1, :10] = d["block_table"][0, :10]
+    _close(_run(d), d)
+
+
+def test_many_calls_in_flight():
+    """Calls of different sizes one behind the other on one workspace, without waiting."""
+    cases = [tree_case(30 + k, B, H, (0, ctx), (1, new), 32, tree)
+             for k, (B, H, ctx, new, tree) in enumerate(((1, 64, 900, 8, True), (9, 16, 300, 64, True),
+                                                         (40, 64, 500, 1, False), (3, 8, 40, 5, True)))]
+    want = [_run(d).clone() for d in cases]
+    outs = [torch.empty_like(w) for w in want]
+    for k in range(200):
+        i = k % 4
+        d = cases[i]
+        mla.mla_latent_tree_fwd(d["q_nope"], d["q_pe"], d["c_pages"], d["pe_pages"],
+                                d["block_table"], d["kv_len"], d["cu_q"], d["draft_mask"],
+                                d["w_kvb"], SCALE, out=outs[i])
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert torch.equal(w, o)
+    assert mla.mla_attn_get_status() == 0
+
+
+def test_a_workspace_that_is_only_16_byte_aligned():
+    d = tree_case(18, 5, 64, (0, 600), (1, 20), 16, True)
+    want = _run(d)
+    ws = mla.Workspace()
+    T, H = d["q_nope"].shape[:2]
+    n = binding.library().mla_latent_tree_workspace_bytes(T, H, 5)
+    ws.buf = torch.zeros(n + 16, dtype=torch.uint8, device="cuda")[16:]
+    assert torch.equal(_run(d, workspace=ws), want)
+
+
+@pytest.mark.parametrize("T,H,rounds", [(2736, 64, 150), (5000, 16, 150), (288, 64, 150)])
+def test_folded_queries_are_the_same_every_time(T, H, rounds):
+    """Token counts whose last 128 end early, so that part of the warps have no row to write: every
+    call's result is the first one's, whatever the workspace held before."""
+    d = tree_case(50, 1, H, (0, 0), (T, T), 64, False)
+    ws = mla.Workspace()
+    want = _run(d, workspace=ws).clone()
+    for k in range(rounds):
+        if k % 3 == 0:
+            ws.buf[256:].random_(0, 255)
+        out = mla.mla_latent_tree_fwd(d["q_nope"], d["q_pe"], d["c_pages"], d["pe_pages"],
+                                      d["block_table"], d["kv_len"], d["cu_q"], d["draft_mask"],
+                                      d["w_kvb"], SCALE, workspace=ws)
+        assert torch.equal(out, want), k

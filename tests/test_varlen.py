@@ -88,6 +88,7 @@ def _close(got, d, seqs=None):
     ([2100], 6, 2, True),
     ([64] * 40, 8, 8, False),
     ([1] * 300, 4, 2, True),                 # more sequences than CTAs
+    ([0, 0], 4, 4, False),                   # nothing to do
 ])
 def test_varlen_matches_definition(ns, H, Hkv, fused):
     d = _case(len(ns) * 100 + H, ns, H, Hkv, fused, pad=5)
@@ -202,3 +203,17 @@ def test_many_calls_in_flight():
     for k in range(4):
         assert torch.equal(outs[k], want["d" if k % 2 == 0 else "e"])
     assert mla.mla_attn_get_status() == 0
+
+
+def test_results_are_the_same_every_time():
+    """Whatever the workspace held before, and in whatever order units of equal length run."""
+    r = random.Random(5)
+    for k in range(4):
+        ns = [r.choice((1, 60, 128, 200, 300, 900)) for _ in range(24)]
+        d = _case(70 + k, ns, 16, 4, True)
+        ws = mla.Workspace()
+        want = _run(d, workspace=ws).clone()
+        for i in range(40):
+            if i % 3 == 0:
+                ws.buf[256:].random_(0, 255)
+            assert torch.equal(_run(d, workspace=ws), want), (k, i)
