@@ -403,6 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 3 && rank == 0) {
     // ================= mix MMAs =================
+    // In two batches.  Four, so that scores queue behind less of a mix, took 1.36 instead of 1.21
+    // ms for the 64-token trees, and 1.64 with a batch held back until the one before the last had
+    // finished; one batch of 16 took 1.25.
     constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, 256, true);
     const uint64_t d_p = tc::smem_desc_sw128(0, 16, 1024);     // K-major
     const uint64_t d_v = tc::smem_desc_sw128(0, kSubV, 1024);  // MN-major: 64-column halves
