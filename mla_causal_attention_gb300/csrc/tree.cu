@@ -101,6 +101,12 @@ __device__ __forceinline__ int key_row(const TreeArgs& a, int b, int kv, int key
   return (page << a.page_shift) + (key & ((1 << a.page_shift) - 1));
 }
 
+// Rows of a unit in the even CTA: half of those of a unit that has at most 64 (a sequence with
+// one token), so that both CTAs share the writing of its mix, else 64.
+__device__ __forceinline__ int rows_first(const TreeArgs& a, const Seg& g) {
+  return g.s.n * a.H - g.m * kRows <= 64 ? 32 : 64;
+}
+
 // Boxes of `box` keys that hold one of the first min(left, 64) keys.
 __device__ __forceinline__ int boxes_of(int left, int box) {
   return (min(max(left, 0), 64) + box - 1) / box;
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (ns > 0) ok = mbar_wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int q_row = g.s.q0 * a.H + g.m * kRows + 64 * rank;
+      const int q_row = g.s.q0 * a.H + g.m * kRows + rows_first(a, g) * rank;
       if (tc::elect_one()) {
         tp::arrive_expect_tx(q_full, 9 * kSubQ);
 #pragma unroll 1
@@ -461,8 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t t = 0;
     bool ok = true, gone = false;  // a wait of this thread's gave up; all four warps leave
     for (; more; g = after) {
-      const int row = g.m * kRows + 64 * rank + r;  // row of the sequence
-      const bool real = row < g.s.n * a.H;
+      const int first = rows_first(a, g);
+      const int row = g.m * kRows + first * rank + r;  // row of the sequence
+      const bool real = r < first && row < g.s.n * a.H;
       const int i = row / a.H;                      // new token
       const bool masked = a.draft_mask != nullptr;
       const uint64_t mask = masked && real ? (uint64_t)a.draft_mask[g.s.q0 + i] : 0ull;
@@ -585,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         a.part_note[g.slot] = make_int4(g.s.q0 * a.H + g.m * kRows,
                                         min(kRows, g.s.n * a.H - g.m * kRows), g.k0 == 0,
                                         g.k1 == seq_tiles(g.s));
-      const size_t slot_row = (size_t)(whole ? 0 : g.slot) * kRows + 64 * rank;
-      if (!whole && half == 0)
+      const size_t slot_row = (size_t)(whole ? 0 : g.slot) * kRows + first * rank;
+      if (!whole && half == 0 && r < first)
         *reinterpret_cast<float2*>(a.part_ml + (slot_row + r) * 2) = make_float2(m, l);
       // Each lane writes its own row, 64 columns at a time, in 32-byte stores, a whole sector each:
       // a store instruction takes a cycle per row, so a segment's 64 KB per warp take about 4100
