@@ -11,6 +11,10 @@ namespace tree {
 
 constexpr int kTile = 128;  // keys per tile
 constexpr int kRows = 128;  // query rows per unit, 64 per CTA
+// What the end of a unit costs -- its mix read out and written, the next one's rows fetched -- in
+// tiles: 0, 2, 3, 4, 8 of them give 446, 437, 427, 430, 436 us for ragged batches of trees, 64.7,
+// 62.0, 61.8, 61.6, 66.3 for a ragged decode.
+constexpr int kEndTiles = 3;
 
 // ---- the partition -----------------------------------------------------------------------
 // Sequence b has n_b H rows in M_b units and K_b key tiles.  Units are numbered, and their tiles
@@ -19,8 +23,8 @@ constexpr int kRows = 128;  // query rows per unit, 64 per CTA
 // same few sequences at the same time, and find them in L2 (64-token trees on 32768 keys: 1.20 ms;
 // all tiles cut into equal ranges, where every pair is at another key, 1.61, and in five rounds
 // of such ranges 1.30).  The tiles of the remaining units
-// are cut into one contiguous range per pair, each as long as brings the pair's work to the
-// common level; n_w is the largest number of waves that leaves every pair at or below it.  A
+// are cut into one contiguous range per pair, each as long as brings the pair's work, with
+// kEndTiles for every unit's end, to the common level; n_w is the largest number of waves that leaves every pair at or below it.  A
 // range's tiles of one unit are a segment: a unit within one segment is finished there, the
 // others leave partial mixes, range c's first segment in slot 2 c, its last, if another, in slot
 // 2 c + 1.
@@ -129,13 +133,13 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a) {
   // Thread c: the tiles of pair c's whole units, for ever fewer waves until no pair is above the
   // level.
   const int P = a.pairs;  // at most 256
-  const int64_t level = (W + P - 1) / P;
+  const int64_t cost = W + kEndTiles * U, level = (cost + P - 1) / P;
   int64_t nw = U / P, load = 0;
   int at = 0;  // the sequence of the unit looked at last
   const auto tiles_of = [&](int64_t u) {
     while (a.unit0[at + 1] <= u) ++at;
     while (a.unit0[at] > u) --at;
-    return (int64_t)seq_tiles(tree_seq(a, at));
+    return (int64_t)seq_tiles(tree_seq(a, at)) + kEndTiles;
   };
   if (tid < P)
     for (int64_t i = 0; i < nw; ++i) load += tiles_of(i * P + tid);
@@ -158,16 +162,29 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a) {
     if (lane >= o) inc += x;
   }
   if (lane == 31) s_w[warp] = inc;
-  if (tid == 0) {
+  if (tid == 0) {  // the cost of the whole units
     const int64_t u = nw * P;
-    s_x = W;
+    s_x = cost;
     if (u < U) {
       const int b = find_last(a.unit0, a.B, u);
-      s_x = a.tile0[b] + (u - a.unit0[b]) * seq_tiles(tree_seq(a, b));
+      s_x = a.tile0[b] + (u - a.unit0[b]) * seq_tiles(tree_seq(a, b)) + kEndTiles * u;
     }
   }
   __syncthreads();
   for (int k = 0; k < warp; ++k) inc += s_w[k];
+  // The tile at which a running cost is reached.
+  const auto tile_at = [&](int64_t x) {
+    if (x >= cost) return W;
+    int lo = 0, hi = a.B;  // the last sequence whose cost begins at or before x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.tile0[mid] + kEndTiles * a.unit0[mid] <= x) lo = mid; else hi = mid;
+    }
+    const int64_t off = x - (a.tile0[lo] + kEndTiles * a.unit0[lo]);
+    const int K = seq_tiles(tree_seq(a, lo));
+    const int64_t m = off / (K + kEndTiles);
+    return a.tile0[lo] + m * K + min(off - m * (K + kEndTiles), (int64_t)K);
+  };
   if (tid == 0) {
     a.range0[P] = W;
     a.range0[P + 1] = nw;
@@ -175,7 +192,7 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a) {
   // Each pair's first segment, spelled out: every role of the split kernel starts with one load
   // instead of a search.
   if (tid < P) {
-    const int64_t x = min(s_x + inc - need, W), x1 = min(s_x + inc, W);
+    const int64_t x = tile_at(s_x + inc - need), x1 = tile_at(s_x + inc);
     a.range0[tid] = x;
     Seg g = {};
     g.b = -1;
