@@ -23,6 +23,7 @@
 //                 O_t += P_t V_j       8 x (M128 N128 K16), P from TMEM, V from smem.
 //               Order per key tile: PV_0(j-1), QK_0(j), PV_1(j-1), QK_1(j), so one
 //               softmax warpgroup works while the tensor core runs the other tile.
+//               Packed prompts: warps 1 and 3 issue, one for each query tile.
 //   warps 2, 3  only with the fused cache append: the unit that holds a new key tile on
 //               its diagonal writes it from shared memory into the caches (warp 2 the
 //               key sub-tiles, warp 3 the value sub-tiles, tensor stores issued as soon as
@@ -291,9 +292,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->kfull[i], 1);
       mbar_init(&bars->vfull[i], 1);
-      // With the fused append a tile's slots are also read by the cache writers.
-      mbar_init(&bars->kempty[i], p.append ? 2 : 1);
-      mbar_init(&bars->vempty[i], p.append ? 2 : 1);
+      // With the fused append a tile's slots are also read by the cache writers; packed: each
+      // query tile's issuer passes them on.
+      mbar_init(&bars->kempty[i], kPacked || p.append ? 2 : 1);
+      mbar_init(&bars->vempty[i], kPacked || p.append ? 2 : 1);
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
       mbar_init(&bars->s_full[i], 1);
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->o_done[i], 1);
       mbar_init(&bars->o_free[i], 4);
     }
-    mbar_init(&bars->mma_done, 1);
+    mbar_init(&bars->mma_done, kPacked ? 2 : 1);
     if (kPacked)
       for (int i = 0; i < 2; ++i) mbar_init(&bars->v_tail[i], 1);
     bars->abort_flag = 0;
@@ -472,6 +474,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         u += w.n * kSubPerKv;
         g += w.n;
       }
+    } else if (kPacked && (warp & 1)) {
+      // ================= MMA issuers, one per query tile =================
+      // Each tile's chain (scores, weights, mix) runs at its own pace, into the next unit as well:
+      // with few key tiles per unit the chains' latencies are what the kernel takes (32 prompts of
+      // up to 1024 rows 314 -> 302 us; long ones the same).  The ring is what bounds both chains:
+      // a tile's five slots are refilled when both have read them.
+      constexpr uint32_t kIdescQK = tc::idesc_bf16_f32(128, 128, false);
+      constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(128, 128, true);
+      constexpr uint32_t kSubLo = kSub >> 4;
+      const uint64_t dhi_k = tc::smem_desc_sw128(0, 16, 1024);
+      const uint64_t dhi_v_near = tc::smem_desc_sw128(0, kSub, 1024);
+      const uint64_t dhi_v_far = tc::smem_desc_sw128(0, (kSlots - 1) * kSub, 1024);
+      const int t = warp >> 1;
+      const uint32_t q_lo = (smem_u32(sQ) >> 4) + t * 3 * kSubLo;
+      const uint32_t ring_lo = smem_u32(sRing) >> 4;
+      const uint32_t s_tmem = tbase + t * 128, o_tmem = tbase + 256 + t * 128;
+      uint32_t g = 0;   // key tiles over the run
+      uint32_t st = 0;  // value mixes of this query tile over the run
+      bool ok = true;
+      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
+      for (int i = 0; ok; ++i) {
+        const int unit = unit_index<kPacked>(p, n_units, i);
+        if (unit < 0) break;
+        const Unit w = unit_make<kPacked>(p, unit, next);
+        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));
+        const int ntt = w.nt(t);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full[t], i & 1, p.status, abort_flag));
+        for (int j = 0; j <= w.n && ok; ++j) {
+          const uint32_t gk = g + (uint32_t)j, uk = gk * kSubPerKv;
+          if (j > 0) {  // O_t += P_t(j-1) V(j-1)
+            const uint32_t gv = gk - 1, uv = uk - 2u;
+            ok = mbar_wait(&bars->vfull[gv & 1], (gv >> 1) & 1, p.status, abort_flag);
+            if (j - 1 < ntt) {
+              ok = ok && mbar_wait(&bars->p_ready[t], st & 1, p.status, abort_flag);
+              if (ok && j == 1 && i > 0)
+                ok = mbar_wait(&bars->o_free[t], (i - 1) & 1, p.status, abort_flag);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc::fence_after_sync();
+              const uint32_t va = uv & (kSlots - 1), vb = (uv + 1) & (kSlots - 1);
+              const uint64_t vdesc = (vb > va ? dhi_v_near : dhi_v_far) |
+                                     (uint64_t)(ring_lo + min(va, vb) * kSubLo);
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  tc::mma_ts(o_tmem, s_tmem + kk * 8, vdesc + kk * (2048 >> 4), kIdescPV,
+                             kk > 0 || j > 1 ? 1u : 0u);
+                tc::commit(&bars->vempty[gv & 1]);
+                if (j == ntt) tc::commit(&bars->o_done[t]);
+              }
+              __syncwarp();
+              ++st;
+            } else {  // not this query tile's: passed on
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive(&bars->vempty[gv & 1]);
+            }
+          }
+          if (j < w.n) {  // S_t = Q_t K(j)^T over 192 columns
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->kfull[gk & 1], (gk >> 1) & 1, p.status,
+                                                   abort_flag));
+            if (!ok) break;
+            if (j < ntt) {
+              tc::fence_after_sync();
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 12; ++kk) {
+                  const uint32_t koff = (kk & 3) * (32 >> 4);
+                  const uint32_t klo = ring_lo + ((uk + (kk >> 2)) & (kSlots - 1)) * kSubLo;
+                  tc::mma_ss(s_tmem, dhi_k | (uint64_t)(q_lo + (kk >> 2) * kSubLo + koff),
+                             dhi_k | (uint64_t)(klo + koff), kIdescQK, kk > 0 ? 1u : 0u);
+                }
+                tc::commit(&bars->s_full[t]);
+                tc::commit(&bars->kempty[gk & 1]);
+                if (j == ntt - 1) tc::commit(&bars->q_empty[t]);
+              }
+              __syncwarp();
+            } else if (lane == 0) {
+              mbar_arrive(&bars->kempty[gk & 1]);
+            }
+          }
+        }
+        if (!ok) break;
+        if (ntt == 0) {  // a tile without rows still completes its phases, one unit at a time
+          ok = i == 0 || mbar_wait(&bars->o_free[t], (i - 1) & 1, p.status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive(&bars->q_empty[t]);
+            mbar_arrive(&bars->o_done[t]);
+          }
+        }
+        g += (uint32_t)w.n;
+      }
+      // No MMA may still be running when TMEM is released.
+      if (tc::elect_one()) tc::commit(&bars->mma_done);
+      __syncwarp();
+      drain_wait(&bars->mma_done, 0);
     } else if ((warp == 2 || warp == 3) && lane == 0 && p.append) {
       // ================= cache writers (fused append) =================
       // warp 2: the key sub-tiles of every tile (kfull / kempty), warp 3: the value
@@ -520,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       bulk_wait_all();  // the cache rows are written before the kernel ends
-    } else if (warp == 1) {
+    } else if (!kPacked && warp == 1) {
       // ================= MMA issuer =================
       // The whole warp runs this loop (waits, descriptor arithmetic: warp-uniform values);
       // one elected lane issues each batch of MMAs and commits.  Descriptors are built once
