@@ -269,8 +269,8 @@ struct VarlenArgs {
       v_head;
   const int32_t* cu_seqlens;
   uint16_t* out;
-  int4* pairs;   // workspace [varlen_max_pairs]: query tile pairs, most keys first
-  int* n_pairs;  // workspace [1]
+  int4* pairs;   // workspace [varlen_max_pairs]: query tile pairs in the order of their work
+  int* n_pairs;  // workspace [2]: their number, and a counter of the units handed out
   int* count;    // workspace [ceil(T / 256)]
   int* status;
   int B, T, H, Hkv;

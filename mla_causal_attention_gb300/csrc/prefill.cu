@@ -85,11 +85,13 @@ struct PrefillParams {
   int* status;
   int B, H, Tq, Tk, past_len, n_qb, n_kt;
   float scale_log2;
-  // Packed sequences only (kPacked): the query tile pairs of all sequences, most keys first, as
-  // {first row, length, tile pair, 0}, their number, and query heads per key/value head.  The
-  // maps are {128, T, heads} of the packed rows.
+  // Packed sequences only (kPacked): the query tile pairs of all sequences in the order in which
+  // they are done, as {first row, length, tile pair, 0}, their number, the number of units that
+  // have been taken beyond one per CTA, and query heads per key/value head.  The maps are
+  // {128, T, heads} of the packed rows.
   const int4* pairs;
   const int* n_pairs;
+  unsigned* taken;
   int group;
 };
 
@@ -114,6 +116,10 @@ struct Bars {
   uint64_t v_tail[2];
   uint32_t tmem_base;
   int abort_flag;
+  // Packed: unit i of the CTA, by its parity: {first row, length, tile pair, head or -1 behind the
+  // last}, written by the producer and read by the eleven other warps at work.
+  int4 unit[2];
+  uint64_t unit_full[2], unit_empty[2];
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
@@ -161,60 +167,55 @@ struct Unit {
   __device__ __forceinline__ int nt(int t) const { return t ? nt1 : nt0; }
 };
 
-// Packed: units in all (elsewhere they follow from the sizes).
-template <bool kPacked>
-__device__ __forceinline__ int64_t unit_count(const PrefillParams& p) {
-  return kPacked ? (int64_t)*p.n_pairs * p.H : 0;
-}
-
 // Unit index of the CTA's i-th unit, or -1 past the end.
-template <bool kPacked>
-__device__ __forceinline__ int unit_index(const PrefillParams& p, int64_t n_units, int i) {
+__device__ __forceinline__ int unit_index(const PrefillParams& p, int i) {
   const int G = gridDim.x;
   const int64_t k = (int64_t)i * G + ((i & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x);
-  return k < (kPacked ? n_units : (int64_t)p.B * p.H * p.n_qb) ? (int)k : -1;
+  return k < (int64_t)p.B * p.H * p.n_qb ? (int)k : -1;
 }
 
 // The only global load of a unit's description, which each role fetches one unit ahead: kv_len
-// of its sequence as stored (unclamped), or Tk without kv_len; packed: its entry of the pairs.
-template <bool kPacked>
-struct UnitSource {
-  int kv;
-};
-template <>
-struct UnitSource<true> {
-  int4 pair;
-};
+// of its sequence as stored (unclamped), or Tk without kv_len.
 __device__ __forceinline__ int unit_kv(const PrefillParams& p, int unit) {
   if (unit < 0 || !p.kv_len) return p.Tk;
   return p.kv_len[(unit % (p.B * p.H)) / p.H];
 }
-template <bool kPacked>
-__device__ __forceinline__ UnitSource<kPacked> unit_fetch(const PrefillParams& p, int unit) {
-  if constexpr (kPacked) {
-    UnitSource<true> s;
-    s.pair = unit < 0 ? make_int4(0, 0, 0, 0) : p.pairs[unit / p.H];
-    return s;
-  } else {
-    UnitSource<false> s;
-    s.kv = unit_kv(p, unit);
-    return s;
-  }
+
+// Packed units are handed out as CTAs come free (32 prompts of up to 1024 rows: the CTAs' times
+// differed by 20% in a fixed order).  The first of each CTA is its own index; the producer takes
+// the others from a counter, two units ahead of its loads, and tells the other warps.
+__device__ __forceinline__ int4 packed_unit(const PrefillParams& p, int64_t k, int64_t n_units) {
+  if (k >= n_units) return make_int4(0, 0, 0, -1);
+  const int pair = (int)(k / p.H);
+  int4 u = p.pairs[pair];
+  u.w = (int)(k - (int64_t)pair * p.H);
+  return u;
+}
+// By a whole warp: unit i of the CTA; false when the wait gave up.
+__device__ __forceinline__ bool packed_take(Bars* bars, int i, int4& u, int lane, int* status,
+                                            volatile int* abort_flag) {
+  const bool ok = __all_sync(
+      0xffffffffu, mbar_wait(&bars->unit_full[i & 1], (i >> 1) & 1, status, abort_flag));
+  if (!ok) return false;
+  u = bars->unit[i & 1];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bars->unit_empty[i & 1]);
+  return true;
 }
 
-template <bool kPacked>
-__device__ __forceinline__ Unit unit_make(const PrefillParams& p, int unit,
-                                          const UnitSource<kPacked>& src) {
+// src: kv_len as stored; packed: the unit as handed out.
+template <bool kPacked, typename Source>
+__device__ __forceinline__ Unit unit_make(const PrefillParams& p, int unit, const Source& src) {
   Unit w;
   int rows, past;  // query rows of the sequence, keys before them
   if constexpr (kPacked) {
-    w.bh = unit % p.H;
+    w.bh = src.w;
     w.b = 0;
     w.kvh = w.bh / p.group;
-    w.row0 = src.pair.x;
-    w.kvl = src.pair.y;
-    w.r0 = src.pair.z * 2 * kBM;
-    rows = src.pair.y;
+    w.row0 = src.x;
+    w.kvl = src.y;
+    w.r0 = src.z * 2 * kBM;
+    rows = src.y;
     past = 0;
   } else {
     const int BH = p.B * p.H;
@@ -224,7 +225,7 @@ __device__ __forceinline__ Unit unit_make(const PrefillParams& p, int unit,
     w.kvh = w.bh;
     w.row0 = 0;
     w.r0 = qb * 2 * kBM;
-    w.kvl = min(max(src.kv, 1), p.Tk);
+    w.kvl = min(max(src, 1), p.Tk);
     rows = p.Tq;
     past = p.past_len;
   }
@@ -286,7 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   if (kPacked) grid_dep_wait();  // the pairs are the kernel in front's
-  const int64_t n_units = unit_count<kPacked>(p);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -305,12 +305,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bars->mma_done, kPacked ? 2 : 1);
     if (kPacked)
-      for (int i = 0; i < 2; ++i) mbar_init(&bars->v_tail[i], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars->v_tail[i], 1);
+        mbar_init(&bars->unit_full[i], 1);
+        mbar_init(&bars->unit_empty[i], 11);  // two issuers, ends of sequences, softmax
+      }
     bars->abort_flag = 0;
     fence_barrier_init();
     // Out-of-range kv_len is reported once per CTA that meets it (and clamped).
     for (int i = 0; !kPacked; ++i) {
-      const int u = unit_index<kPacked>(p, n_units, i);
+      const int u = unit_index(p, i);
       if (u < 0) break;
       const int raw = unit_kv(p, u);
       if (raw < 1 || raw > p.Tk) {
@@ -376,13 +380,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       int q_units = 0;  // units whose Q transactions have been posted
       uint32_t tails[2] = {0, 0};  // packed: tiles that ended inside, by parity
       bool ok = true;
-      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
+      int next_kv = 0;
+      int4 here, next;  // packed: this unit and the next
+      int64_t n_units = 0, ahead = 0;  // .. and the one behind it
+      if constexpr (kPacked) {
+        n_units = (int64_t)*p.n_pairs * p.H;
+        next = packed_unit(p, blockIdx.x, n_units);
+        ahead = (int64_t)gridDim.x + atomicAdd(p.taken, 1u);
+      } else {
+        next_kv = unit_kv(p, unit_index(p, 0));
+      }
       for (int i = 0; ok; ++i) {
-        const int unit = unit_index<kPacked>(p, n_units, i);
-        if (unit < 0) break;
-        Unit w = unit_make<kPacked>(p, unit, next);
-        unit_skip_hidden<kMasked>(p, w);
-        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));  // fetched a unit ahead
+        Unit w;
+        if constexpr (kPacked) {
+          here = next;
+          if (i > 1)
+            ok = mbar_wait(&bars->unit_empty[i & 1], ((i >> 1) - 1) & 1, p.status, abort_flag);
+          if (!ok) break;
+          bars->unit[i & 1] = here;
+          mbar_arrive(&bars->unit_full[i & 1]);
+          if (here.w < 0) break;
+          w = unit_make<true>(p, 0, here);
+          next = packed_unit(p, ahead, n_units);
+          if (next.w >= 0) ahead = (int64_t)gridDim.x + atomicAdd(p.taken, 1u);
+        } else {
+          const int unit = unit_index(p, i);
+          if (unit < 0) break;
+          w = unit_make<false>(p, unit, next_kv);
+          unit_skip_hidden<kMasked>(p, w);
+          next_kv = unit_kv(p, unit_index(p, i + 1));
+        }
         ok = load_q(i, 0, w.r0, w.nt0, w.bh, w.row0);
         q_units = i + 1;
         for (int j = 0; j < w.n && ok; ++j, ++g, u += kSubPerKv) {
@@ -448,12 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // weight is zero, but zero times an infinity is not, so they are cleared.
       uint32_t u = 0, g = 0, tails[2] = {0, 0};
       bool ok = true;
-      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
-      for (int i = 0; ok; ++i) {
-        const int unit = unit_index<kPacked>(p, n_units, i);
-        if (unit < 0) break;
-        const Unit w = unit_make<kPacked>(p, unit, next);
-        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));
+      int4 next;
+      for (int i = 0;; ++i) {
+        ok = packed_take(bars, i, next, lane, p.status, abort_flag);
+        if (!ok || next.w < 0) break;
+        const Unit w = unit_make<true>(p, 0, next);
         if (w.n * kBN > w.kvl) {  // the unit's last tile
           const uint32_t ul = u + (w.n - 1) * kSubPerKv, gl = g + w.n - 1;
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_tail[gl & 1], tails[gl & 1] & 1,
@@ -493,12 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;   // key tiles over the run
       uint32_t st = 0;  // value mixes of this query tile over the run
       bool ok = true;
-      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
+      int4 next;
+      ok = packed_take(bars, 0, next, lane, p.status, abort_flag);
       for (int i = 0; ok; ++i) {
-        const int unit = unit_index<kPacked>(p, n_units, i);
-        if (unit < 0) break;
-        const Unit w = unit_make<kPacked>(p, unit, next);
-        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));
+        if (next.w < 0) break;
+        const Unit w = unit_make<true>(p, 0, next);
         const int ntt = w.nt(t);
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full[t], i & 1, p.status, abort_flag));
         for (int j = 0; j <= w.n && ok; ++j) {
@@ -554,6 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if (lane == 0) {
               mbar_arrive(&bars->kempty[gk & 1]);
             }
+            // The next unit, while this one's last weights are computed.
+            if (j == w.n - 1) ok = packed_take(bars, i + 1, next, lane, p.status, abort_flag);
           }
         }
         if (!ok) break;
@@ -584,13 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool keys = warp == 2;
       uint32_t u = 0, g = 0;
       bool ok = true;
-      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
+      int next = unit_kv(p, unit_index(p, 0));
       for (int i = 0; ok; ++i) {
-        const int unit = unit_index<kPacked>(p, n_units, i);
+        const int unit = unit_index(p, i);
         if (unit < 0) break;
-        Unit w = unit_make<kPacked>(p, unit, next);
+        Unit w = unit_make<false>(p, unit, next);
         unit_skip_hidden<kMasked>(p, w);
-        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));
+        next = unit_kv(p, unit_index(p, i + 1));
         const int qt0 = w.r0 / kBM;  // the unit's first query tile
         for (int j = 0; j < w.n && ok; ++j, ++g, u += kSubPerKv) {
           const int kt = j + w.js;          // key tile
@@ -639,13 +666,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;             // key tiles consumed over the run
       uint32_t stp[2] = {0, 0};   // value mixes issued per tile over the run
       bool ok = true;
-      auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
+      int next = unit_kv(p, unit_index(p, 0));
       for (int i = 0; ok; ++i) {
-        const int unit = unit_index<kPacked>(p, n_units, i);
+        const int unit = unit_index(p, i);
         if (unit < 0) break;
-        Unit w = unit_make<kPacked>(p, unit, next);
+        Unit w = unit_make<false>(p, unit, next);
         unit_skip_hidden<kMasked>(p, w);
-        next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));  // fetched a unit ahead
+        next = unit_kv(p, unit_index(p, i + 1));  // fetched a unit ahead
         for (int j = 0; j <= w.n && ok; ++j) {
           const uint32_t gk = g + (uint32_t)j;           // key tile j of this unit
           const uint32_t uk = gk * kSubPerKv;            // its sub-tiles: uk .. uk+2
@@ -760,13 +787,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = p.scale_log2;
     uint32_t st = 0;  // score steps of this tile over the run
     bool ok = true;
-    auto next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, 0));
+    int next_kv = 0;
+    int4 next;
+    if constexpr (kPacked)
+      ok = packed_take(bars, 0, next, lane, p.status, abort_flag);
+    else
+      next_kv = unit_kv(p, unit_index(p, 0));
     for (int i = 0; ok; ++i) {
-      const int unit = unit_index<kPacked>(p, n_units, i);
-      if (unit < 0) break;
-      Unit w = unit_make<kPacked>(p, unit, next);
-      unit_skip_hidden<kMasked>(p, w);
-      next = unit_fetch<kPacked>(p, unit_index<kPacked>(p, n_units, i + 1));  // fetched a unit ahead
+      Unit w;
+      if constexpr (kPacked) {
+        if (next.w < 0) break;
+        w = unit_make<true>(p, 0, next);
+      } else {
+        const int unit = unit_index(p, i);
+        if (unit < 0) break;
+        w = unit_make<false>(p, unit, next_kv);
+        unit_skip_hidden<kMasked>(p, w);
+        next_kv = unit_kv(p, unit_index(p, i + 1));  // fetched a unit ahead
+      }
       const int ntt = w.nt(t);
       const int qi = w.r0 + t * kBM + tw;  // query row within the sequence
       const int limit = min(qi + (kPacked ? 0 : p.past_len) + 1, w.kvl);  // keys [0, limit) are visible
@@ -886,6 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #endif
         if (lane == 0 && !withhold) mbar_arrive(&bars->p_ready[t]);
       }
+      if (kPacked && ok) ok = packed_take(bars, i + 1, next, lane, p.status, abort_flag);
       if (!ok) break;
       // The unit's output: wait for the last value mix, move O_t to registers, release
       // O_t for the next unit, then normalise and store.
@@ -1243,7 +1282,10 @@ __global__ void __launch_bounds__(kPlanThreads) packed_pairs_kernel(const Varlen
   }
   // Offsets that fall can make sequences overlap, and more pairs than there is room for.
   const int most = (int)min(varlen_max_pairs(a.T, a.B), (int64_t)0x7fffffff);
-  if (tid == 0) *a.n_pairs = min(place, most);
+  if (tid == 0) {
+    a.n_pairs[0] = min(place, most);
+    a.n_pairs[1] = 0;  // units taken
+  }
   __syncthreads();
   // A warp per sequence, lanes over its pairs, the last one first.
   for (int b = warp; b < a.B; b += kPlanThreads / 32) {
@@ -1317,6 +1359,7 @@ cudaError_t launch_varlen(const VarlenArgs& a, cudaStream_t stream) {
   if (!packed_maps(a, &p)) return cudaErrorInvalidValue;
   p.pairs = a.pairs;
   p.n_pairs = a.n_pairs;
+  p.taken = reinterpret_cast<unsigned*>(a.n_pairs) + 1;
   p.group = a.H / a.Hkv;
   p.out = a.out;
   p.status = a.status;
