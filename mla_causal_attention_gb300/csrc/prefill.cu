@@ -116,7 +116,7 @@ struct Bars {
   uint64_t v_tail[2];
   uint32_t tmem_base;
   int abort_flag;
-  // Packed: unit i of the CTA, by its parity: {first row, length, tile pair, head or -1 behind the
+  // Packed: unit i > 0 of the CTA, by its parity: {first row, length, tile pair, head or -1 behind the
   // last}, written by the producer and read by the eleven other warps at work.
   int4 unit[2];
   uint64_t unit_full[2], unit_empty[2];
@@ -191,11 +191,19 @@ __device__ __forceinline__ int4 packed_unit(const PrefillParams& p, int64_t k, i
   u.w = (int)(k - (int64_t)pair * p.H);
   return u;
 }
-// By a whole warp: unit i of the CTA; false when the wait gave up.
+__device__ __forceinline__ int4 packed_first(const PrefillParams& p, int64_t& n_units) {
+  // There is room for every CTA's first pair, whether the batch has it or not: one wait.
+  const int pairs = *p.n_pairs;
+  int4 u = packed_unit(p, blockIdx.x, gridDim.x);
+  n_units = (int64_t)pairs * p.H;
+  if (blockIdx.x >= n_units) u.w = -1;
+  return u;
+}
+// By a whole warp: unit i > 0 of the CTA; false when the wait gave up.
 __device__ __forceinline__ bool packed_take(Bars* bars, int i, int4& u, int lane, int* status,
                                             volatile int* abort_flag) {
   const bool ok = __all_sync(
-      0xffffffffu, mbar_wait(&bars->unit_full[i & 1], (i >> 1) & 1, status, abort_flag));
+      0xffffffffu, mbar_wait(&bars->unit_full[i & 1], ((i - 1) >> 1) & 1, status, abort_flag));
   if (!ok) return false;
   u = bars->unit[i & 1];
   __syncwarp();
@@ -375,6 +383,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_3d(dst + 2 * kSub, &p.tm_qr, &bars->q_full[t], 0, rt, bh, pol_q);
         return true;
       };
+      // Packed: unit i > 0 for the other warps, once they have all read unit i - 2.
+      auto tell = [&](int i, const int4& unit) -> bool {
+        if (i > 2 &&
+            !mbar_wait(&bars->unit_empty[i & 1], ((i - 3) >> 1) & 1, p.status, abort_flag))
+          return false;
+        bars->unit[i & 1] = unit;
+        mbar_arrive(&bars->unit_full[i & 1]);
+        return true;
+      };
       uint32_t u = 0;   // ring sub-tiles issued over the run
       uint32_t g = 0;   // key tiles issued over the run
       int q_units = 0;  // units whose Q transactions have been posted
@@ -384,8 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int4 here, next;  // packed: this unit and the next
       int64_t n_units = 0, ahead = 0;  // .. and the one behind it
       if constexpr (kPacked) {
-        n_units = (int64_t)*p.n_pairs * p.H;
-        next = packed_unit(p, blockIdx.x, n_units);
+        next = packed_first(p, n_units);
         ahead = (int64_t)gridDim.x + atomicAdd(p.taken, 1u);
       } else {
         next_kv = unit_kv(p, unit_index(p, 0));
@@ -394,11 +410,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit w;
         if constexpr (kPacked) {
           here = next;
-          if (i > 1)
-            ok = mbar_wait(&bars->unit_empty[i & 1], ((i >> 1) - 1) & 1, p.status, abort_flag);
-          if (!ok) break;
-          bars->unit[i & 1] = here;
-          mbar_arrive(&bars->unit_full[i & 1]);
           if (here.w < 0) break;
           w = unit_make<true>(p, 0, here);
           next = packed_unit(p, ahead, n_units);
@@ -437,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Q_0 and K(0).
           if (j == 0) {
             ok = load_q(i, 1, w.r0, w.nt1, w.bh, w.row0);
+            if (kPacked && ok) ok = tell(i + 1, next);
             if (!ok) break;
           }
           // V(j): columns 0-63 go to the lower-addressed of its two slots, so one MMA with
@@ -475,9 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // weight is zero, but zero times an infinity is not, so they are cleared.
       uint32_t u = 0, g = 0, tails[2] = {0, 0};
       bool ok = true;
-      int4 next;
+      int64_t n_units;
+      int4 next = packed_first(p, n_units);
       for (int i = 0;; ++i) {
-        ok = packed_take(bars, i, next, lane, p.status, abort_flag);
+        if (i > 0) ok = packed_take(bars, i, next, lane, p.status, abort_flag);
         if (!ok || next.w < 0) break;
         const Unit w = unit_make<true>(p, 0, next);
         if (w.n * kBN > w.kvl) {  // the unit's last tile
@@ -519,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;   // key tiles over the run
       uint32_t st = 0;  // value mixes of this query tile over the run
       bool ok = true;
-      int4 next;
-      ok = packed_take(bars, 0, next, lane, p.status, abort_flag);
+      int64_t n_units;
+      int4 next = packed_first(p, n_units);
       for (int i = 0; ok; ++i) {
         if (next.w < 0) break;
         const Unit w = unit_make<true>(p, 0, next);
@@ -788,9 +801,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t st = 0;  // score steps of this tile over the run
     bool ok = true;
     int next_kv = 0;
+    int64_t n_units;
     int4 next;
     if constexpr (kPacked)
-      ok = packed_take(bars, 0, next, lane, p.status, abort_flag);
+      next = packed_first(p, n_units);
     else
       next_kv = unit_kv(p, unit_index(p, 0));
     for (int i = 0; ok; ++i) {
@@ -1220,10 +1234,10 @@ namespace {
 // The order in which the query tile pairs of all sequences are done, by one block: a counting sort
 // (pairs with the same key come in any order, which changes when a unit runs and nothing else).
 // While no sequence is longer than kBySequence pairs: the longest sequences first, all pairs of
-// one together, so that they find its keys and values in L2 (32 prompts of up to 1024 rows: 307
-// us, and 325 in the other order, where each pair reads them from HBM).  Otherwise the pairs
+// one together, so that they find its keys and values in L2 (32 prompts of up to 1024 rows: 290
+// us, and 308 in the other order, where each pair reads them from HBM).  Otherwise the pairs
 // with the most keys first, wherever they are from, so that all SMs end together (4 prompts of
-// 2048 to 4096 rows: 597 us, and 653 sequence by sequence).
+// 2048 to 4096 rows: 597 us, and 606 sequence by sequence).
 constexpr int kBySequence = 4;
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) packed_pairs_kernel(const VarlenArgs a) {
