@@ -455,7 +455,8 @@ MLA_API mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k
  *   c_pages, pe_pages, block_table [B, max_pages], cu_q [B + 1], kv_len [B]    as above
  *   draft_mask [T] int64 or NULL        w_kvb [H * 256, 512] bf16
  * Only the entries of the block table below ceil(kv_len[b] / page_size) are read.
- * H up to 1024, T * H up to 2^26, max_pages * page_size up to 2^30; workspace mla_latent_tree_workspace_bytes(T, H, B) bytes, zeroed once.
+ * H up to 1024, T * H up to 2^26, max_pages * page_size up to 2^30; workspace
+ * mla_latent_tree_workspace_bytes(T, H, B) bytes, zeroed once.
  * Device-side problems (the call completes): cu_q not rising within [0, T], kv_len[b] below n
  * or past max_pages * page_size (MLA_ERR_KVLEN, clamped); a page outside the pool
  * (MLA_ERR_PAGE, read as zeros); n > 64 with draft_mask (MLA_ERR_TREE: the keys past 64 are
