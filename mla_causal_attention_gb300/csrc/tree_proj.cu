@@ -37,7 +37,7 @@ constexpr int kMaxSlots = 5;          // ring of the rows' sub-tiles: 5, or 3 wi
 constexpr int kOffRing = 8 * kSub;    // staging behind it; behind the weight's 8 sub-tiles
 constexpr int kOffBar = kOffRing + kMaxSlots * kSub;
 constexpr int kSmem = kOffBar + 256 + 1024;
-static_assert(kSmem <= 232448, "shared memory per block");
+static_assert(kSmem <= 232448 && kPartSmem <= kSmem, "shared memory per block");
 
 struct ProjParams {
   CUtensorMap tm_x;  // rows    {K, T, H}, boxes {64, 128, 1}
@@ -156,11 +156,11 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
   constexpr uint32_t kSlots = kUp ? 5 : 3;
   grid_dep_launch();
   const TreeArgs& a = p.a;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
   if (!kUp && blockIdx.x == gridDim.x - 1) {
-    tree_partition(a);
+    tree_partition(a, smem_raw);
     return;
   }
-  extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sW = smem;
   uint8_t* sX = smem + kOffRing;
