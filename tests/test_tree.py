@@ -33,9 +33,12 @@ def _run(d, **kw):
     return out
 
 
-def _close(got, d):
-    used = int(d["cu_q"][-1])
+def _close(got, d, rows=None):
+    """rows: got's rows are these of the case."""
+    used = int(d["cu_q"][-1]) if rows is None else len(rows)
     ref, spread, mixed = tree_reference(d, SCALE)
+    if rows is not None:
+        ref, spread, mixed = ref[rows], spread[rows], mixed[rows]
     err = (got.double() - ref).abs()[:used]
     if used == 0:
         return
@@ -255,6 +258,29 @@ def test_many_empty_sequences():
     cu[0], cu[-1] = 0, int(d["cu_q"][2])
     want = _run(d)
     assert torch.equal(_run(dict(d, block_table=table, kv_len=kv, cu_q=cu)), want)
+    assert mla.mla_attn_get_status() == 0
+
+
+@pytest.mark.parametrize("B", [1025, 8192, 8193, 20000])
+def test_many_short_sequences(B):
+    """Copies of six sequences, one of them without new tokens, as many as the partition's searches
+    in shared memory take, and more."""
+    d = tree_case(18, 6, 2, (0, 300), (1, 3), 16, True)
+    cu = d["cu_q"].tolist()
+    pick = [(5 * b + b // 7) % 6 for b in range(B)]
+    none = 3  # its copies ask for nothing
+    rows, cu_all, kv = [], [0], []
+    for b in pick:
+        n = 0 if b == none else cu[b + 1] - cu[b]
+        rows += range(cu[b], cu[b] + n)
+        cu_all.append(len(rows))
+        kv.append(int(d["kv_len"][b]))
+    rows = torch.tensor(rows, device="cuda")
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    e = dict(d, block_table=d["block_table"][pick].contiguous(), kv_len=i(kv), cu_q=i(cu_all))
+    for k in ("q_nope", "q_pe", "draft_mask"):
+        e[k] = d[k][rows].contiguous()
+    _close(_run(e), d, rows)
     assert mla.mla_attn_get_status() == 0
 
 
