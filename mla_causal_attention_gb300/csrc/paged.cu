@@ -139,25 +139,43 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
     if (tid == 0) s_tok[kPlanChunk] = tok;
     __syncthreads();
 
-    // Per sequence: cu_q, kv_len and the fresh table entries.  A single chunk is shared by
-    // sequence among all blocks; one warp per sequence, its lanes over the pages taken.
-    if (rows_mine) {
-      const int first = a.B <= kPlanChunk ? blockIdx.x * (kPlanThreads / 32) + warp : warp;
-      const int step = (a.B <= kPlanChunk ? gridDim.x : 1) * (kPlanThreads / 32);
-      for (int i = first; i < nb; i += step) {
-        const int have = pages_of(a, s_ctx[i]), take = pages_of(a, s_kv[i]) - have;
-        if (lane == 0) {
-          a.cu_q[b0 + i] = (int)min(s_tok[i], (int64_t)a.T);
-          a.kv_len[b0 + i] = s_kv[i];
-        }
-        int32_t* row = a.block_table + (int64_t)(b0 + i) * a.max_pages + have;
-        bool none = false;
-        for (int k = lane; k < take; k += 32) {
-          const int page = plan_page(a, head, s_pg[i] + k);
-          row[k] = page;
-          none |= page < 0;
-        }
-        if (none) set_status(a.status, MLA_ERR_PAGE);
+    // Per sequence: cu_q, kv_len and the fresh table entries.
+    const auto take_of = [&](int i) { return pages_of(a, s_kv[i]) - pages_of(a, s_ctx[i]); };
+    const auto lengths = [&](int i) {
+      a.cu_q[b0 + i] = (int)min(s_tok[i], (int64_t)a.T);
+      a.kv_len[b0 + i] = s_kv[i];
+    };
+    const auto fill = [&](int i, int k0, int step) {  // entries k0, k0 + step, ..
+      const int have = pages_of(a, s_ctx[i]), take = pages_of(a, s_kv[i]) - have;
+      int32_t* row = a.block_table + (int64_t)(b0 + i) * a.max_pages + have;
+      bool none = false;
+      for (int k = k0; k < take; k += step) {
+        const int page = plan_page(a, head, s_pg[i] + k);
+        row[k] = page;
+        none |= page < 0;
+      }
+      if (none) set_status(a.status, MLA_ERR_PAGE);
+    };
+    if (a.B <= kPlanChunk) {
+      // A single chunk is shared among the warps of all blocks, several to a sequence where its
+      // table is long (a sequence of a million tokens: 9 us, 85 by one warp).
+      const int w = blockIdx.x * (kPlanThreads / 32) + warp;
+      const int warps = gridDim.x * (kPlanThreads / 32);
+      const int parts = max(min(warps / nb, (a.max_pages + 255) / 256), 1);
+      for (int i = w; i < nb * parts; i += warps) {
+        if (i < nb && lane == 0) lengths(i);
+        fill(i % nb, i / nb * 32 + lane, parts * 32);
+      }
+    } else if (rows_mine) {
+      // Of many sequences most take few pages: a thread each, and the whole warp for the others
+      // (4096 of one token: 15 us, 35 with a warp each).
+      for (int i0 = 0; i0 < nb; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        const bool few = i < nb && take_of(i) <= 4;
+        if (i < nb) lengths(i);
+        if (few) fill(i, 0, 1);
+        for (uint32_t m = __ballot_sync(0xffffffffu, i < nb && !few); m != 0; m &= m - 1)
+          fill(i0 + warp * 32 + __ffs(m) - 1, lane, 32);
       }
     }
 

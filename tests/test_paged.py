@@ -53,6 +53,8 @@ def _same(p, t, want):
     (1025, (0, 50), (0, 5), 16, True),       # one sequence past a scan's 1024
     (5000, (0, 20), (0, 3), 1024, False),    # several scans
     (7, (0, 5000), (1, 6000), 16, False),    # tokens of a sequence over many blocks
+    (1500, (0, 50), (0, 200), 16, False),    # several scans, few and many pages per sequence
+    (2, (0, 10), (20000, 30000), 16, False),  # a table row over many blocks
 ])
 def test_plan(B, ctx, new, page, tree):
     r, c, n, table, free, num = random_batch(B + page, B, ctx, new, page)
