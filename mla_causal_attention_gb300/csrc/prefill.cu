@@ -1301,17 +1301,25 @@ __global__ void __launch_bounds__(kPlanThreads) packed_pairs_kernel(const Varlen
     a.n_pairs[1] = 0;  // units taken
   }
   __syncthreads();
-  // A warp per sequence, lanes over its pairs, the last one first.
-  for (int b = warp; b < a.B; b += kPlanThreads / 32) {
-    int row0;
-    const int n = seq(b, row0), last = (n - 1) / (2 * kBM);
-    if (n == 0) continue;
-    int first = 0;
-    if (whole && lane == 0) first = atomicAdd(&a.count[last], last + 1);
-    first = __shfl_sync(0xffffffffu, first, 0);
-    for (int k = lane; k <= last; k += 32) {
-      const int at = whole ? first + k : atomicAdd(&a.count[last - k], 1);
-      if (at < most) a.pairs[at] = make_int4(row0, n, last - k, 0);
+  // A thread per sequence, its last pair first; a whole warp for one of many pairs.
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int row0 = 0;
+    const int n = b < a.B ? seq(b, row0) : 0, last = n > 0 ? (n - 1) / (2 * kBM) : -1;
+    const int first = whole && n > 0 ? atomicAdd(&a.count[last], last + 1) : 0;
+    const bool many = last >= kBySequence;
+    if (!many)
+      for (int k = 0; k <= last; ++k) {
+        const int at = whole ? first + k : atomicAdd(&a.count[last - k], 1);
+        if (at < most) a.pairs[at] = make_int4(row0, n, last - k, 0);
+      }
+    for (uint32_t m = __ballot_sync(0xffffffffu, many); m != 0; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      const int r = __shfl_sync(0xffffffffu, row0, src), len = __shfl_sync(0xffffffffu, n, src);
+      for (int q = (len - 1) / (2 * kBM) - lane; q >= 0; q -= 32) {
+        const int at = atomicAdd(&a.count[q], 1);  // !whole: the longest has more pairs
+        if (at < most) a.pairs[at] = make_int4(r, len, q, 0);
+      }
     }
   }
 }

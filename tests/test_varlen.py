@@ -89,6 +89,8 @@ def _close(got, d, seqs=None):
     ([64] * 40, 8, 8, False),
     ([1] * 300, 4, 2, True),                 # more sequences than CTAs
     ([0, 0], 4, 4, False),                   # nothing to do
+    ([2, 0, 1] * 500, 2, 1, True),           # more sequences than threads that list their tiles
+    ([3] * 40 + [1500] + [5, 0] * 600 + [1100, 700], 2, 2, False),  # long ones among them
 ])
 def test_varlen_matches_definition(ns, H, Hkv, fused):
     d = _case(len(ns) * 100 + H, ns, H, Hkv, fused, pad=5)
