@@ -170,17 +170,23 @@ class Workspace:
 
     A workspace serves one stream at a time: calls that may overlap on the GPU (on
     different streams) need workspaces of their own.  The default one, used when a call
-    gets none, is shared by every call on its device.
+    gets none, is shared by every call on its device.  A buffer that was outgrown is kept,
+    since a captured graph may go on using it; growth is at least twofold, so that the kept
+    ones together are smaller than the one in use.
     """
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self.outgrown = []
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         """The buffer, at least nbytes long.  A new buffer is allocated and zero-filled on
         `stream` (the one the call launches on), so the fill precedes the call's kernels."""
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.buf is not None:
+                self.outgrown.append(self.buf)
+                nbytes = max(nbytes, 2 * self.buf.numel())
             with torch.cuda.stream(stream):
                 self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         return self.buf
@@ -703,9 +709,12 @@ def mla_attn_get_status(workspace: Workspace | None = None, device=None, stream=
     """Synchronise and read/clear the device status word (0 = no device-side error)."""
     dev = torch.device(device or "cuda")
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    ws = (workspace or _default_workspace(dev)).get(256, stream=s)
+    ws = workspace or _default_workspace(dev)
+    bufs = [ws.get(256, stream=s), *ws.outgrown]  # each has a status word of its own
     with torch.cuda.device(dev):
-        return int(library().mla_attn_get_status(_ptr(ws), ctypes.c_void_p(s.cuda_stream)))
+        codes = [int(library().mla_attn_get_status(_ptr(b), ctypes.c_void_p(s.cuda_stream)))
+                 for b in bufs]
+    return next((c for c in codes if c != 0), 0)
 
 
 _default_ws: dict = {}

@@ -212,3 +212,15 @@ def test_varlen_refuses_strides_and_alignment(lib, base):
     if not torch.cuda.is_available():
         a = _varlen_args(base, lib)
         assert lib.mla_attn_varlen_fwd(*[a[n] for n in VARLEN]) in _no_device()
+
+
+def test_an_outgrown_workspace_is_kept():
+    """A captured graph may still use it."""
+    ws = binding.Workspace("cpu")
+    first = ws.get(300)
+    at = first.data_ptr()
+    assert first.numel() == 300 and ws.get(200) is first
+    del first
+    second = ws.get(400)
+    assert second.numel() == 600 and [b.data_ptr() for b in ws.outgrown] == [at]
+    assert ws.get(10000).numel() == 10000 and ws.outgrown[1] is second

@@ -153,3 +153,36 @@ def test_two_streams_at_once():
         assert torch.equal(o, w)
     for w in spaces:
         assert mla.mla_attn_get_status(workspace=w) == 0
+
+
+def test_a_graph_outlives_its_workspace_growing():
+    """A graph captured with the default workspace, then larger calls, then the graph again."""
+    from paged_helpers import tree_case
+    small = tree_case(62, 3, 8, (100, 400), (1, 9), 32, True)
+    large = tree_case(63, 30, 64, (0, 300), (1, 40), 32, True)
+
+    def call(d, **kw):
+        return mla.mla_latent_tree_fwd(d["q_nope"], d["q_pe"], d["c_pages"], d["pe_pages"],
+                                       d["block_table"], d["kv_len"], d["cu_q"], d["draft_mask"],
+                                       d["w_kvb"], SCALE, **kw)
+
+    ws = mla.Workspace()
+    want = call(small, workspace=ws).clone()
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(small, out=out, workspace=ws)
+    call(large, workspace=ws)
+    assert len(ws.outgrown) == 1
+    other = torch.full_like(ws.outgrown[0], 255)  # where the first buffer would have been reused
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert bool((other == 255).all())
+    small["kv_len"][0] = 0  # below its new tokens: in the status word of the captured call's buffer
+    g.replay()
+    assert mla.mla_attn_get_status(workspace=ws) == mla.MlaStatus.ERR_KVLEN
+    assert mla.mla_attn_get_status(workspace=ws) == 0
