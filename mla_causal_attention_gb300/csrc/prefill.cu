@@ -23,7 +23,9 @@
 //                 O_t += P_t V_j       8 x (M128 N128 K16), P from TMEM, V from smem.
 //               Order per key tile: PV_0(j-1), QK_0(j), PV_1(j-1), QK_1(j), so one
 //               softmax warpgroup works while the tensor core runs the other tile.
-//               Packed prompts: warps 1 and 3 issue, one for each query tile.
+//               Packed prompts: warps 1 and 3 issue, one for each query tile, warp 2 clears
+//               the value rows behind a prompt's end, and units are handed out as CTAs come
+//               free.
 //   warps 2, 3  only with the fused cache append: the unit that holds a new key tile on
 //               its diagonal writes it from shared memory into the caches (warp 2 the
 //               key sub-tiles, warp 3 the value sub-tiles, tensor stores issued as soon as
