@@ -338,8 +338,9 @@ MLA_API mla_status mla_attn_rope_append_fwd(const uint16_t* q_nope, const uint16
  * empty; rows from cu_seqlens[B] on are padding, and out is left as it was there.  Another
  * sequence's rows never reach a result, whatever they hold.
  * Offsets that are not rising within [0, T] are clamped (MLA_ERR_KVLEN in the status word; what
- * their sequences get is not meaningful).  Workspace: mla_attn_varlen_workspace_bytes(T, B),
- * zeroed once.
+ * their sequences get is not meaningful, and where falling offsets make sequences overlap beyond
+ * T / 256 + min(B, T) pairs of 128-row tiles, the sequences behind get nothing).  Workspace:
+ * mla_attn_varlen_workspace_bytes(T, B), zeroed once.
  */
 typedef struct {
   int64_t q_nope_row, q_nope_head, q_pe_row, q_pe_head;

@@ -1244,31 +1244,39 @@ constexpr int kBySequence = 4;
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) packed_pairs_kernel(const VarlenArgs a) {
   grid_dep_launch();
-  __shared__ int s_warp[kPlanThreads / 32], s_top;
+  __shared__ int s_warp[kPlanThreads / 32], s_top, s_end;
+  __shared__ bool s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int classes = (a.T + 2 * kBM - 1) / (2 * kBM);
-  for (int q = tid; q < classes; q += kPlanThreads) a.count[q] = 0;
-  if (tid == 0) s_top = 0;
-  __syncthreads();
+  // What the list has room for: at most 2^24 + 2^18.
+  const int most = (int)varlen_max_pairs(a.T, a.B);
+  if (tid == 0) s_bad = false;
   const auto seq = [&](int b, int& row0) {  // offsets clamped to the buffer
     const int c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1];
     row0 = min(max(c0, 0), a.T);
     const int n = min(max(c1, row0), a.T) - row0;
-    if (row0 != c0 || row0 + n != c1) set_status(a.status, MLA_ERR_KVLEN);
+    if (row0 != c0 || row0 + n != c1) {
+      s_bad = true;
+      set_status(a.status, MLA_ERR_KVLEN);
+    }
     return n;
   };
-  // count[q]: sequences whose last pair is q
-  for (int b = tid; b < a.B; b += kPlanThreads) {
-    int row0;
-    const int n = seq(b, row0);
-    if (n > 0) {
-      atomicAdd(&a.count[(n - 1) / (2 * kBM)], 1);
-      atomicMax(&s_top, (n - 1) / (2 * kBM) + 1);
+  // count[q]: sequences, of the first B, whose last pair is q
+  const auto count_to = [&](int B) {
+    for (int q = tid; q < classes; q += kPlanThreads) a.count[q] = 0;
+    if (tid == 0) s_top = 0;
+    __syncthreads();
+    for (int b = tid; b < B; b += kPlanThreads) {
+      int row0;
+      const int n = seq(b, row0);
+      if (n > 0) {
+        atomicAdd(&a.count[(n - 1) / (2 * kBM)], 1);
+        atomicMax(&s_top, (n - 1) / (2 * kBM) + 1);
+      }
     }
-  }
-  __syncthreads();
-  const bool whole = s_top <= kBySequence;
-  // Running sums from the top class down, 1024 classes at a time (all threads take part).
+    __syncthreads();
+  };
+  // Running sums, 1024 values at a time (all threads take part).
   const auto scan = [&](int x, int& total) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1285,8 +1293,30 @@ __global__ void __launch_bounds__(kPlanThreads) packed_pairs_kernel(const Varlen
     }
     return x;
   };
+  int B = a.B;
+  count_to(B);
+  // Sequences between rising offsets share no row and have at most `most` pairs.  Offsets that fall
+  // can make any number of sequences overlap, with more pairs than the list, a 32-bit sum and a
+  // reasonable time hold: then only the first sequences count, as many as there is room for.
+  if (s_bad) {
+    int total = 0;  // below most + 1024 * 2^18 < 2^31 behind the last round
+    for (int b0 = 0; b0 < a.B && total <= most; b0 += kPlanThreads) {
+      const int b = b0 + tid;
+      int row0;
+      const int n = b < a.B ? seq(b, row0) : 0, own = (n + 2 * kBM - 1) / (2 * kBM);
+      const int upto = scan(own, total);
+      if (upto > most && upto - own <= most) s_end = b;
+    }
+    __syncthreads();
+    if (total > most) {
+      B = s_end;
+      count_to(B);
+    }
+  }
+  const bool whole = s_top <= kBySequence;
   // count[q] becomes the first place of class q: behind the pairs of all sequences of more pairs
-  // (whole), or behind the pairs above q, one for each sequence that has it.
+  // (whole), or behind the pairs above q, one for each sequence that has it.  From the top class
+  // down.
   int seqs = 0, place = 0;
   for (int top = s_top; top > 0; top -= kPlanThreads) {
     const int q = top - 1 - tid;
@@ -1296,31 +1326,29 @@ __global__ void __launch_bounds__(kPlanThreads) packed_pairs_kernel(const Varlen
     const int upto = scan(add, place);
     if (q >= 0) a.count[q] = upto - add;
   }
-  // Offsets that fall can make sequences overlap, and more pairs than there is room for.
-  const int most = (int)min(varlen_max_pairs(a.T, a.B), (int64_t)0x7fffffff);
   if (tid == 0) {
-    a.n_pairs[0] = min(place, most);
+    a.n_pairs[0] = place;
     a.n_pairs[1] = 0;  // units taken
   }
   __syncthreads();
   // A thread per sequence, its last pair first; a whole warp for one of many pairs.
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     int row0 = 0;
-    const int n = b < a.B ? seq(b, row0) : 0, last = n > 0 ? (n - 1) / (2 * kBM) : -1;
+    const int n = b < B ? seq(b, row0) : 0, last = n > 0 ? (n - 1) / (2 * kBM) : -1;
     const int first = whole && n > 0 ? atomicAdd(&a.count[last], last + 1) : 0;
     const bool many = last >= kBySequence;
     if (!many)
       for (int k = 0; k <= last; ++k) {
         const int at = whole ? first + k : atomicAdd(&a.count[last - k], 1);
-        if (at < most) a.pairs[at] = make_int4(row0, n, last - k, 0);
+        a.pairs[at] = make_int4(row0, n, last - k, 0);
       }
     for (uint32_t m = __ballot_sync(0xffffffffu, many); m != 0; m &= m - 1) {
       const int src = __ffs(m) - 1;
       const int r = __shfl_sync(0xffffffffu, row0, src), len = __shfl_sync(0xffffffffu, n, src);
       for (int q = (len - 1) / (2 * kBM) - lane; q >= 0; q -= 32) {
         const int at = atomicAdd(&a.count[q], 1);  // !whole: the longest has more pairs
-        if (at < most) a.pairs[at] = make_int4(r, len, q, 0);
+        a.pairs[at] = make_int4(r, len, q, 0);
       }
     }
   }

@@ -219,3 +219,37 @@ def test_results_are_the_same_every_time():
             if i % 3 == 0:
                 ws.buf[256:].random_(0, 255)
             assert torch.equal(_run(d, workspace=ws), want), (k, i)
+
+
+def test_offsets_that_fall_over_and_over():
+    """Sequences that overlap, with more pairs of query tiles together than rising offsets can have:
+    the first ones count, as many as the list has room for."""
+    mla.mla_attn_get_status()
+    d = _case(11, [600], 4, 2, False)
+    want = _run(d)
+    e = dict(d, cu_seqlens=torch.tensor([0, 600] * 50, dtype=torch.int32, device="cuda"))
+    ws = mla.Workspace()
+    assert torch.equal(_run(e, workspace=ws), want)  # 50 sequences of the same rows
+    assert mla.mla_attn_get_status(ws) == S.ERR_KVLEN
+    # room for 600 // 256 + 99 = 101 pairs, three to a sequence
+    assert int(ws.buf[256:260].view(torch.int32)) == 33 * 3
+    assert torch.equal(_run(d, workspace=ws), want) and mla.mla_attn_get_status(ws) == 0
+
+
+def test_more_pairs_than_32_bits_count():
+    """2^23 sequences of 2^16 rows, the same ones: 2^31 pairs of query tiles if all were counted."""
+    mla.mla_attn_get_status()
+    T, B = 1 << 16, 1 << 24
+    x = torch.zeros((T, 1, 128), dtype=torch.bfloat16, device="cuda")
+    pe = torch.zeros((T, 1, 64), dtype=torch.bfloat16, device="cuda")
+    v = torch.randn((1, 128), device="cuda").to(torch.bfloat16).repeat(T, 1)[:, None].contiguous()
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = T
+    ws = mla.Workspace()
+    out = mla.mla_attn_varlen_fwd(x, pe, x, pe[:, 0], v, cu, SCALE, workspace=ws)
+    assert mla.mla_attn_get_status(ws) == S.ERR_KVLEN
+    most = T // 256 + T
+    assert int(ws.buf[256:260].view(torch.int32)) == most // 256 * 256
+    # Every value row is the same and every weight 1, so each row's mean is that row: half a step of
+    # bf16, 2^-8, and in fp32 at most 2^16 / 16 sums of a tensor instruction, off by 2^-23 each.
+    assert bool(((out.float() - v.float()).abs() <= v.float().abs() * 2 ** -7).all())
