@@ -335,8 +335,8 @@ MLA_API mla_status mla_attn_rope_append_fwd(const uint16_t* q_nope, const uint16
  * strides (elements; NULL: contiguous) lets the inputs be slices of larger tensors, such as the
  * query projection's [T, H, 192] and the key/value projection's [T, Hkv, 256]: the last
  * dimension is contiguous, the others' strides are positive multiples of 8.  Sequences may be
- * empty; rows from cu_seqlens[B] on are padding, and out is left as it was there.  Another
- * sequence's rows never reach a result, whatever they hold.
+ * empty; rows in front of cu_seqlens[0] and from cu_seqlens[B] on are nobody's, and out is left
+ * as it was there.  Another sequence's rows never reach a result, whatever they hold.
  * Offsets that are not rising within [0, T] are clamped (MLA_ERR_KVLEN in the status word; what
  * their sequences get is not meaningful, and where falling offsets make sequences overlap beyond
  * T / 256 + min(B, T) pairs of 128-row tiles, the sequences behind get nothing).  Workspace:
@@ -451,8 +451,10 @@ MLA_API mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k
  * and other sequences' rows never reach a result, whatever they hold; a new key that the mask
  * hides from a row takes part with weight zero, so it has to be finite.
  *
- *   q_nope [T, H, 128], q_pe [T, H, 64], out [T, H, 128]    bf16; rows from cu_q[B] on of
- *                                       out are left as they were
+ *   q_nope [T, H, 128], q_pe [T, H, 64], out [T, H, 128]    bf16; rows of out in front of
+ *                                       cu_q[0] and from cu_q[B] on are left as they were (a
+ *                                       call may take some of a batch's sequences: their
+ *                                       entries of cu_q, kv_len and block_table)
  *   c_pages, pe_pages, block_table [B, max_pages], cu_q [B + 1], kv_len [B]    as above
  *   draft_mask [T] int64 or NULL        w_kvb [H * 256, 512] bf16
  * Only the entries of the block table below ceil(kv_len[b] / page_size) are read.

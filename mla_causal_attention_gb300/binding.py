@@ -562,7 +562,7 @@ def mla_latent_tree_fwd(q_nope, q_pe, c_pages, pe_pages, block_table, kv_len, cu
     pe_pages [num_pages, page_size, 64]; block_table [B, max_pages], kv_len [B] (with the new
     tokens), cu_q [B+1] (int32, from mla_paged_plan); draft_mask [T] int64 for token trees, or
     None for tokens in order (one per sequence: plain decode); w_kvb [H*256,512].  Returns out
-    [T,H,128]; rows from cu_q[B] on are left as they were."""
+    [T,H,128]; rows in front of cu_q[0] and from cu_q[B] on are left as they were."""
     dev = q_nope.device
     if dev.type != "cuda":
         raise ValueError("inputs must be CUDA tensors")
@@ -615,7 +615,7 @@ def mla_attn_varlen_fwd(q_nope, q_pe, k_nope, k_pe, v, cu_seqlens, softmax_scale
 
     q_nope [T,H,128], q_pe [T,H,64], k_nope / v [T,Hkv,128] (Hkv divides H), k_pe [T,64]
     (bf16; slices of larger tensors are read in place), cu_seqlens [B+1] int32.  Returns out
-    [T,H,128]; rows from cu_seqlens[B] on are left as they were."""
+    [T,H,128]; rows in front of cu_seqlens[0] and from cu_seqlens[B] on are left as they were."""
     dev = q_nope.device
     if dev.type != "cuda":
         raise ValueError("inputs must be CUDA tensors")

@@ -201,6 +201,8 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
       tma_load_2d(sW + s * kSub, &p.tm_w, &bars->w_full, 64 * s, h * 256 + (kUp ? 128 : 0));
   }
   if (kUp) grid_dep_wait();
+  // Rows in front of the first sequence and behind the last are left as they are.
+  const int row0 = kUp ? min(max(a.cu_q[0], 0), a.T) : 0;
   const int rows = kUp ? min(max(a.cu_q[a.B], 0), a.T) : a.T;
   const int tiles = (rows + kM - 1) / kM;
   const bool merge = kUp && p.merge;
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
           for (int c = 0; c < kN / 32; ++c) {
             uint32_t o[32];
             take(c, o, c == kN / 32 - 1);
-            if (t < rows)
+            if (t >= row0 && t < rows)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 *reinterpret_cast<uint4*>(dst + c * 32 + 8 * e) = pack8(o, e);

@@ -334,3 +334,17 @@ def test_folded_queries_are_the_same_every_time(T, H, rounds):
                                       d["block_table"], d["kv_len"], d["cu_q"], d["draft_mask"],
                                       d["w_kvb"], SCALE, workspace=ws)
         assert torch.equal(out, want), k
+
+
+@pytest.mark.parametrize("new", [(1, 4), (20, 60)])  # merged in the up-projection, and apart
+def test_some_of_a_batchs_sequences(new):
+    """The last sequences of a batch in a call of their own: the rows in front are left alone."""
+    d = tree_case(19, 4, 64, (100, 500), new, 32, True)
+    cu = d["cu_q"].tolist()
+    out = torch.full_like(d["q_nope"], 7.0)
+    e = dict(d, cu_q=d["cu_q"][2:].contiguous(), kv_len=d["kv_len"][2:].contiguous(),
+             block_table=d["block_table"][2:].contiguous())
+    _run(e, out=out)
+    assert mla.mla_attn_get_status() == 0
+    assert bool((out[:cu[2]] == 7.0).all())
+    _close(out[cu[2]:], d, list(range(cu[2], cu[4])))

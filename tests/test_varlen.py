@@ -253,3 +253,13 @@ def test_more_pairs_than_32_bits_count():
     # Every value row is the same and every weight 1, so each row's mean is that row: half a step of
     # bf16, 2^-8, and in fp32 at most 2^16 / 16 sums of a tensor instruction, off by 2^-23 each.
     assert bool(((out.float() - v.float()).abs() <= v.float().abs() * 2 ** -7).all())
+
+
+def test_some_of_a_batchs_prompts():
+    d = _case(12, [40, 300, 129, 5], 8, 4, True)
+    want = _run(d)
+    out = torch.full_like(want, 7.0)
+    _run(dict(d, cu_seqlens=d["cu_seqlens"][2:4].contiguous()), out=out)
+    assert mla.mla_attn_get_status() == 0
+    assert torch.equal(out[340:469], want[340:469])
+    assert bool((out[:340] == 7.0).all()) and bool((out[469:] == 7.0).all())
