@@ -463,7 +463,7 @@ MLA_API mla_status mla_latent_append(const uint16_t* c_kv_new, const uint16_t* k
  * Device-side problems (the call completes): cu_q not rising within [0, T], kv_len[b] below n
  * or past max_pages * page_size (MLA_ERR_KVLEN, clamped); a page outside the pool
  * (MLA_ERR_PAGE, read as zeros); n > 64 with draft_mask (MLA_ERR_TREE: the keys past 64 are
- * hidden).  The output of such a sequence is not meaningful.
+ * hidden).  The output of such a sequence is not meaningful, but zero if no key is left.
  */
 MLA_API size_t mla_latent_tree_workspace_bytes(int T, int H, int B);
 MLA_API mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,

@@ -126,7 +126,7 @@ TreeLayout tree_layout(int T, int H, int B, int sms) {
   l.tile0 = l.q_lat + r256((size_t)T * H * 512 * 2);
   l.unit0 = l.tile0 + r256((size_t)(B + 1) * 8);
   l.range0 = l.unit0 + r256((size_t)(B + 1) * 8);
-  l.first = l.range0 + r256((size_t)(l.pairs + 2) * 8);
+  l.first = l.range0 + r256((size_t)(l.pairs + 3) * 8);
   l.part_note = l.first + r256((size_t)l.pairs * 48);
   l.part_ml = l.part_note + r256((size_t)l.pairs * 32);
   l.part_acc = l.part_ml + (size_t)2 * l.pairs * 128 * 2 * 4;

@@ -241,7 +241,8 @@ struct TreeArgs {
   uint16_t* out;
   uint16_t* q_lat;   // workspace [T,H,512]: folded queries, then their rows' mixes
   // workspace, the partition (see tree.cu): first tile and first unit of each sequence and their
-  // totals [B+1]; first tile of each pair's range, all tiles, waves [pairs+2]
+  // totals [B+1]; first tile of each pair's range, all tiles, waves, whether a
+  // sequence has new tokens and no keys [pairs+3]
   int64_t* tile0;
   int64_t* unit0;
   int64_t* range0;

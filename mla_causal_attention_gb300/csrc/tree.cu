@@ -464,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       a.part_note[2 * pair_id] = make_int4(0, 0, 0, 0);
       a.part_note[2 * pair_id + 1] = make_int4(0, 0, 0, 0);
     }
+    clear_keyless(a, pair_id, rank * 128 + threadIdx.x - 128, 256);
     uint32_t t = 0;
     bool ok = true, gone = false;  // a wait of this thread's gave up; all four warps leave
     for (; more; g = after) {

@@ -43,7 +43,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
   return s;
 }
 __device__ __forceinline__ int seq_tiles(const TreeSeq& s) { return (s.kv + kTile - 1) / kTile; }
-// Units of a sequence; without keys (a bad length) it has none, and its rows are zero.
+// Units of a sequence; without keys (a bad length) it has none, and clear_keyless zeroes its rows.
 __device__ __forceinline__ int seq_units(const TreeArgs& a, const TreeSeq& s) {
   return s.kv > 0 ? (s.n * a.H + kRows - 1) / kRows : 0;
 }
@@ -94,8 +94,10 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a, uint8_t* r
   int64_t* unit0 = near ? tile0 + a.B + 1 : a.unit0;
   int* tiles = reinterpret_cast<int*>(unit0 + a.B + 1);  // of a sequence's units, if near
   __shared__ int64_t s_w[8], s_u[8], s_x;
-  __shared__ int s_nw;
+  __shared__ int s_nw, s_keyless;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_keyless = 0;
+  __syncthreads();
   int64_t W = 0, U = 0;
   for (int b0 = 0; b0 < a.B; b0 += 256) {
     const int b = b0 + tid;
@@ -105,6 +107,7 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a, uint8_t* r
       const TreeSeq s = tree_seq(a, b);
       if (s.bad) set_status(a.status, MLA_ERR_KVLEN);
       if (a.draft_mask && s.n > 64) set_status(a.status, MLA_ERR_TREE);
+      if (s.n > 0 && s.kv == 0) s_keyless = 1;
       u = seq_units(a, s);
       K = seq_tiles(s);
       w = u * K;
@@ -235,6 +238,7 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a, uint8_t* r
   if (tid == 0) {
     a.range0[P] = W;
     a.range0[P + 1] = nw;
+    a.range0[P + 2] = s_keyless;
   }
   // Each pair's first segment, spelled out: every role of the split kernel starts with one load
   // instead of a search.
@@ -263,6 +267,19 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a, uint8_t* r
     rec[0] = make_int4(g.b, g.m, g.k0, g.k1);
     rec[1] = make_int4(g.s.q0, g.s.n, g.s.kv, g.s.ctx);
     rec[2] = make_int4(g.slot, 0, 0, 0);
+  }
+}
+
+// Zeroes the mixes of sequences that have new tokens and no keys: no unit writes them, and the folded
+// queries in their place would be taken for mixes.  By `threads` threads of each pair's CTAs.
+__device__ __forceinline__ void clear_keyless(const TreeArgs& a, int pair, int thread, int threads) {
+  if (a.range0[a.pairs + 2] == 0) return;
+  for (int b = pair; b < a.B; b += a.pairs) {
+    const TreeSeq s = tree_seq(a, b);
+    if (s.kv > 0) continue;
+    uint4* rows = reinterpret_cast<uint4*>(a.q_lat + (size_t)s.q0 * a.H * 512);
+    for (int64_t i = thread; i < (int64_t)s.n * a.H * 64; i += threads)
+      rows[i] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 

@@ -348,3 +348,20 @@ def test_some_of_a_batchs_sequences(new):
     assert mla.mla_attn_get_status() == 0
     assert bool((out[:cu[2]] == 7.0).all())
     _close(out[cu[2]:], d, list(range(cu[2], cu[4])))
+
+
+@pytest.mark.parametrize("new", [(1, 4), (20, 60)])  # merged in the up-projection, and apart
+def test_a_sequence_without_keys_is_zero(new):
+    """New tokens whose sequence has no keys at all (a bad length): reported, and their rows see
+    nothing; the other sequences come out as they would."""
+    mla.mla_attn_get_status()
+    d = tree_case(20, 4, 64, (100, 500), new, 32, True, pad=1)
+    cu = d["cu_q"].tolist()
+    kv = d["kv_len"].clone()
+    kv[1], kv[2] = 0, -5
+    out = torch.full_like(d["q_nope"], 7.0)
+    _run(dict(d, kv_len=kv), out=out)
+    assert mla.mla_attn_get_status() == S.ERR_KVLEN
+    assert bool((out[cu[1]:cu[3]] == 0).all()) and bool((out[cu[4]:] == 7.0).all())
+    rows = [*range(cu[1]), *range(cu[3], cu[4])]
+    _close(out[rows], d, rows)
