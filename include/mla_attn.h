@@ -393,16 +393,17 @@ MLA_API mla_status mla_attn_varlen_fwd(const uint16_t* q_nope, const uint16_t* q
  *               mla_latent_tree_fwd takes.  At most 64 new tokens per sequence then.
  * Rows t from cu_q[B] to T - 1: slots -1, positions 0, draft_mask 0.
  *
- * free_next must not be free_head, nor kv_len a length that is read (blocks read the one while
- * others write the other; MLA_ERR_ARG).  Entries of the table at or past ceil(ctx / page_size) are
- * taken to be free: a server that drops drafted tokens puts their pages back on its list first.
+ * No output may overlap an input or another output (blocks read the ones while others write the
+ * other; MLA_ERR_ARG); the block table is read and written.  Its entries at or past
+ * ceil(ctx / page_size) are taken to be free: a server that drops drafted tokens puts their pages
+ * back on its list first.
  * Problems only the device sees go to the status word, and the call completes: lengths below
  * zero or past max_pages * page_size, or more than T new tokens in all (MLA_ERR_KVLEN:
  * lengths are clamped, tokens past the table get slot -1); a free list that runs out, or an
  * entry outside [0, num_pages) (MLA_ERR_PAGE: table entry and slots become -1); a bad parent
  * or a sequence of more than 64 drafted tokens (MLA_ERR_TREE: the token becomes a root; the
  * tokens past 64 see nothing).
- * Lengths must not overlap the outputs.  workspace: 256 bytes (the status word), zeroed once.
+ * workspace: 256 bytes (the status word), zeroed once.
  */
 MLA_API mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int B,
                                   int32_t* block_table, int max_pages, const int32_t* free_pages,

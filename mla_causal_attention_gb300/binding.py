@@ -482,7 +482,7 @@ def mla_paged_plan(ctx_len, new_len, block_table, free_pages, free_head, page_si
     free_head[0] (int32 [1]) on; parent [num_tokens] int32 for drafted trees (index within the
     sequence's new tokens, -1 for a root).  num_tokens: rows of the per-token outputs, at least
     the new tokens (rows behind them get slot -1).  ``out``: a PagedPlan (or a tuple like it)
-    to fill instead of new tensors; its free_next must not be free_head."""
+    to fill instead of new tensors; none of them may overlap an input or another one."""
     dev = ctx_len.device
     if dev.type != "cuda":
         raise ValueError("inputs must be CUDA tensors")

@@ -155,6 +155,16 @@ int page_shift(int page_size) {
   return s;
 }
 
+// A buffer of a call, for the checks that no output is another buffer too.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+bool overlap(const Span& x, const Span& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.at), b = reinterpret_cast<uintptr_t>(y.at);
+  return x.bytes && y.bytes && a < b + y.bytes && b < a + x.bytes;
+}
+
 bool rope_config_ok(const mla_rope_config& c) {
   const double v[7] = {c.rope_theta, c.factor, c.original_max_position, c.beta_fast,
                        c.beta_slow, c.mscale, c.mscale_all_dim};
@@ -642,8 +652,19 @@ mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int B,
   if (!aligned16(slots) || !aligned16(positions) || !aligned16(draft_mask) ||
       !aligned16(workspace))
     return MLA_ERR_ALIGN;
-  // Blocks read these while others write.
-  if (free_next == free_head || kv_len == ctx_len || kv_len == new_len) return MLA_ERR_ARG;
+  // Blocks read the inputs over and over while others write the outputs.
+  const size_t n_tok = (size_t)T * 4, n_seq = (size_t)B * 4;
+  const Span in[] = {{ctx_len, n_seq}, {new_len, n_seq}, {free_pages, (size_t)n_free * 4},
+                     {free_head, 4}, {parent, parent ? n_tok : 0}};
+  const Span out[] = {{block_table, n_seq * max_pages}, {cu_q, n_seq + 4}, {kv_len, n_seq},
+                      {slots, n_tok}, {positions, n_tok}, {free_next, 4},
+                      {draft_mask, draft_mask ? 2 * n_tok : 0}};
+  for (const Span& o : out) {
+    for (const Span& i : in)
+      if (overlap(o, i)) return MLA_ERR_ARG;
+    for (const Span& other : out)
+      if (&other != &o && overlap(o, other)) return MLA_ERR_ARG;
+  }
   if (workspace_bytes < kStatusBytes) return MLA_ERR_WORKSPACE;
   const mla_status st = check_device(nullptr);
   if (st != MLA_OK) return st;

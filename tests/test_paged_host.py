@@ -224,3 +224,30 @@ def test_an_outgrown_workspace_is_kept():
     second = ws.get(400)
     assert second.numel() == 600 and [b.data_ptr() for b in ws.outgrown] == [at]
     assert ws.get(10000).numel() == 10000 and ws.outgrown[1] is second
+
+
+def test_plan_refuses_overlap(lib, base):
+    """Every output with every input and every other output, from its first byte to its last."""
+    size = dict(ctx_len=8, new_len=8, free_pages=12, free_head=4, parent=20, block_table=32, cu_q=12,
+                kv_len=8, slots=20, positions=20, draft_mask=40, free_next=4)
+    outs = ["block_table", "cu_q", "kv_len", "slots", "positions", "draft_mask", "free_next"]
+    def call(**change):
+        a = _plan_args(base)
+        a.update(parent=base + 256 * 30, draft_mask=base + 256 * 31, **change)
+        return a, lambda: lib.mla_paged_plan(*[a[n] for n in PLAN])
+
+    for o in outs:
+        for other in size:
+            if other == o:
+                continue
+            a, run = call()
+            align = 16 if o in ("slots", "positions", "draft_mask") else 4
+            a[o] = a[other]
+            assert run() == S.ERR_ARG, (o, other)
+            # the output's first byte just inside the other's last word
+            inside = (size[other] - 4) // align * align
+            a[o] = a[other] + inside
+            assert run() == S.ERR_ARG, (o, other, inside)
+            if not torch.cuda.is_available():  # and just behind it: no call of this is run on a GPU
+                a[o] = a[other] + -(-size[other] // align) * align
+                assert run() in _no_device(), (o, other)
