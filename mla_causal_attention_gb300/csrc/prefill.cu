@@ -154,6 +154,12 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// The limit of a wait that lasts for a whole unit (for the last tile's values, for the next unit, or
+// of a query tile without rows): a key tile takes about 2.4 us, and a prompt of 2^26 rows has 2^19 of them.
+__device__ __forceinline__ uint64_t unit_limit(int tiles) {
+  return kWaitLimitNs + (uint64_t)tiles * 20000u;
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -203,9 +209,10 @@ __device__ __forceinline__ int4 packed_first(const PrefillParams& p, int64_t& n_
 }
 // By a whole warp: unit i > 0 of the CTA; false when the wait gave up.
 __device__ __forceinline__ bool packed_take(Bars* bars, int i, int4& u, int lane, int* status,
-                                            volatile int* abort_flag) {
-  const bool ok = __all_sync(
-      0xffffffffu, mbar_wait(&bars->unit_full[i & 1], ((i - 1) >> 1) & 1, status, abort_flag));
+                                            volatile int* abort_flag,
+                                            uint64_t limit = kWaitLimitNs) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->unit_full[i & 1], ((i - 1) >> 1) & 1,
+                                                    status, abort_flag, limit));
   if (!ok) return false;
   u = bars->unit[i & 1];
   __syncwarp();
@@ -491,14 +498,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int64_t n_units;
       int4 next = packed_first(p, n_units);
+      int longest = 0;  // it has nothing to do in most units, and runs a unit ahead of the others
       for (int i = 0;; ++i) {
-        if (i > 0) ok = packed_take(bars, i, next, lane, p.status, abort_flag);
+        if (i > 0)
+          ok = packed_take(bars, i, next, lane, p.status, abort_flag, unit_limit(longest));
         if (!ok || next.w < 0) break;
         const Unit w = unit_make<true>(p, 0, next);
+        longest = max(longest, w.n);
         if (w.n * kBN > w.kvl) {  // the unit's last tile
           const uint32_t ul = u + (w.n - 1) * kSubPerKv, gl = g + w.n - 1;
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_tail[gl & 1], tails[gl & 1] & 1,
-                                                 p.status, abort_flag));
+                                                 p.status, abort_flag, unit_limit(w.n)));
           if (!ok) break;
           ++tails[gl & 1];
           const int left = w.kvl - (w.n - 1) * kBN;
@@ -944,7 +954,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // The unit's output: wait for the last value mix, move O_t to registers, release
       // O_t for the next unit, then normalise and store.
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t], i & 1, p.status, abort_flag));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t], i & 1, p.status, abort_flag,
+                                             unit_limit(w.n)));
       if (!ok) break;
       tc::fence_after_sync();
       if (ntt == 0) {

@@ -81,18 +81,18 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity
 }
 
 // Waits until the phase with the given parity has completed.  Bounded: after
-// kWaitLimitNs it records MLA_ERR_TIMEOUT, sets *abort and returns false.  Once *abort is
+// `limit` ns it records MLA_ERR_TIMEOUT, sets *abort and returns false.  Once *abort is
 // set (by this or another thread of the CTA, via shared memory) every later wait returns
 // false at once, so a CTA unwinds instead of waiting on work that will never arrive.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* status,
-                                          volatile int* abort) {
+                                          volatile int* abort, uint64_t limit = kWaitLimitNs) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait(a, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     if (mbar_try_wait_hint(a, parity)) return true;
     if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+    if (globaltimer_ns() - t0 > limit) {
       set_status(status, MLA_ERR_TIMEOUT);
       *abort = 1;
       return false;

@@ -4,6 +4,7 @@ Tolerances.  The softmax weights and the output are rounded to bf16, by at most 
 2^-8 of the value: per element 2^-8 of spread = sum_j p_j |v_j| for the weights, 2^-8 of |out| <=
 spread for the output, 2 * 2^-8 spread in all (and 2^-16 of it for fp32 sums over at most a few
 thousand keys).  In the 2-norm the two are independent and at most 2^-8 / sqrt(3) each: 0.0032."""
+import ctypes
 import random
 
 import pytest
@@ -11,6 +12,7 @@ import torch
 
 import mla_causal_attention_gb300 as mla
 from mla_causal_attention_gb300 import binding
+from mla_causal_attention_gb300.build import build_test_variant
 from mla_causal_attention_gb300.workloads import softmax_scale_192
 
 pytestmark = pytest.mark.gpu
@@ -263,3 +265,30 @@ def test_some_of_a_batchs_prompts():
     assert mla.mla_attn_get_status() == 0
     assert torch.equal(out[340:469], want[340:469])
     assert bool((out[:340] == 7.0).all()) and bool((out[469:] == 7.0).all())
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_waits_that_last_for_a_whole_unit(packed):
+    """A prompt of 2049 key tiles whose last query tile pair has rows in one tile only, by a test
+    build whose waits give up after 1 ms: the warps that wait for the whole unit, about 3 ms, do not
+    take its length for a hang.  (The library gives up after a second, a unit of 2^26 keys.)"""
+    lib = ctypes.CDLL(build_test_variant("wait_long", "prefill.cu", ["-DMLA_WAIT_LIMIT_NS=1000000ull"]))
+    p, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.mla_attn_varlen_fwd.argtypes = [p, p, p, p, p, p, p, i, i, i, i, f, p, p, sz, p]
+    lib.mla_attn_fwd.argtypes = [p, p, p, p, p, p, i, i, i, i, i, f, p, p, sz, p]
+    lib.mla_attn_get_status.argtypes = [p, p]
+    T = (1 << 18) + 100
+    d = _case(13, [T], 1, 1, False)
+    out = torch.zeros((T, 1, 128), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(1 << 23, dtype=torch.uint8, device="cuda")
+    at = [d[k].data_ptr() for k in ("q_nope", "q_pe", "k_nope", "k_pe", "v")]
+    tail = [SCALE, out.data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream]
+    torch.cuda.synchronize()
+    if packed:
+        rc = lib.mla_attn_varlen_fwd(*at, None, d["cu_seqlens"].data_ptr(), 1, T, 1, 1, *tail)
+    else:
+        rc = lib.mla_attn_fwd(*at, None, 1, 1, T, T, 0, *tail)
+    assert rc == 0
+    assert lib.mla_attn_get_status(ws.data_ptr(), tail[-1]) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, _run(d))
