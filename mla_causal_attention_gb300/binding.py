@@ -172,7 +172,8 @@ class Workspace:
     different streams) need workspaces of their own.  The default one, used when a call
     gets none, is shared by every call on its device.  A buffer that was outgrown is kept,
     since a captured graph may go on using it; growth is at least twofold, so that the kept
-    ones together are smaller than the one in use.
+    ones together are smaller than the one in use.  A program without graphs of the smaller
+    calls gives them back with release_outgrown().
     """
 
     def __init__(self, device=None):
@@ -190,6 +191,11 @@ class Workspace:
             with torch.cuda.stream(stream):
                 self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         return self.buf
+
+    def release_outgrown(self) -> None:
+        """Frees the outgrown buffers, with what their status words hold.  Only once no captured
+        graph or PreparedCall uses them and the calls on this workspace have completed."""
+        self.outgrown.clear()
 
 
 def _ptr(t):

@@ -251,3 +251,13 @@ def test_plan_refuses_overlap(lib, base):
             if not torch.cuda.is_available():  # and just behind it: no call of this is run on a GPU
                 a[o] = a[other] + -(-size[other] // align) * align
                 assert run() in _no_device(), (o, other)
+
+
+def test_outgrown_workspaces_are_given_back():
+    import weakref
+    ws = binding.Workspace("cpu")
+    gone = weakref.ref(ws.get(300))
+    kept = ws.get(400)
+    assert gone() is not None
+    ws.release_outgrown()
+    assert gone() is None and ws.outgrown == [] and ws.get(400) is kept
