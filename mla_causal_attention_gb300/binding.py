@@ -198,6 +198,17 @@ class Workspace:
         self.outgrown.clear()
 
 
+def _buffer(workspace, dev, nbytes, stream):
+    """A call's workspace buffer, at least nbytes long and on the call's device."""
+    ws = workspace or _default_workspace(dev)
+    buf = ws.buf
+    if buf is None or buf.numel() < nbytes:
+        buf = ws.get(nbytes, stream=stream or torch.cuda.current_stream(dev))
+    if buf.get_device() != dev.index:
+        raise ValueError(f"the workspace is on {buf.device}, the call on {dev}")
+    return buf
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -231,10 +242,7 @@ def _enqueue(name, dev, stream, workspace, ws_bytes, args):
     fn = getattr(_lib or library(), name)
     index = dev.index
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    ws = workspace or _default_workspace(dev)
-    buf = ws.buf
-    if buf is None or buf.numel() < ws_bytes:
-        buf = ws.get(ws_bytes, stream=stream or torch.cuda.current_stream(dev))
+    buf = _buffer(workspace, dev, ws_bytes, stream)
     if torch._C._cuda_getDevice() == index:
         rc = fn(*args, buf.data_ptr(), buf.numel(), s)
     else:
@@ -291,7 +299,7 @@ class PreparedCall:
             ws_bytes = max(ws_bytes, 256 + (-(-B * H * splits * 8 // 256)) * 256
                            + B * H * splits * 512)
         s = stream if stream is not None else torch.cuda.current_stream(dev)
-        ws = (workspace or _default_workspace(dev)).get(ws_bytes, stream=s)
+        ws = _buffer(workspace, dev, ws_bytes, s)
         self.out = out
         self.device = dev
         self._keep = (q_nope, q_pe, k_nope, k_pe_shared, v, kv_len, out, ws, s)
@@ -353,8 +361,7 @@ def mla_attn_append_fwd(q_nope, q_pe, k_nope_new, k_pe_new, v_new, k_nope_cache,
         out = torch.empty((B, H, Tq, 128), dtype=bf, device=dev)
     _check(out, "out", bf, (B, H, Tq, 128), dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    ws = (workspace or _default_workspace(dev)).get(
-        lib.mla_attn_workspace_bytes(B, H, Tq, past_len + Tq), stream=s)
+    ws = _buffer(workspace, dev, lib.mla_attn_workspace_bytes(B, H, Tq, past_len + Tq), s)
     with torch.cuda.device(dev):
         rc = lib.mla_attn_append_fwd(_ptr(q_nope), _ptr(q_pe), _ptr(k_nope_new),
                                      _ptr(k_pe_new), _ptr(v_new), _ptr(k_nope_cache),
@@ -393,8 +400,7 @@ def mla_attn_masked_fwd(q_nope, q_pe, k_nope, k_pe_shared, v, kv_len, key_mask,
         out = torch.empty((B, H, Tq, 128), dtype=bf, device=dev)
     _check(out, "out", bf, (B, H, Tq, 128), dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    ws = (workspace or _default_workspace(dev)).get(
-        lib.mla_attn_masked_workspace_bytes(B, H, Tq, Tk), stream=s)
+    ws = _buffer(workspace, dev, lib.mla_attn_masked_workspace_bytes(B, H, Tq, Tk), s)
     with torch.cuda.device(dev):
         rc = lib.mla_attn_masked_fwd(_ptr(q_nope), _ptr(q_pe), _ptr(k_nope), _ptr(k_pe_shared),
                                      _ptr(v), _ptr(kv_len), _ptr(key_mask), B, H, Tq, Tk,
@@ -428,8 +434,7 @@ def mla_latent_decode_fwd(q_nope, q_pe, c_kv, k_pe, w_kvb, kv_len, softmax_scale
         out = torch.empty((B, H, 128), dtype=bf, device=dev)
     _check(out, "out", bf, (B, H, 128), dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    ws = (workspace or _default_workspace(dev)).get(lib.mla_latent_workspace_bytes(B, H, Tk),
-                                                    stream=s)
+    ws = _buffer(workspace, dev, lib.mla_latent_workspace_bytes(B, H, Tk), s)
     with torch.cuda.device(dev):
         rc = lib.mla_latent_decode_fwd(_ptr(q_nope), _ptr(q_pe), _ptr(c_kv), _ptr(k_pe),
                                        _ptr(w_kvb), _ptr(kv_len), B, H, Tk,
@@ -456,8 +461,7 @@ def mla_oproj_fwd(attn, w_o, out=None, workspace: "Workspace | None" = None, str
         out = torch.empty((B, T, N), dtype=bf, device=dev)
     _check(out, "out", bf, (B, T, N), dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    ws = (workspace or _default_workspace(dev)).get(lib.mla_oproj_workspace_bytes(),
-                                                    stream=s)
+    ws = _buffer(workspace, dev, lib.mla_oproj_workspace_bytes(), s)
     with torch.cuda.device(dev):
         rc = lib.mla_oproj_fwd(_ptr(attn), _ptr(w_o), B, H, T, N, _ptr(out), _ptr(ws),
                                ws.numel(), ctypes.c_void_p(s.cuda_stream))
@@ -698,8 +702,7 @@ def mla_attn_rope_append_fwd(q_nope, q_pe_raw, k_nope_new, k_pe_new_raw, v_new, 
         out = torch.empty((B, H, Tq, 128), dtype=bf, device=dev)
     _check(out, "out", bf, (B, H, Tq, 128), dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    ws = (workspace or _default_workspace(dev)).get(
-        lib.mla_attn_rope_workspace_bytes(B, H, Tq, past_len + Tq), stream=s)
+    ws = _buffer(workspace, dev, lib.mla_attn_rope_workspace_bytes(B, H, Tq, past_len + Tq), s)
     with torch.cuda.device(dev):
         rc = lib.mla_attn_rope_append_fwd(
             _ptr(q_nope), _ptr(q_pe_raw), _ptr(k_nope_new), _ptr(k_pe_new_raw), _ptr(v_new),

@@ -261,3 +261,10 @@ def test_outgrown_workspaces_are_given_back():
     assert gone() is not None
     ws.release_outgrown()
     assert gone() is None and ws.outgrown == [] and ws.get(400) is kept
+
+
+def test_a_workspace_of_another_device_is_refused():
+    ws = binding.Workspace("cpu")
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        ws.get(300)
+        binding._buffer(ws, torch.device("cuda", 0), 300, None)

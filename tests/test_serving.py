@@ -186,3 +186,28 @@ def test_a_graph_outlives_its_workspace_growing():
     g.replay()
     assert mla.mla_attn_get_status(workspace=ws) == mla.MlaStatus.ERR_KVLEN
     assert mla.mla_attn_get_status(workspace=ws) == 0
+
+
+def test_workspaces_of_another_device_are_refused():
+    """Before anything is launched: the kernels write to the workspace."""
+    from paged_helpers import tree_case
+    ws = mla.Workspace("cpu")
+    ws.buf = torch.zeros(1 << 28, dtype=torch.uint8)
+    d = tree_case(64, 2, 8, (10, 40), (1, 3), 32, True)
+    x = torch.zeros((1, 8, 4, 128), dtype=torch.bfloat16, device="cuda")
+    rot = torch.zeros((1, 8, 4, 64), dtype=torch.bfloat16, device="cuda")
+    w_o = torch.zeros((7168, 8 * 128), dtype=torch.bfloat16, device="cuda")
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c = torch.zeros((1, 16, 512), dtype=torch.bfloat16, device="cuda")
+    for call in (
+            lambda: mla.mla_latent_tree_fwd(d["q_nope"], d["q_pe"], d["c_pages"], d["pe_pages"],
+                                            d["block_table"], d["kv_len"], d["cu_q"],
+                                            d["draft_mask"], d["w_kvb"], SCALE, workspace=ws),
+            lambda: mla.mla_paged_plan(i, i, i[None], i, i, 16, 1, 1, workspace=ws),
+            lambda: mla.mla_latent_append(c[0, :1], c[0, :1, :64].contiguous(), i, c,
+                                          c[..., :64].contiguous(), workspace=ws),
+            lambda: mla.mla_attn_fwd(x, rot, x, rot[:, 0], x, None, 0, SCALE, workspace=ws),
+            lambda: mla.mla_oproj_fwd(x, w_o, workspace=ws)):
+        with pytest.raises(ValueError, match="workspace is on cpu"):
+            call()
+    torch.cuda.synchronize()
