@@ -336,7 +336,8 @@ MLA_API mla_status mla_attn_rope_append_fwd(const uint16_t* q_nope, const uint16
  * query projection's [T, H, 192] and the key/value projection's [T, Hkv, 256]: the last
  * dimension is contiguous, the others' strides are positive multiples of 8.  Sequences may be
  * empty; rows in front of cu_seqlens[0] and from cu_seqlens[B] on are nobody's, and out is left
- * as it was there.  Another sequence's rows never reach a result, whatever they hold.
+ * as it was there.  Another sequence's rows never reach a result, whatever they hold; a later row
+ * of the same one takes part with weight zero, so its v has to be finite.
  * Offsets that are not rising within [0, T] are clamped (MLA_ERR_KVLEN in the status word; what
  * their sequences get is not meaningful, and where falling offsets make sequences overlap beyond
  * T / 256 + min(B, T) pairs of 128-row tiles, the sequences behind get nothing).  Workspace:

@@ -22,6 +22,9 @@
 // shared memory beside the queries' 72 KB.  So the next tile's scores run on the tensor cores
 // while this tile's softmax is computed.
 //
+// Rounded to bf16, the type of the MMAs' operands: the folded queries, the softmax weights (their sum
+// is taken before), each row's mix, the output.  Scores, maxima, sums and partial mixes are fp32.
+//
 // Per tile of 128 keys:  S = Q K^T   M128 N128 K576: CTA r stages keys 64 r .. 64 r + 63
 //                        O += P C    M128 N256 K128, twice: CTA r stages latent columns
 //                                    256 n + 128 r .. + 127 of all 128 keys
@@ -657,7 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
-// Tensor maps, cached by pointers and sizes (encoding costs microseconds of host time).
+// Tensor maps, cached by pointers and sizes.  Calls that go round more sets than there are entries (a
+// model's layers, each with its pages and weight) encode all ten of a call, 0.8 us of its 17 on the
+// host.
 struct MapKey {
   const void* ptr[4];
   int T, H, num_pages, page_shift;

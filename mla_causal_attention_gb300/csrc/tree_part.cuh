@@ -94,20 +94,20 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a, uint8_t* r
   int64_t* unit0 = near ? tile0 + a.B + 1 : a.unit0;
   int* tiles = reinterpret_cast<int*>(unit0 + a.B + 1);  // of a sequence's units, if near
   __shared__ int64_t s_w[8], s_u[8], s_x;
-  __shared__ int s_nw, s_keyless;
+  __shared__ int s_nw;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_keyless = 0;
-  __syncthreads();
   int64_t W = 0, U = 0;
+  int keyless = 0;  // a sequence has new tokens and no keys
   for (int b0 = 0; b0 < a.B; b0 += 256) {
     const int b = b0 + tid;
     int64_t w = 0, u = 0;
     int K = 0;
+    bool none = false;
     if (b < a.B) {
       const TreeSeq s = tree_seq(a, b);
       if (s.bad) set_status(a.status, MLA_ERR_KVLEN);
       if (a.draft_mask && s.n > 64) set_status(a.status, MLA_ERR_TREE);
-      if (s.n > 0 && s.kv == 0) s_keyless = 1;
+      none = s.n > 0 && s.kv == 0;
       u = seq_units(a, s);
       K = seq_tiles(s);
       w = u * K;
@@ -126,7 +126,7 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a, uint8_t* r
       s_w[warp] = inc_w;
       s_u[warp] = inc_u;
     }
-    __syncthreads();
+    keyless |= __syncthreads_or(none);
     int64_t before_w = W, before_u = U;
     for (int k = 0; k < 8; ++k) {
       if (k < warp) {
@@ -238,7 +238,7 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a, uint8_t* r
   if (tid == 0) {
     a.range0[P] = W;
     a.range0[P + 1] = nw;
-    a.range0[P + 2] = s_keyless;
+    a.range0[P + 2] = keyless;
   }
   // Each pair's first segment, spelled out: every role of the split kernel starts with one load
   // instead of a search.

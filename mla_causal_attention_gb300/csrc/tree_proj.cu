@@ -150,6 +150,8 @@ __device__ __forceinline__ void merge_row(const TreeArgs& a, const int4* note, i
 // one block per head, most SMs are idle and the weight's load is the critical path: the fold's
 // two column blocks then go to two blocks.
 // Warps: 0 TMA, 1 MMA, 4-7 epilogue.  The fold launch has one block more, which makes the partition.
+// It is the last: where the others fill every SM (8 heads from 2305 tokens on) it runs behind one of
+// them, about 2 us of 35.
 template <bool kUp>
 __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant__ ProjParams p) {
   constexpr int kKs = kUp ? 8 : 2, kNb = kUp ? 1 : 2, kN = kUp ? 128 : 256;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeA
   for (int k = 0; k < 4; ++k) *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * k) = w[k];
 }
 
-// Tensor maps, cached by pointers and sizes (encoding costs microseconds of host time).
+// Tensor maps, cached by pointers and sizes, two entries a call (see tree.cu).
 struct MapKey {
   const void* x;
   const void* w;
