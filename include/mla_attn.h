@@ -293,6 +293,46 @@ MLA_API mla_status mla_rope_frequencies(const mla_rope_config* cfg, double* inv_
 MLA_API mla_status mla_rope_table(const mla_rope_config* cfg, int max_pos, float* table,
                                   void* cuda_stream);
 
+/*
+ * The same for rotary parts of another width: dim columns (even, 2 .. 256) in place of the 64,
+ * dim / 2 frequencies, a table of dim columns (cosines in the first dim / 2).  With factor 1 the
+ * angles are the plain p theta^(-2d/dim).  MLA_ERR_SHAPE for other dims.
+ */
+MLA_API mla_status mla_rope_frequencies_dim(const mla_rope_config* cfg, int dim, double* inv_freq,
+                                            double* mscale_ratio);
+MLA_API mla_status mla_rope_table_dim(const mla_rope_config* cfg, int dim, int max_pos,
+                                      float* table, void* cuda_stream);
+
+/*
+ * The rotary step by itself, on rows of any tensor: queries before their attention, keys of a
+ * checkpoint whose rotary columns come in neighbouring pairs, cached keys that are turned back,
+ * gradients.  Row (t, h) of x is the R elements from x + t * x_row + h * x_head on (strides in
+ * elements, the R elements contiguous: a part of a wider head is a slice), and with c, s the
+ * columns d and R/2 + d of the table's row positions[t], for d < R/2
+ *
+ *   (u, v) = elements (d, d + R/2)   (MLA_ROPE_HALF) or (2d, 2d + 1)   (MLA_ROPE_INTERLEAVED)
+ *   (u, v) -> (u c - v s, v c + u s),    with inverse (u c + v s, v c - u s)
+ *
+ * is written to row (t, h) of y in out_layout, rounded once to the tensors' type.  For a table of
+ * ratio 1 the inverse undoes the step; for any table the gradient of a step from `layout` to
+ * `out_layout` is the inverse step of y's gradient from `out_layout` to `layout`.
+ *   x [T, H, R], y [T, H, R]   bf16, fp16 or fp32, both alike; x's strides may be 0, y's rows
+ *                              do not overlap; y is x (with its strides), or shares no element
+ *                              with it (other memory, or other columns of the same rows)
+ *   positions [T] int32        rope_table [table_rows, R] float (mla_rope_table_dim)
+ * R even, 2 .. 256.  MLA_ERR_SHAPE, MLA_ERR_ALIGN (a pointer that is no multiple of its element,
+ * table and workspace 16 bytes), MLA_ERR_ARG (an option, or a y that overlaps what is read).  A
+ * position outside the table is clamped to it (MLA_ERR_KVLEN in the status word).
+ * workspace: 256 bytes (the status word), zeroed once.
+ */
+typedef enum { MLA_TYPE_BF16 = 0, MLA_TYPE_FP16 = 1, MLA_TYPE_FP32 = 2 } mla_type;
+typedef enum { MLA_ROPE_HALF = 0, MLA_ROPE_INTERLEAVED = 1 } mla_rope_layout;
+MLA_API mla_status mla_rope_apply(const void* x, int64_t x_row, int64_t x_head, void* y,
+                                  int64_t y_row, int64_t y_head, int type, int T, int H, int R,
+                                  const int32_t* positions, const float* rope_table,
+                                  int table_rows, int layout, int out_layout, int inverse,
+                                  void* workspace, size_t workspace_bytes, void* cuda_stream);
+
 /* Bytes of workspace mla_attn_rope_append_fwd needs (0 for invalid sizes). */
 MLA_API size_t mla_attn_rope_workspace_bytes(int B, int H, int Tq, int Tk);
 
@@ -476,6 +516,61 @@ MLA_API mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q
                                        int T, int H, float softmax_scale, uint16_t* out,
                                        void* workspace, size_t workspace_bytes,
                                        void* cuda_stream);
+
+/*
+ * The rows that a sequence's cache keeps within its budget.  weights [num_pages, page_size] float
+ * holds a weight per slot (mla_latent_key_weights accumulates the attention that each cached key
+ * receives).  Of sequence b's n = kv_len[b] rows, k = min(n, budget[b]) are kept: all of them if
+ * n <= budget[b]; otherwise the first s = min(sinks, k), the last r = min(recent, k - s), and of
+ * those between the k - s - r with the largest weights.  Of equal weights the lower rows are kept;
+ * NaN counts as lower than any number.
+ *
+ *   kept[b, i], i < k    the kept rows, rising; -1 for k <= i < K        kept [B, K]
+ *   kept_len[b] = k
+ *   freed, n_freed       (both or neither) the pages block_table[b, p] with ceil(k / page_size)
+ *                        <= p < ceil(n / page_size), in order of b, then p, and their number;
+ *                        freed [B * max_pages], entries from n_freed[0] on are left as they were
+ *
+ * Nothing is moved and the table is not changed: mla_latent_compact moves the rows, in every layer
+ * whose pages the table names (a layer may keep other rows than the next, as long as it keeps as
+ * many), and only then may the freed pages go to another sequence.  kept_len is then the
+ * sequence's cached length.  Positions of later tokens go on from where they were, which is then
+ * more than the cached length: mla_paged_plan's positions count from the cached length, so a
+ * server adds what it has dropped.
+ *
+ * K at least every min(kv_len[b], budget[b]), B up to 65535, max_pages * page_size below 2^31; no
+ * output may overlap an input or another output (MLA_ERR_ARG, as for negative sinks or recent).
+ * Device-side problems (the call completes): a length outside the table, a budget below zero or more
+ * rows to keep than K (MLA_ERR_KVLEN, clamped); a page outside the pool (MLA_ERR_PAGE: its rows
+ * count as lowest).  workspace: 256 bytes (the status word), zeroed once.
+ */
+MLA_API mla_status mla_paged_evict(const float* weights, int num_pages, int page_size,
+                                   const int32_t* block_table, int max_pages,
+                                   const int32_t* kv_len, const int32_t* budget, int B, int sinks,
+                                   int recent, int32_t* kept, int K, int32_t* kept_len,
+                                   int32_t* freed, int32_t* n_freed, void* workspace,
+                                   size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * Moves the kept rows of every sequence to the front of its pages: for i < kept_len[b], row
+ * kept[b, i] of sequence b becomes its row i, in c_pages [num_pages, page_size, 512], pe_pages
+ * [num_pages, page_size, 64] and, if given, weights [num_pages, page_size] (float).  Other rows
+ * keep what they held, or hold what a moved row left behind.  The cached keys keep the rotary
+ * angles that they have.
+ *
+ * kept [B, K] int32, each row rising, as mla_paged_evict lists it (any rising list of rows will
+ * do); kept_len [B].  The sequences of a call have pages of their own: a page that two of them
+ * name is moved by both at once, and holds some mixture.  B up to 65535.
+ * Device-side problems (the call completes): kept_len outside [0, K] (MLA_ERR_KVLEN, clamped); an
+ * entry below its own index or past the table (MLA_ERR_KVLEN), or a page outside the pool
+ * (MLA_ERR_PAGE): that row is not moved.  A list that does not rise moves rows that others have
+ * overwritten.  workspace: 256 bytes (the status word), zeroed once.
+ */
+MLA_API mla_status mla_latent_compact(uint16_t* c_pages, uint16_t* pe_pages, float* weights,
+                                      int num_pages, int page_size, const int32_t* block_table,
+                                      int max_pages, const int32_t* kept, int K,
+                                      const int32_t* kept_len, int B, void* workspace,
+                                      size_t workspace_bytes, void* cuda_stream);
 
 /*
  * Synchronises cuda_stream, reads the device status word in the workspace, clears it,

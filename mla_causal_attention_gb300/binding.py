@@ -72,7 +72,9 @@ EXPORTED = ("mla_attn_workspace_bytes", "mla_attn_fwd", "mla_attn_fwd_ex",
             "mla_latent_workspace_bytes", "mla_latent_decode_fwd",
             "mla_oproj_workspace_bytes", "mla_oproj_fwd", "mla_paged_plan",
             "mla_attn_varlen_workspace_bytes", "mla_attn_varlen_fwd",
-            "mla_latent_append", "mla_latent_tree_workspace_bytes", "mla_latent_tree_fwd")
+            "mla_latent_append", "mla_latent_tree_workspace_bytes", "mla_latent_tree_fwd",
+            "mla_rope_frequencies_dim", "mla_rope_table_dim", "mla_rope_apply", "mla_paged_evict",
+            "mla_latent_compact")
 
 
 def library():
@@ -142,6 +144,20 @@ def library():
         lib.mla_attn_varlen_workspace_bytes.argtypes = [i, i]
         lib.mla_attn_varlen_fwd.restype = i
         lib.mla_attn_varlen_fwd.argtypes = [p, p, p, p, p, p, p, i, i, i, i, f, p, p, sz, p]
+        lib.mla_rope_frequencies_dim.restype = i
+        lib.mla_rope_frequencies_dim.argtypes = [ctypes.POINTER(RopeConfig), i,
+                                                 ctypes.POINTER(ctypes.c_double),
+                                                 ctypes.POINTER(ctypes.c_double)]
+        lib.mla_rope_table_dim.restype = i
+        lib.mla_rope_table_dim.argtypes = [ctypes.POINTER(RopeConfig), i, i, p, p]
+        i64 = ctypes.c_int64
+        lib.mla_rope_apply.restype = i
+        lib.mla_rope_apply.argtypes = [p, i64, i64, p, i64, i64, i, i, i, i, p, p, i, i, i, i, p, sz,
+                                       p]
+        lib.mla_paged_evict.restype = i
+        lib.mla_paged_evict.argtypes = [p, i, i, p, i, p, p, i, i, i, p, i, p, p, p, p, sz, p]
+        lib.mla_latent_compact.restype = i
+        lib.mla_latent_compact.argtypes = [p, p, p, i, i, p, i, p, i, p, i, p, sz, p]
         _lib = lib
         return lib
 
@@ -648,29 +664,162 @@ def mla_attn_varlen_fwd(q_nope, q_pe, k_nope, k_pe, v, cu_seqlens, softmax_scale
     return out
 
 
-def mla_rope_frequencies(cfg: RopeConfig | None = None):
-    """(inv_freq[32] as a list of floats, mscale ratio) computed by the library's host code."""
+class PagedEviction(NamedTuple):
+    """What mla_paged_evict lists: the rows each sequence keeps, rising, -1 behind them [B, K], and
+    their number [B]; the pages that come free [B * max_pages] and their number [1] (both None if
+    they were not asked for)."""
+    kept: torch.Tensor
+    kept_len: torch.Tensor
+    freed: "torch.Tensor | None"
+    n_freed: "torch.Tensor | None"
+
+
+def mla_paged_evict(weights, block_table, kv_len, budget, sinks: int = 0, recent: int = 0,
+                    max_keep: "int | None" = None, out=None,
+                    workspace: "Workspace | None" = None, stream=None) -> PagedEviction:
+    """Lists the rows that each sequence of a paged cache keeps within its budget.
+
+    weights [num_pages, page_size] float32, one per slot (mla_latent_key_weights); block_table
+    [B, max_pages], kv_len [B], budget [B] int32.  A sequence over its budget keeps its first
+    ``sinks`` and last ``recent`` rows and the heaviest of the others, ties to the lower row.
+    max_keep: columns of ``kept`` (default: what the table can hold), at least every kept_len.
+    ``out``: a PagedEviction (or a tuple like it) to fill instead of new tensors; entries of its
+    ``freed`` behind n_freed are left as they were."""
+    dev = weights.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    i32 = torch.int32
+    num_pages, page_size = weights.shape
+    B, max_pages = block_table.shape
+    if out is None:
+        K = max_pages * page_size if max_keep is None else int(max_keep)
+        new = lambda *n: torch.empty(n, dtype=i32, device=dev)  # noqa: E731
+        out = PagedEviction(new(B, K), new(B), new(B * max_pages), new(1))
+    elif not isinstance(out, PagedEviction):
+        out = PagedEviction(*out)
+    kept, kept_len, freed, n_freed = out
+    K = kept.shape[-1]
+    _check(weights, "weights", torch.float32, (num_pages, page_size), dev)
+    _check_all(dev, i32, (
+        ("block_table", block_table, (B, max_pages)), ("kv_len", kv_len, (B,)),
+        ("budget", budget, (B,)), ("kept", kept, (B, K)), ("kept_len", kept_len, (B,))))
+    if (freed is None) != (n_freed is None):
+        raise ValueError("freed and n_freed are listed together")
+    if freed is not None:
+        _check_all(dev, i32, (("freed", freed, (B * max_pages,)), ("n_freed", n_freed, (1,))))
+    _enqueue("mla_paged_evict", dev, stream, workspace, 256, (
+        weights.data_ptr(), num_pages, page_size, block_table.data_ptr(), max_pages,
+        kv_len.data_ptr(), budget.data_ptr(), B, int(sinks), int(recent), kept.data_ptr(), K,
+        kept_len.data_ptr(), _addr(freed), _addr(n_freed)))
+    return out
+
+
+def mla_latent_compact(c_pages, pe_pages, block_table, kept, kept_len, weights=None,
+                       workspace: "Workspace | None" = None, stream=None) -> None:
+    """Moves row kept[b, i] of every sequence to its row i (i < kept_len[b]), in place.
+
+    c_pages [num_pages, page_size, 512], pe_pages [num_pages, page_size, 64] (bf16), weights
+    [num_pages, page_size] (float32) or None; block_table [B, max_pages], kept [B, K], rising as
+    mla_paged_evict lists it, kept_len [B] (int32)."""
+    dev = c_pages.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    num_pages, page_size = c_pages.shape[:2]
+    B, max_pages = block_table.shape
+    K = kept.shape[-1]
+    _check_all(dev, torch.bfloat16, (("c_pages", c_pages, (num_pages, page_size, 512)),
+                                     ("pe_pages", pe_pages, (num_pages, page_size, 64))))
+    _check_all(dev, torch.int32, (("block_table", block_table, (B, max_pages)),
+                                  ("kept", kept, (B, K)), ("kept_len", kept_len, (B,))))
+    if weights is not None:
+        _check(weights, "weights", torch.float32, (num_pages, page_size), dev)
+    _enqueue("mla_latent_compact", dev, stream, workspace, 256, (
+        c_pages.data_ptr(), pe_pages.data_ptr(), _addr(weights), num_pages, page_size,
+        block_table.data_ptr(), max_pages, kept.data_ptr(), K, kept_len.data_ptr(), B))
+
+
+def mla_rope_frequencies(cfg: RopeConfig | None = None, dim: int = 64):
+    """(inv_freq[dim / 2] as a list of floats, mscale ratio) computed by the library's host code."""
     cfg = cfg or RopeConfig()
-    f = (ctypes.c_double * 32)()
+    f = (ctypes.c_double * max(1, int(dim) // 2))()
     m = ctypes.c_double()
-    rc = library().mla_rope_frequencies(ctypes.byref(cfg), f, ctypes.byref(m))
+    rc = library().mla_rope_frequencies_dim(ctypes.byref(cfg), int(dim), f, ctypes.byref(m))
     if rc != 0:
         raise MlaAttnError(rc, "mla_rope_frequencies: ")
     return list(f), m.value
 
 
-def mla_rope_table(max_pos: int, cfg: RopeConfig | None = None, device=None, stream=None):
-    """Device float32 [max_pos, 64] cos|sin table (times the mscale ratio)."""
+def mla_rope_table(max_pos: int, cfg: RopeConfig | None = None, device=None, stream=None,
+                   dim: int = 64):
+    """Device float32 [max_pos, dim] cos|sin table (times the mscale ratio)."""
     cfg = cfg or RopeConfig()
     dev = torch.device(device or "cuda")
-    table = torch.empty((max_pos, 64), dtype=torch.float32, device=dev)
+    table = torch.empty((max_pos, dim), dtype=torch.float32, device=dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
-        rc = library().mla_rope_table(ctypes.byref(cfg), int(max_pos), _ptr(table),
-                                      ctypes.c_void_p(s.cuda_stream))
+        rc = library().mla_rope_table_dim(ctypes.byref(cfg), int(dim), int(max_pos), _ptr(table),
+                                          ctypes.c_void_p(s.cuda_stream))
     if rc != 0:
         raise MlaAttnError(rc, "mla_rope_table: ")
     return table
+
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _row_steps(t, name, shape, device):
+    """(row, head) strides of a [T, R] or [T, H, R] tensor whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous, got strides {st}")
+    return st[0], st[1] if len(shape) == 3 else 0
+
+
+def mla_rope_apply(x, positions, rope_table, layout: str = "half",
+                   out_layout: "str | None" = None, inverse: bool = False, out=None,
+                   workspace: "Workspace | None" = None, stream=None):
+    """The rotary step on the rows of x [T, H, R] or [T, R] (bf16, fp16 or fp32; slices of wider
+    tensors are read in place), at positions [T] (int32) with rope_table [rows, R]
+    (mla_rope_table(..., dim=R)).
+
+    layout, out_layout (default: layout): "half" pairs columns d and d + R/2, "interleaved" 2d and
+    2d + 1.  inverse turns back; the gradient of a call is the inverse call on y's gradient with
+    the layouts exchanged.  ``out``: written instead of a new tensor; may be x itself."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [T, H, R] or [T, R], got {tuple(x.shape)}")
+    kind = _TYPES.get(x.dtype)
+    if kind is None:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    to = layout if out_layout is None else out_layout
+    if layout not in _LAYOUTS or to not in _LAYOUTS:
+        raise ValueError(f"layouts are 'half' and 'interleaved', got {layout!r} and {to!r}")
+    shape = x.shape
+    T, R = shape[0], shape[-1]
+    H = shape[1] if len(shape) == 3 else 1
+    x_row, x_head = _row_steps(x, "x", shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    elif out.dtype is not x.dtype:
+        raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
+    y_row, y_head = _row_steps(out, "out", shape, dev)
+    rows = rope_table.shape[0]
+    _check(rope_table, "rope_table", torch.float32, (rows, R), dev)
+    _check(positions, "positions", torch.int32, (T,), dev)
+    _enqueue("mla_rope_apply", dev, stream, workspace, 256, (
+        x.data_ptr(), x_row, x_head, out.data_ptr(), y_row, y_head, kind, T, H, R,
+        positions.data_ptr(), rope_table.data_ptr(), rows, _LAYOUTS[layout], _LAYOUTS[to],
+        1 if inverse else 0))
+    return out
 
 
 def mla_attn_rope_append_fwd(q_nope, q_pe_raw, k_nope_new, k_pe_new_raw, v_new, k_nope_cache,

@@ -450,7 +450,7 @@ mla_status mla_rope_frequencies(const mla_rope_config* cfg, double* inv_freq,
   if (!cfg) return MLA_ERR_NULL;
   if (!rope_config_ok(*cfg)) return MLA_ERR_ARG;
   double f[32], m = 1.0;
-  yarn_frequencies(*cfg, f, &m);
+  yarn_frequencies(*cfg, 64, f, &m);
   if (inv_freq) std::memcpy(inv_freq, f, sizeof(f));
   if (mscale_ratio) *mscale_ratio = m;
   return MLA_OK;
@@ -464,10 +464,96 @@ mla_status mla_rope_table(const mla_rope_config* cfg, int max_pos, float* table,
   if (!rope_config_ok(*cfg)) return MLA_ERR_ARG;
   const mla_status st = check_device(nullptr);
   if (st != MLA_OK) return st;
-  return launch_rope_table(table, max_pos, *cfg, static_cast<cudaStream_t>(cuda_stream)) ==
+  return launch_rope_table(table, 64, max_pos, *cfg, static_cast<cudaStream_t>(cuda_stream)) ==
                  cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
+}
+
+mla_status mla_rope_table_dim(const mla_rope_config* cfg, int dim, int max_pos, float* table,
+                              void* cuda_stream) {
+  if (!cfg || !table) return MLA_ERR_NULL;
+  if (max_pos < 1 || dim < 2 || dim > kMaxRopeDim || dim % 2 != 0) return MLA_ERR_SHAPE;
+  if (!aligned16(table)) return MLA_ERR_ALIGN;
+  if (!rope_config_ok(*cfg)) return MLA_ERR_ARG;
+  const mla_status st = check_device(nullptr);
+  if (st != MLA_OK) return st;
+  return launch_rope_table(table, dim, max_pos, *cfg, static_cast<cudaStream_t>(cuda_stream)) ==
+                 cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+mla_status mla_rope_apply(const void* x, int64_t x_row, int64_t x_head, void* y, int64_t y_row,
+                          int64_t y_head, int type, int T, int H, int R, const int32_t* positions,
+                          const float* rope_table, int table_rows, int layout, int out_layout,
+                          int inverse, void* workspace, size_t workspace_bytes,
+                          void* cuda_stream) {
+  if (!x || !y || !positions || !rope_table) return MLA_ERR_NULL;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  if (type < MLA_TYPE_BF16 || type > MLA_TYPE_FP32 || layout < MLA_ROPE_HALF ||
+      layout > MLA_ROPE_INTERLEAVED || out_layout < MLA_ROPE_HALF ||
+      out_layout > MLA_ROPE_INTERLEAVED || inverse < 0 || inverse > 1)
+    return MLA_ERR_ARG;
+  if (T < 1 || H < 1 || R < 2 || R > kMaxRopeDim || R % 2 != 0 || table_rows < 1 || x_row < 0 ||
+      x_head < 0 || y_row < 0 || y_head < 0 || x_row > kMaxElems || x_head > kMaxElems ||
+      y_row > kMaxElems || y_head > kMaxElems)
+    return MLA_ERR_SHAPE;
+  // A dimension of one element has no stride that is used.
+  if (T == 1) x_row = y_row = 0;
+  if (H == 1) x_head = y_head = 0;
+  const double span = (double)(T - 1) * std::max(x_row, y_row) + (double)(H - 1) * std::max(x_head, y_head);
+  if ((int64_t)T * H > kMaxElems / R || span > (double)kMaxElems) return MLA_ERR_SHAPE;
+  // y's rows do not meet: one dimension's steps clear a row, the other's all of those.
+  const int64_t all_heads = (H - 1) * y_head + R, all_rows = (T - 1) * y_row + R;
+  const bool apart = (T == 1 && H == 1) || (H == 1 && y_row >= R) || (T == 1 && y_head >= R) ||
+                     (y_head >= R && y_row >= all_heads) || (y_row >= R && y_head >= all_rows);
+  if (!apart) return MLA_ERR_SHAPE;
+  const size_t size = type == MLA_TYPE_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % size != 0 || reinterpret_cast<uintptr_t>(y) % size != 0 ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) != 0 || !aligned16(rope_table) ||
+      !aligned16(workspace))
+    return MLA_ERR_ALIGN;
+  // y is x, or no element of it is one of x's: apart in memory, or other columns of the same rows.
+  const Span sx = {x, ((size_t)((T - 1) * x_row + (H - 1) * x_head) + R) * size};
+  const Span sy = {y, ((size_t)((T - 1) * y_row + (H - 1) * y_head) + R) * size};
+  const bool same_steps = x_row == y_row && x_head == y_head;
+  if (overlap(sx, sy) && !(x == y && same_steps)) {
+    const int64_t inner = H == 1 ? y_row : T == 1 ? y_head : std::min(y_row, y_head);
+    const int64_t outer = std::max(y_row, y_head);
+    const int64_t off = reinterpret_cast<intptr_t>(y) - reinterpret_cast<intptr_t>(x);
+    const int64_t step = inner * (int64_t)size;
+    if (!same_steps || inner == 0 || outer % inner != 0) return MLA_ERR_ARG;
+    const int64_t m = (off % step + step) % step, row = R * (int64_t)size;
+    if (m < row || m > step - row) return MLA_ERR_ARG;
+  }
+  const Span read[] = {{positions, (size_t)T * 4}, {rope_table, (size_t)table_rows * R * 4}};
+  for (const Span& r : read)
+    if (overlap(sy, r)) return MLA_ERR_ARG;
+  if (workspace_bytes < kStatusBytes) return MLA_ERR_WORKSPACE;
+  const mla_status st = check_device(nullptr);
+  if (st != MLA_OK) return st;
+  RopeApplyArgs a{};
+  a.x = x; a.y = y; a.x_row = x_row; a.x_head = x_head; a.y_row = y_row; a.y_head = y_head;
+  a.positions = positions; a.table = rope_table; a.status = static_cast<int*>(workspace);
+  a.type = type; a.T = T; a.H = H; a.R = R; a.table_rows = table_rows;
+  a.from_pairs = layout == MLA_ROPE_INTERLEAVED;
+  a.to_pairs = out_layout == MLA_ROPE_INTERLEAVED;
+  a.sign = inverse ? -1.0f : 1.0f;
+  return launch_rope_apply(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? MLA_OK
+                                                                                      : MLA_ERR_CUDA;
+}
+
+mla_status mla_rope_frequencies_dim(const mla_rope_config* cfg, int dim, double* inv_freq,
+                                    double* mscale_ratio) {
+  if (!cfg) return MLA_ERR_NULL;
+  if (dim < 2 || dim > kMaxRopeDim || dim % 2 != 0) return MLA_ERR_SHAPE;
+  if (!rope_config_ok(*cfg)) return MLA_ERR_ARG;
+  double f[kMaxRopeDim / 2], m = 1.0;
+  yarn_frequencies(*cfg, dim, f, &m);
+  if (inv_freq) std::memcpy(inv_freq, f, sizeof(double) * (dim / 2));
+  if (mscale_ratio) *mscale_ratio = m;
+  return MLA_OK;
 }
 
 size_t mla_attn_rope_workspace_bytes(int B, int H, int Tq, int Tk) {
@@ -768,6 +854,79 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
   a.B = B; a.T = T; a.H = H; a.pairs = lay.pairs;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   return launch_latent_tree(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+mla_status mla_paged_evict(const float* weights, int num_pages, int page_size,
+                           const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                           const int32_t* budget, int B, int sinks, int recent, int32_t* kept,
+                           int K, int32_t* kept_len, int32_t* freed, int32_t* n_freed,
+                           void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  if (!weights || !block_table || !kv_len || !budget || !kept || !kept_len ||
+      (freed != nullptr) != (n_freed != nullptr))
+    return MLA_ERR_NULL;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  const mla_status ps = check_pool(num_pages, page_size);
+  if (ps != MLA_OK) return ps;
+  if (B < 1 || B > 65535 || K < 1 || max_pages < 1 || (int64_t)max_pages * page_size > 0x7fffffff ||
+      (int64_t)B * K > kMaxElems)
+    return MLA_ERR_SHAPE;
+  if (sinks < 0 || recent < 0) return MLA_ERR_ARG;
+  const void* words[] = {weights, block_table, kv_len, budget, kept, kept_len, freed, n_freed};
+  for (const void* w : words)
+    if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0) return MLA_ERR_ALIGN;
+  if (!aligned16(workspace)) return MLA_ERR_ALIGN;
+  // Clusters read the inputs while others write the outputs.
+  const size_t n_seq = (size_t)B * 4, n_table = n_seq * max_pages;
+  const Span in[] = {{weights, (size_t)num_pages * page_size * 4}, {block_table, n_table},
+                     {kv_len, n_seq}, {budget, n_seq}};
+  const Span out[] = {{kept, n_seq * K}, {kept_len, n_seq}, {freed, freed ? n_table : 0},
+                      {n_freed, n_freed ? (size_t)4 : 0}};
+  for (const Span& o : out) {
+    for (const Span& i : in)
+      if (overlap(o, i)) return MLA_ERR_ARG;
+    for (const Span& other : out)
+      if (&other != &o && overlap(o, other)) return MLA_ERR_ARG;
+  }
+  if (workspace_bytes < kStatusBytes) return MLA_ERR_WORKSPACE;
+  const mla_status st = check_device(nullptr);
+  if (st != MLA_OK) return st;
+  PagedEvictArgs a{};
+  a.weights = weights; a.block_table = block_table; a.kv_len = kv_len; a.budget = budget;
+  a.kept = kept; a.kept_len = kept_len; a.freed = freed; a.n_freed = n_freed;
+  a.status = static_cast<int*>(workspace);
+  a.B = B; a.K = K; a.sinks = sinks; a.recent = recent; a.num_pages = num_pages;
+  a.page_shift = page_shift(page_size); a.max_pages = max_pages;
+  return launch_paged_evict(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+mla_status mla_latent_compact(uint16_t* c_pages, uint16_t* pe_pages, float* weights, int num_pages,
+                              int page_size, const int32_t* block_table, int max_pages,
+                              const int32_t* kept, int K, const int32_t* kept_len, int B,
+                              void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  if (!c_pages || !pe_pages || !block_table || !kept || !kept_len) return MLA_ERR_NULL;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  const mla_status ps = check_pool(num_pages, page_size);
+  if (ps != MLA_OK) return ps;
+  if (B < 1 || B > 65535 || K < 1 || max_pages < 1 || (int64_t)max_pages * page_size > 0x7fffffff ||
+      (int64_t)B * K > kMaxElems)
+    return MLA_ERR_SHAPE;
+  const void* words[] = {weights, block_table, kept, kept_len};
+  for (const void* w : words)
+    if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0) return MLA_ERR_ALIGN;
+  if (!aligned16(c_pages) || !aligned16(pe_pages) || !aligned16(workspace)) return MLA_ERR_ALIGN;
+  if (workspace_bytes < kStatusBytes) return MLA_ERR_WORKSPACE;
+  const mla_status st = check_device(nullptr);
+  if (st != MLA_OK) return st;
+  LatentCompactArgs a{};
+  a.c_pages = c_pages; a.pe_pages = pe_pages; a.weights = weights; a.block_table = block_table;
+  a.kept = kept; a.kept_len = kept_len; a.status = static_cast<int*>(workspace);
+  a.B = B; a.K = K; a.num_pages = num_pages; a.page_shift = page_shift(page_size);
+  a.max_pages = max_pages;
+  return launch_latent_compact(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }

@@ -101,12 +101,28 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 
-// YaRN frequencies and mscale ratio of a configuration (host arithmetic, double).
-void yarn_frequencies(const mla_rope_config& cfg, double* inv_freq, double* mscale);
+constexpr int kMaxRopeDim = 256;
 
-// cos / sin table [max_pos][64] (cos in columns 0..31, sin in 32..63, times the ratio).
-cudaError_t launch_rope_table(float* cos_sin, int max_pos, const mla_rope_config& cfg,
+// YaRN frequencies (dim / 2 of them) and mscale ratio of a configuration (host arithmetic, double).
+void yarn_frequencies(const mla_rope_config& cfg, int dim, double* inv_freq, double* mscale);
+
+// cos / sin table [max_pos][dim] (cos in the first dim / 2 columns, then sin, times the ratio).
+cudaError_t launch_rope_table(float* cos_sin, int dim, int max_pos, const mla_rope_config& cfg,
                               cudaStream_t stream);
+
+// The rotary step by itself (see mla_rope_apply).  Strides in elements.
+struct RopeApplyArgs {
+  const void* x;
+  void* y;
+  int64_t x_row, x_head, y_row, y_head;
+  const int32_t* positions;
+  const float* table;
+  int* status;
+  int type, T, H, R, table_rows;
+  bool from_pairs, to_pairs;  // interleaved layout of x, of y
+  float sign;                 // of the angle: -1 turns back
+};
+cudaError_t launch_rope_apply(const RopeApplyArgs& a, cudaStream_t stream);
 
 // Rotary pre-pass: query t and new rotary key t are rotated at position past_len + t.
 // Rotated queries go to q_pe_rot [B,H,Tq,64]; rotated keys (b, t) to
@@ -226,6 +242,35 @@ struct LatentAppendArgs {
   unsigned q_blocks;           // set by the launcher
 };
 cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream);
+
+// The rows of a paged cache that stay within each sequence's budget (see mla_paged_evict).
+struct PagedEvictArgs {
+  const float* weights;
+  const int32_t* block_table;
+  const int32_t* kv_len;
+  const int32_t* budget;
+  int32_t* kept;
+  int32_t* kept_len;
+  int32_t* freed;    // may be null
+  int32_t* n_freed;  // null without freed
+  int* status;
+  int B, K, sinks, recent, num_pages, page_shift, max_pages;
+  int held;          // set by the launcher
+};
+cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream);
+
+// Kept rows to the front of their sequence's pages (see mla_latent_compact).
+struct LatentCompactArgs {
+  uint16_t* c_pages;
+  uint16_t* pe_pages;
+  float* weights;  // may be null
+  const int32_t* block_table;
+  const int32_t* kept;
+  const int32_t* kept_len;
+  int* status;
+  int B, K, num_pages, page_shift, max_pages;
+};
+cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t stream);
 
 // Attention of packed new tokens over the paged latent cache (see mla_latent_tree_fwd).
 struct TreeArgs {

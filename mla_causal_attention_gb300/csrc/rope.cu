@@ -19,22 +19,22 @@ namespace mla {
 namespace {
 
 struct TableArgs {
-  float* cos_sin;  // [max_pos][64]: cos of the 32 angles, then sin, times the mscale ratio
-  int max_pos;
-  double inv_freq[32];
+  float* cos_sin;  // [max_pos][2 half]: cos of the half angles, then sin, times the mscale ratio
+  int max_pos, half;
+  double inv_freq[kMaxRopeDim / 2];
   double mscale;
 };
 
 __global__ void __launch_bounds__(256) rope_table_kernel(const TableArgs a) {
-  const size_t n = (size_t)a.max_pos * 32;
+  const size_t n = (size_t)a.max_pos * a.half;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
        i += (size_t)gridDim.x * blockDim.x) {
-    const size_t pos = i >> 5;
-    const int d = (int)(i & 31);
+    const size_t pos = i / a.half;
+    const int d = (int)(i - pos * a.half);
     double s, c;
     sincos((double)pos * a.inv_freq[d], &s, &c);  // double: angles reach 10^5 radians
-    a.cos_sin[pos * 64 + d] = (float)(c * a.mscale);
-    a.cos_sin[pos * 64 + 32 + d] = (float)(s * a.mscale);
+    a.cos_sin[pos * 2 * a.half + d] = (float)(c * a.mscale);
+    a.cos_sin[pos * 2 * a.half + a.half + d] = (float)(s * a.mscale);
   }
 }
 
@@ -111,21 +111,21 @@ unsigned grid_for(size_t n) {
 
 }  // namespace
 
-// YaRN frequencies (extrapolated theta^(-2d/64), interpolated / factor, linear ramp between
+// YaRN frequencies (extrapolated theta^(-2d/dim), interpolated / factor, linear ramp between
 // the dimensions whose wavelengths make beta_fast and beta_slow rotations over the original
 // context) and the ratio of attention factors 0.1 k ln(factor) + 1, k = mscale over
 // k = mscale_all_dim.
-void yarn_frequencies(const mla_rope_config& c, double* inv_freq, double* mscale) {
+void yarn_frequencies(const mla_rope_config& c, int dim, double* inv_freq, double* mscale) {
   const double two_pi = 6.283185307179586;
   auto dim_for = [&](double rotations) {
-    return 64.0 * std::log(c.original_max_position / (two_pi * rotations)) /
+    return dim * std::log(c.original_max_position / (two_pi * rotations)) /
            (2.0 * std::log(c.rope_theta));
   };
   const double lo = std::max(std::floor(dim_for(c.beta_fast)), 0.0);
-  double hi = std::min(std::ceil(dim_for(c.beta_slow)), 31.0);
+  double hi = std::min(std::ceil(dim_for(c.beta_slow)), dim / 2 - 1.0);
   if (hi == lo) hi += 0.001;
-  for (int d = 0; d < 32; ++d) {
-    const double plain = std::pow(c.rope_theta, -2.0 * d / 64.0);
+  for (int d = 0; d < dim / 2; ++d) {
+    const double plain = std::pow(c.rope_theta, -2.0 * d / dim);
     const double w = std::min(std::max((d - lo) / (hi - lo), 0.0), 1.0);  // 1: interpolate
     inv_freq[d] = plain / c.factor * w + plain * (1.0 - w);
   }
@@ -133,13 +133,14 @@ void yarn_frequencies(const mla_rope_config& c, double* inv_freq, double* mscale
   *mscale = attn(c.mscale) / attn(c.mscale_all_dim);
 }
 
-cudaError_t launch_rope_table(float* cos_sin, int max_pos, const mla_rope_config& cfg,
+cudaError_t launch_rope_table(float* cos_sin, int dim, int max_pos, const mla_rope_config& cfg,
                               cudaStream_t stream) {
   TableArgs a;
   a.cos_sin = cos_sin;
   a.max_pos = max_pos;
-  yarn_frequencies(cfg, a.inv_freq, &a.mscale);
-  rope_table_kernel<<<grid_for((size_t)max_pos * 32), 256, 0, stream>>>(a);
+  a.half = dim / 2;
+  yarn_frequencies(cfg, dim, a.inv_freq, &a.mscale);
+  rope_table_kernel<<<grid_for((size_t)max_pos * a.half), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
