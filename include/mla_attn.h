@@ -518,6 +518,40 @@ MLA_API mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q
                                        void* cuda_stream);
 
 /*
+ * The attention weight that each cached key receives from a step's new tokens, added to what its
+ * slot holds: what mla_paged_evict goes by.  Over the tokens i of sequence b, all heads h and the
+ * keys that token i sees (all as in mla_latent_tree_fwd, whose arguments these are), with
+ *   s_ihj = softmax_scale * (W_K[h] c_j . q_nope[i,h] + k_pe_j . q_pe[i,h])
+ *
+ *   weights[slot of j] = decay * weights[slot of j] + sum_{i,h} softmax_j(s_ih)_j   j < ctx, cached
+ *                      =                              sum_{i,h} softmax_j(s_ih)_j   a new token's key
+ *
+ * in fp32, with scores that are exact to about 2^-17 of their size.  With decay 0 nothing is read
+ * from weights, whatever it holds.  A hidden key gets nothing from a row, whatever it holds, and a
+ * row that sees nothing gives nothing.  Sequences without new tokens are left as they are, and so
+ * are all slots behind kv_len[b].  The weights of one token sum to H.  To let the last tokens of a prompt
+ * observe the whole of it, call with those tokens' queries alone and decay 0.
+ *
+ *   weights [num_pages, page_size] float.  The sequences of a call have pages of their own: a slot
+ *   of two of them gets the sum of one.
+ * Results do not depend on how the work is shared out but through the order of fp32 sums, which
+ * the sizes and lengths fix: the same call gives the same bits.  workspace:
+ * mla_latent_key_weights_workspace_bytes(T, H, B) bytes, zeroed once.  Limits and device-side
+ * problems as for mla_latent_tree_fwd; a key on a page outside the pool counts as zeros.
+ * MLA_ERR_ARG for a decay that is not finite.
+ */
+MLA_API size_t mla_latent_key_weights_workspace_bytes(int T, int H, int B);
+MLA_API mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t* q_pe,
+                                          const uint16_t* c_pages, const uint16_t* pe_pages,
+                                          int num_pages, int page_size,
+                                          const int32_t* block_table, int max_pages,
+                                          const int32_t* kv_len, const int32_t* cu_q,
+                                          const int64_t* draft_mask, const uint16_t* w_kvb, int B,
+                                          int T, int H, float softmax_scale, float decay,
+                                          float* weights, void* workspace, size_t workspace_bytes,
+                                          void* cuda_stream);
+
+/*
  * The rows that a sequence's cache keeps within its budget.  weights [num_pages, page_size] float
  * holds a weight per slot (mla_latent_key_weights accumulates the attention that each cached key
  * receives).  Of sequence b's n = kv_len[b] rows, k = min(n, budget[b]) are kept: all of them if

@@ -13,7 +13,8 @@ _BINDING_NAMES = ("MlaAttnError", "mla_attn_fwd", "mla_attn_workspace_bytes",
                   "mla_rope_frequencies", "RopeConfig", "mla_attn_masked_fwd",
                   "mla_latent_decode_fwd", "mla_oproj_fwd", "mla_paged_plan", "PagedPlan",
                   "mla_latent_append", "mla_latent_tree_fwd", "mla_attn_varlen_fwd",
-                  "mla_rope_apply", "mla_paged_evict", "PagedEviction", "mla_latent_compact")
+                  "mla_rope_apply", "mla_paged_evict", "PagedEviction", "mla_latent_compact",
+                  "mla_latent_key_weights")
 
 
 def __getattr__(name):

@@ -74,7 +74,8 @@ EXPORTED = ("mla_attn_workspace_bytes", "mla_attn_fwd", "mla_attn_fwd_ex",
             "mla_attn_varlen_workspace_bytes", "mla_attn_varlen_fwd",
             "mla_latent_append", "mla_latent_tree_workspace_bytes", "mla_latent_tree_fwd",
             "mla_rope_frequencies_dim", "mla_rope_table_dim", "mla_rope_apply", "mla_paged_evict",
-            "mla_latent_compact")
+            "mla_latent_compact", "mla_latent_key_weights_workspace_bytes",
+            "mla_latent_key_weights")
 
 
 def library():
@@ -154,6 +155,11 @@ def library():
         lib.mla_rope_apply.restype = i
         lib.mla_rope_apply.argtypes = [p, i64, i64, p, i64, i64, i, i, i, i, p, p, i, i, i, i, p, sz,
                                        p]
+        lib.mla_latent_key_weights_workspace_bytes.restype = sz
+        lib.mla_latent_key_weights_workspace_bytes.argtypes = [i, i, i]
+        lib.mla_latent_key_weights.restype = i
+        lib.mla_latent_key_weights.argtypes = [p, p, p, p, i, i, p, i, p, p, p, p, i, i, i, f, f, p,
+                                               p, sz, p]
         lib.mla_paged_evict.restype = i
         lib.mla_paged_evict.argtypes = [p, i, i, p, i, p, p, i, i, i, p, i, p, p, p, p, sz, p]
         lib.mla_latent_compact.restype = i
@@ -662,6 +668,38 @@ def mla_attn_varlen_fwd(q_nope, q_pe, k_nope, k_pe, v, cu_seqlens, softmax_scale
                  v.data_ptr(), ctypes.addressof(strides), cu_seqlens.data_ptr(), B, T, H, Hkv,
                  float(softmax_scale), out.data_ptr()))
     return out
+
+
+def mla_latent_key_weights(q_nope, q_pe, c_pages, pe_pages, block_table, kv_len, cu_q, draft_mask,
+                           w_kvb, softmax_scale: float, weights, decay: float = 1.0,
+                           workspace: "Workspace | None" = None, stream=None):
+    """Adds up the attention weight that each cached key receives from a step's new tokens.
+
+    The arguments are those of mla_latent_tree_fwd (the tokens' rows appended); weights [num_pages,
+    page_size] float32, one per slot, updated in place: a cached key's is multiplied by ``decay``
+    and goes on from there (0: whatever it held), a new token's begins.  Returns weights."""
+    dev = q_nope.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    T, H = q_nope.shape[:2]
+    num_pages, page_size = c_pages.shape[:2]
+    B, max_pages = block_table.shape
+    _check_all(dev, torch.bfloat16, (
+        ("q_nope", q_nope, (T, H, 128)), ("q_pe", q_pe, (T, H, 64)),
+        ("c_pages", c_pages, (num_pages, page_size, 512)),
+        ("pe_pages", pe_pages, (num_pages, page_size, 64)), ("w_kvb", w_kvb, (H * 256, 512))))
+    _check_all(dev, torch.int32, (("block_table", block_table, (B, max_pages)),
+                                  ("kv_len", kv_len, (B,)), ("cu_q", cu_q, (B + 1,))))
+    _check(weights, "weights", torch.float32, (num_pages, page_size), dev)
+    if draft_mask is not None:
+        _check(draft_mask, "draft_mask", torch.int64, (T,), dev)
+    nbytes = library().mla_latent_key_weights_workspace_bytes(T, H, B)
+    _enqueue("mla_latent_key_weights", dev, stream, workspace, nbytes, (
+        q_nope.data_ptr(), q_pe.data_ptr(), c_pages.data_ptr(), pe_pages.data_ptr(), num_pages,
+        page_size, block_table.data_ptr(), max_pages, kv_len.data_ptr(), cu_q.data_ptr(),
+        _addr(draft_mask), w_kvb.data_ptr(), B, T, H, float(softmax_scale), float(decay),
+        weights.data_ptr()))
+    return weights
 
 
 class PagedEviction(NamedTuple):

@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmla_attn.so")
 SOURCES = ["host.cu", "decode.cu", "prefill.cu", "noalloc.cu", "rope.cu", "mask.cu", "latent.cu",
            "oproj.cu", "paged.cu", "tree.cu",
-           "tree_proj.cu", "rope_apply.cu", "evict.cu"]
+           "tree_proj.cu", "rope_apply.cu", "evict.cu", "key_weights.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

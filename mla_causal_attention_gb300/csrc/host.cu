@@ -134,6 +134,32 @@ TreeLayout tree_layout(int T, int H, int B, int sms) {
   return l;
 }
 
+// Workspace of the key weights: the status word; the queries folded into the latent space in two
+// parts [T, H, 1024] bf16 and each row's log-sum; the tree attention's partition with two partial
+// (max, sum) of 128 rows per CTA pair; the sum's partition, with two partial sums of 256 keys and two
+// counters per pair.
+struct KeyWeightsLayout {
+  size_t q_lat, lse, tile0, unit0, range0, first, part_note, part_ml, step0, count, part_sum, total;
+  int pairs;
+};
+KeyWeightsLayout key_weights_layout(int T, int H, int B, int sms) {
+  KeyWeightsLayout l;
+  l.pairs = std::min(std::max(1, sms / 2), 256);  // the partition has a thread per pair
+  l.q_lat = kStatusBytes;
+  l.lse = l.q_lat + r256((size_t)T * H * 1024 * 2);
+  l.tile0 = l.lse + r256((size_t)T * H * 4);
+  l.unit0 = l.tile0 + r256((size_t)(B + 1) * 8);
+  l.range0 = l.unit0 + r256((size_t)(B + 1) * 8);
+  l.first = l.range0 + r256((size_t)(l.pairs + 3) * 8);
+  l.part_note = l.first + r256((size_t)l.pairs * 48);
+  l.part_ml = l.part_note + r256((size_t)l.pairs * 32);
+  l.step0 = l.part_ml + (size_t)2 * l.pairs * 128 * 2 * 4;
+  l.count = l.step0 + r256((size_t)(B + 1) * 8);
+  l.part_sum = l.count + r256((size_t)2 * l.pairs * 4);
+  l.total = l.part_sum + (size_t)2 * l.pairs * 256 * 4;
+  return l;
+}
+
 // Rotary workspace: rotated queries [B,H,Tq,64] then rotated new rotary keys [B,Tq,64],
 // each on a 256-byte boundary, after the attention call's own workspace.
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -854,6 +880,71 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
   a.B = B; a.T = T; a.H = H; a.pairs = lay.pairs;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   return launch_latent_tree(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+size_t mla_latent_key_weights_workspace_bytes(int T, int H, int B) {
+  if (T < 1 || H < 1 || H > 1024 || B < 1) return 0;
+  int sms = 0;
+  if (check_device(&sms) != MLA_OK || sms <= 0) sms = 152;
+  return key_weights_layout(T, H, B, sms).total;
+}
+
+mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t* q_pe,
+                                  const uint16_t* c_pages, const uint16_t* pe_pages,
+                                  int num_pages, int page_size, const int32_t* block_table,
+                                  int max_pages, const int32_t* kv_len, const int32_t* cu_q,
+                                  const int64_t* draft_mask, const uint16_t* w_kvb, int B, int T,
+                                  int H, float softmax_scale, float decay, float* weights,
+                                  void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  if (!q_nope || !q_pe || !c_pages || !pe_pages || !block_table || !kv_len || !cu_q || !w_kvb ||
+      !weights)
+    return MLA_ERR_NULL;
+  if (!workspace) return MLA_ERR_WORKSPACE;
+  const mla_status ps = check_pool(num_pages, page_size);
+  if (ps != MLA_OK) return ps;
+  if (B < 1 || T < 1 || H < 1 || H > 1024 || max_pages < 1 || B > (1 << 20) ||
+      (int64_t)max_pages * page_size > (1 << 30) || (int64_t)T * H > (int64_t(1) << 26))
+    return MLA_ERR_SHAPE;
+  if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(c_pages) || !aligned16(pe_pages) ||
+      !aligned16(w_kvb) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(weights) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(kv_len) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(cu_q) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(draft_mask) & 7u) != 0)
+    return MLA_ERR_ALIGN;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0f) || !std::isfinite(decay))
+    return MLA_ERR_ARG;
+  int sms = 0;
+  const mla_status st = check_device(&sms);
+  if (st != MLA_OK) return st;
+  const KeyWeightsLayout lay = key_weights_layout(T, H, B, sms);
+  if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  KeyWeightsArgs k{};
+  TreeArgs& a = k.t;
+  a.q_nope = q_nope; a.q_pe = q_pe; a.c_pages = c_pages; a.pe_pages = pe_pages;
+  a.block_table = block_table; a.kv_len = kv_len; a.cu_q = cu_q; a.draft_mask = draft_mask;
+  a.w_kvb = w_kvb;
+  a.status = reinterpret_cast<int*>(w);
+  a.q_lat = reinterpret_cast<uint16_t*>(w + lay.q_lat);
+  a.tile0 = reinterpret_cast<int64_t*>(w + lay.tile0);
+  a.unit0 = reinterpret_cast<int64_t*>(w + lay.unit0);
+  a.range0 = reinterpret_cast<int64_t*>(w + lay.range0);
+  a.first = reinterpret_cast<int4*>(w + lay.first);
+  a.part_note = reinterpret_cast<int4*>(w + lay.part_note);
+  a.part_ml = reinterpret_cast<float*>(w + lay.part_ml);
+  a.num_pages = num_pages; a.page_shift = page_shift(page_size); a.max_pages = max_pages;
+  a.B = B; a.T = T; a.H = H; a.pairs = lay.pairs;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  k.lse = reinterpret_cast<float*>(w + lay.lse);
+  k.steps.step0 = reinterpret_cast<int64_t*>(w + lay.step0);
+  k.steps.count = reinterpret_cast<int*>(w + lay.count);
+  k.part_sum = reinterpret_cast<float*>(w + lay.part_sum);
+  k.weights = weights; k.decay = decay;
+  return launch_key_weights(k, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }

@@ -301,8 +301,27 @@ struct TreeArgs {
   float scale_log2;
 };
 cudaError_t launch_tree_fold(const TreeArgs& a, cudaStream_t stream);  // q_lat, partition
+// The key weights' share of the work (see key_weights.cu): steps in front of each sequence and in
+// all [B+1], and counters of the shared key tiles' segments [2 pairs].
+struct KeySteps {
+  int64_t* step0;
+  int* count;
+};
+// The folded query in two bf16 parts, q_lat [T,H,1024]; both partitions.
+cudaError_t launch_tree_fold_two(const TreeArgs& a, const KeySteps& steps, cudaStream_t stream);
 cudaError_t launch_tree_up(const TreeArgs& a, cudaStream_t stream);    // merge, out
 cudaError_t launch_latent_tree(const TreeArgs& a, cudaStream_t stream);
+
+// The attention weight that each cached key receives (see mla_latent_key_weights).
+struct KeyWeightsArgs {
+  TreeArgs t;        // q_lat: workspace [T,H,1024]; w/o out and part_acc
+  KeySteps steps;    // workspace
+  float* lse;        // workspace [T,H]: log2 of each row's sum of weights; infinite without keys
+  float* part_sum;   // workspace [2 pairs][256]: sums of a key tile's segments
+  float* weights;    // [num_pages, page_size]
+  float decay;
+};
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream);
 
 // Causal attention over packed prompts (see mla_attn_varlen_fwd).  Strides in elements.
 struct VarlenArgs {

@@ -270,6 +270,49 @@ static __device__ __noinline__ void tree_partition(const TreeArgs& a, uint8_t* r
   }
 }
 
+// ---- the key weights' share ---------------------------------------------------------------
+// Key tiles of 256 rows against tiles of 128 query rows: sequence b has P_b R_b steps, in the order
+// (sequence, key tile, row tile), and pair c of the P = min(pairs, W) that are used does steps
+// [W c / P, W (c + 1) / P).
+constexpr int kKeyTile = 256;
+__device__ __forceinline__ int key_tiles(const TreeSeq& s) {
+  return s.n > 0 ? (s.kv + kKeyTile - 1) / kKeyTile : 0;
+}
+__device__ __forceinline__ int row_tiles(const TreeArgs& a, const TreeSeq& s) {
+  return (s.n * a.H + kRows - 1) / kRows;
+}
+
+// By one block of 256 threads: the steps in front of each sequence; the counters cleared.
+static __device__ __noinline__ void key_steps(const TreeArgs& a, const KeySteps& k) {
+  __shared__ int64_t s_w[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 2 * a.pairs; i += 256) k.count[i] = 0;
+  int64_t W = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 256) {
+    int64_t w = 0;
+    if (b0 + tid < a.B) {
+      const TreeSeq s = tree_seq(a, b0 + tid);
+      w = (int64_t)key_tiles(s) * row_tiles(a, s);
+    }
+    int64_t inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) s_w[warp] = inc;
+    __syncthreads();
+    int64_t before = W;
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) before += s_w[i];
+      W += s_w[i];
+    }
+    if (b0 + tid < a.B) k.step0[b0 + tid] = before + inc - w;
+    __syncthreads();
+  }
+  if (tid == 0) k.step0[a.B] = W;
+}
+
 // Zeroes the mixes of sequences that have new tokens and no keys: no unit writes them, and the folded
 // queries in their place would be taken for mixes.  By `threads` threads of each pair's CTAs.
 __device__ __forceinline__ void clear_keyless(const TreeArgs& a, int pair, int thread, int threads) {

@@ -42,8 +42,9 @@ static_assert(kSmem <= 232448 && kPartSmem <= kSmem, "shared memory per block");
 struct ProjParams {
   CUtensorMap tm_x;  // rows    {K, T, H}, boxes {64, 128, 1}
   CUtensorMap tm_w;  // w_kvb   {512, H * 256}, boxes {64, 128}
-  CUtensorMap tm_y;  // fold: q_lat {512, T, H}, boxes {64, 32, 1}
+  CUtensorMap tm_y;  // fold: q_lat {512, T, H}, boxes {64, 32, 1}; in two parts {1024, T, H}
   TreeArgs a;
+  KeySteps steps;    // fold in two parts: what its last block but one makes
   int blocks_y;      // blocks per head and part along the tokens
   int parts;         // parts of the output columns, a block each: 1, or (few tokens) 2
   int merge;         // up: the blocks merge their rows themselves (up to kMergeTokens tokens)
@@ -152,8 +153,10 @@ __device__ __forceinline__ void merge_row(const TreeArgs& a, const int4* note, i
 // Warps: 0 TMA, 1 MMA, 4-7 epilogue.  The fold launch has one block more, which makes the partition.
 // It is the last: where the others fill every SM (8 heads from 2305 tokens on) it runs behind one of
 // them, about 2 us of 35.
-template <bool kUp>
+// kTwo (a fold): the result in two parts, and one block more, for the key weights' partition.
+template <bool kUp, bool kTwo = false>
 __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant__ ProjParams p) {
+  static_assert(!(kUp && kTwo), "two parts are a fold's");
   constexpr int kKs = kUp ? 8 : 2, kNb = kUp ? 1 : 2, kN = kUp ? 128 : 256;
   constexpr uint32_t kSlots = kUp ? 5 : 3;
   grid_dep_launch();
@@ -161,6 +164,10 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
   extern __shared__ __align__(16) uint8_t smem_raw[];
   if (!kUp && blockIdx.x == gridDim.x - 1) {
     tree_partition(a, smem_raw);
+    return;
+  }
+  if (kTwo && blockIdx.x == gridDim.x - 2) {
+    key_steps(a, p.steps);
     return;
   }
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -343,28 +350,57 @@ __global__ void __launch_bounds__(256, 1) tree_proj_kernel(const __grid_constant
         } else {
           // 64 columns of this warp's 32 rows at a time through one of its two 4 KB stages and a
           // tensor store (lanes writing their own rows touch 32 lines per instruction).
-#pragma unroll 1
-          for (int c = 0; c < kN / 64; ++c) {
-            uint8_t* stage = smem + kOffRing + kSlots * kSub + ((warp & 3) * 2 + (c & 1)) * 4096;
-            if (lane == 0) bulk_wait_read_but_one();  // the stage's last store has read it
-            __syncwarp();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t o[32];
-              take(2 * c + q, o, c == kN / 64 - 1 && q == 1);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + e) ^ (lane & 7)) << 4)) =
-                    pack8(o, e);
-            }
+          const auto store = [&](const uint8_t* stage, int col) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-              // A group for every stage, also where all its rows lie behind T: the wait above
-              // counts groups.
+              // A group for every stage, also where all its rows lie behind T: the wait for a free
+              // stage counts groups.
               if (i * kM + (warp & 3) * 32 < a.T)
-                tma_store_3d(&p.tm_y, stage, 256 * nb + 64 * c, i * kM + (warp & 3) * 32, h);
+                tma_store_3d(&p.tm_y, stage, col, i * kM + (warp & 3) * 32, h);
               bulk_commit_group();
+            }
+          };
+#pragma unroll 1
+          for (int c = 0; c < kN / 64; ++c) {
+            uint8_t* stages = smem + kOffRing + kSlots * kSub + (warp & 3) * 2 * 4096;
+            if constexpr (kTwo) {
+              uint32_t o[2][32];
+              take(2 * c, o[0], false);
+              take(2 * c + 1, o[1], c == kN / 64 - 1);
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                if (lane == 0) bulk_wait_read_but_one();  // this part's last store has read the stage
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    *reinterpret_cast<uint4*>(stages + part * 4096 + lane * 128 +
+                                              (((4 * q + e) ^ (lane & 7)) << 4)) = pack8(o[q], e);
+                    if (part == 0)
+#pragma unroll
+                      for (int k = 8 * e; k < 8 * e + 8; ++k) {  // what the rounding leaves, exactly
+                        const float x = __uint_as_float(o[q][k]);
+                        o[q][k] = __float_as_uint(x - bf16lo_to_f32(pack_bf16x2(x, 0.f)));
+                      }
+                  }
+                store(stages + part * 4096, 512 * part + 256 * nb + 64 * c);
+              }
+            } else {
+              uint8_t* stage = stages + (c & 1) * 4096;
+              if (lane == 0) bulk_wait_read_but_one();  // the stage's last store has read it
+              __syncwarp();
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                uint32_t o[32];
+                take(2 * c + q, o, c == kN / 64 - 1 && q == 1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + e) ^ (lane & 7)) << 4)) =
+                      pack8(o, e);
+              }
+              store(stage, 256 * nb + 64 * c);
             }
           }
         }
@@ -407,9 +443,10 @@ struct MapKey {
   const void* x;
   const void* w;
   const void* y;
-  int T, H, up;
+  int T, H, up, parts;
   bool operator==(const MapKey& o) const {
-    return x == o.x && w == o.w && y == o.y && T == o.T && H == o.H && up == o.up;
+    return x == o.x && w == o.w && y == o.y && T == o.T && H == o.H && up == o.up &&
+           parts == o.parts;
   }
 };
 struct MapEntry {
@@ -421,8 +458,8 @@ std::mutex g_mu;
 MapEntry g_maps[16];
 int g_next = 0;
 
-bool proj_maps(const TreeArgs& a, bool up, ProjParams* p) {
-  const MapKey key = {up ? a.q_lat : a.q_nope, a.w_kvb, a.q_lat, a.T, a.H, up};
+bool proj_maps(const TreeArgs& a, bool up, int parts, ProjParams* p) {
+  const MapKey key = {up ? a.q_lat : a.q_nope, a.w_kvb, a.q_lat, a.T, a.H, up, parts};
   std::lock_guard<std::mutex> lk(g_mu);
   for (const MapEntry& e : g_maps)
     if (e.valid && e.key == key) {
@@ -438,8 +475,9 @@ bool proj_maps(const TreeArgs& a, bool up, ProjParams* p) {
   const uint64_t wdims[2] = {kLD, (uint64_t)a.H * 256};
   const uint64_t wstrides[1] = {kLD * 2};
   const uint32_t wbox[2] = {64, 128};
-  const uint64_t ydims[3] = {kLD, (uint64_t)a.T, (uint64_t)a.H};
-  const uint64_t ystrides[2] = {(uint64_t)a.H * kLD * 2, kLD * 2};
+  const uint64_t ywidth = (uint64_t)kLD * parts;
+  const uint64_t ydims[3] = {ywidth, (uint64_t)a.T, (uint64_t)a.H};
+  const uint64_t ystrides[2] = {(uint64_t)a.H * ywidth * 2, ywidth * 2};
   const uint32_t ybox[3] = {64, 32, 1};
   if (!encode_bf16_tiled(&p->tm_x, key.x, 3, dims, strides, box) ||
       !encode_bf16_tiled(&p->tm_w, key.w, 2, wdims, wstrides, wbox) ||
@@ -465,6 +503,9 @@ cudaError_t set_attributes() {
   e = cudaFuncSetAttribute(tree_proj_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmem);
   if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(tree_proj_kernel<false, true>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(tree_proj_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmem);
   if (e != cudaSuccess) return e;
@@ -483,7 +524,7 @@ cudaError_t launch_tree_fold(const TreeArgs& a, cudaStream_t stream) {
   cudaError_t e = set_attributes();
   if (e != cudaSuccess) return e;
   ProjParams p;
-  if (!proj_maps(a, false, &p)) return cudaErrorInvalidValue;
+  if (!proj_maps(a, false, 1, &p)) return cudaErrorInvalidValue;
   p.a = a;
   p.blocks_y = blocks_per_head(a);
   p.parts = a.T <= kM && a.H <= a.pairs ? 2 : 1;
@@ -492,9 +533,23 @@ cudaError_t launch_tree_fold(const TreeArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+cudaError_t launch_tree_fold_two(const TreeArgs& a, const KeySteps& steps, cudaStream_t stream) {
+  cudaError_t e = set_attributes();
+  if (e != cudaSuccess) return e;
+  ProjParams p;
+  if (!proj_maps(a, false, 2, &p)) return cudaErrorInvalidValue;
+  p.a = a;
+  p.steps = steps;
+  p.blocks_y = blocks_per_head(a);
+  p.parts = a.T <= kM && a.H <= a.pairs ? 2 : 1;
+  p.merge = 0;
+  tree_proj_kernel<false, true><<<a.H * p.blocks_y * p.parts + 2, 256, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_tree_up(const TreeArgs& a, cudaStream_t stream) {
   ProjParams p;
-  if (!proj_maps(a, true, &p)) return cudaErrorInvalidValue;
+  if (!proj_maps(a, true, 1, &p)) return cudaErrorInvalidValue;
   p.a = a;
   p.blocks_y = blocks_per_head(a);
   p.parts = 1;

@@ -160,6 +160,51 @@ def test_compact_refuses_alignment(lib, base):
         assert _accepted(lib.mla_latent_compact(*[a[n] for n in COMPACT]))
 
 
+WEIGHTS = ["q_nope", "q_pe", "c_pages", "pe_pages", "num_pages", "page_size", "block_table",
+           "max_pages", "kv_len", "cu_q", "draft_mask", "w_kvb", "B", "T", "H", "scale", "decay",
+           "weights", "workspace", "workspace_bytes", "stream"]
+
+
+def _weights_args(lib, base):
+    a = {n: base + 1024 * i for i, n in enumerate(WEIGHTS)}
+    a.update(num_pages=8, page_size=16, max_pages=4, B=2, T=3, H=4, scale=0.1, decay=1.0,
+             workspace_bytes=lib.mla_latent_key_weights_workspace_bytes(3, 4, 2), stream=None)
+    return a
+
+
+@pytest.mark.parametrize("change,want", [
+    ({"q_nope": None}, S.ERR_NULL), ({"q_pe": None}, S.ERR_NULL), ({"c_pages": None}, S.ERR_NULL),
+    ({"pe_pages": None}, S.ERR_NULL), ({"block_table": None}, S.ERR_NULL),
+    ({"kv_len": None}, S.ERR_NULL), ({"cu_q": None}, S.ERR_NULL), ({"w_kvb": None}, S.ERR_NULL),
+    ({"weights": None}, S.ERR_NULL), ({"workspace": None}, S.ERR_WORKSPACE),
+    ({"B": 0}, S.ERR_SHAPE), ({"T": 0}, S.ERR_SHAPE), ({"H": 0}, S.ERR_SHAPE),
+    ({"H": 1025}, S.ERR_SHAPE), ({"T": (1 << 24) + 1}, S.ERR_SHAPE), ({"max_pages": 0}, S.ERR_SHAPE),
+    ({"page_size": 20}, S.ERR_SHAPE), ({"num_pages": 0}, S.ERR_SHAPE),
+    ({"scale": 0.0}, S.ERR_ARG), ({"scale": float("inf")}, S.ERR_ARG),
+    ({"decay": float("nan")}, S.ERR_ARG), ({"decay": float("inf")}, S.ERR_ARG),
+])
+def test_weights_refuse(lib, base, change, want):
+    a = _weights_args(lib, base)
+    a.update(change)
+    assert lib.mla_latent_key_weights(*[a[n] for n in WEIGHTS]) == want
+
+
+def test_weights_refuse_alignment_and_small_workspaces(lib, base):
+    for name, off in [("q_nope", 8), ("pe_pages", 8), ("weights", 2), ("draft_mask", 4), ("cu_q", 2)]:
+        a = _weights_args(lib, base)
+        a[name] += off
+        assert lib.mla_latent_key_weights(*[a[n] for n in WEIGHTS]) == S.ERR_ALIGN, name
+    size = lib.mla_latent_key_weights_workspace_bytes
+    assert size(0, 4, 2) == size(3, 0, 2) == size(3, 1025, 2) == size(3, 4, 0) == 0
+    assert size(3, 4, 2) > 3 * 4 * (2048 + 4)
+    a = _weights_args(lib, base)
+    if not torch.cuda.is_available():
+        assert _accepted(lib.mla_latent_key_weights(*[a[n] for n in WEIGHTS]))
+    else:
+        a["workspace_bytes"] -= 1
+        assert lib.mla_latent_key_weights(*[a[n] for n in WEIGHTS]) == S.ERR_WORKSPACE
+
+
 def test_tables_refuse_other_widths(lib):
     for dim in (0, 1, 63, 258):
         with pytest.raises(mla.MlaAttnError):
