@@ -536,11 +536,11 @@ MLA_API mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q
  *   of two of them gets the sum of one.
  * Results do not depend on how the work is shared out but through the order of fp32 sums, which
  * the sizes and lengths fix: the same call gives the same bits.  workspace:
- * mla_latent_key_weights_workspace_bytes(T, H, B) bytes, zeroed once.  Limits and device-side
- * problems as for mla_latent_tree_fwd; a key on a page outside the pool counts as zeros.
- * MLA_ERR_ARG for a decay that is not finite.
+ * mla_latent_key_weights_workspace_bytes(T, H, B, max_pages * page_size) bytes, zeroed once (up to
+ * 256 MB of it for scores).  Limits and device-side problems as for mla_latent_tree_fwd; a key on
+ * a page outside the pool counts as zeros.  MLA_ERR_ARG for a decay that is not finite.
  */
-MLA_API size_t mla_latent_key_weights_workspace_bytes(int T, int H, int B);
+MLA_API size_t mla_latent_key_weights_workspace_bytes(int T, int H, int B, int max_keys);
 MLA_API mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t* q_pe,
                                           const uint16_t* c_pages, const uint16_t* pe_pages,
                                           int num_pages, int page_size,
@@ -598,8 +598,9 @@ MLA_API mla_status mla_paged_evict(const float* weights, int num_pages, int page
  * Device-side problems (the call completes): kept_len outside [0, K] (MLA_ERR_KVLEN, clamped); an
  * entry below its own index or past the table (MLA_ERR_KVLEN), or a page outside the pool
  * (MLA_ERR_PAGE): that row is not moved.  A list that does not rise moves rows that others have
- * overwritten.  workspace: 256 bytes (the status word), zeroed once.
+ * overwritten.  workspace: mla_latent_compact_workspace_bytes(B, K) bytes, zeroed once.
  */
+MLA_API size_t mla_latent_compact_workspace_bytes(int B, int K);
 MLA_API mla_status mla_latent_compact(uint16_t* c_pages, uint16_t* pe_pages, float* weights,
                                       int num_pages, int page_size, const int32_t* block_table,
                                       int max_pages, const int32_t* kept, int K,

@@ -74,7 +74,7 @@ EXPORTED = ("mla_attn_workspace_bytes", "mla_attn_fwd", "mla_attn_fwd_ex",
             "mla_attn_varlen_workspace_bytes", "mla_attn_varlen_fwd",
             "mla_latent_append", "mla_latent_tree_workspace_bytes", "mla_latent_tree_fwd",
             "mla_rope_frequencies_dim", "mla_rope_table_dim", "mla_rope_apply", "mla_paged_evict",
-            "mla_latent_compact", "mla_latent_key_weights_workspace_bytes",
+            "mla_latent_compact", "mla_latent_compact_workspace_bytes", "mla_latent_key_weights_workspace_bytes",
             "mla_latent_key_weights")
 
 
@@ -156,12 +156,14 @@ def library():
         lib.mla_rope_apply.argtypes = [p, i64, i64, p, i64, i64, i, i, i, i, p, p, i, i, i, i, p, sz,
                                        p]
         lib.mla_latent_key_weights_workspace_bytes.restype = sz
-        lib.mla_latent_key_weights_workspace_bytes.argtypes = [i, i, i]
+        lib.mla_latent_key_weights_workspace_bytes.argtypes = [i, i, i, i]
         lib.mla_latent_key_weights.restype = i
         lib.mla_latent_key_weights.argtypes = [p, p, p, p, i, i, p, i, p, p, p, p, i, i, i, f, f, p,
                                                p, sz, p]
         lib.mla_paged_evict.restype = i
         lib.mla_paged_evict.argtypes = [p, i, i, p, i, p, p, i, i, i, p, i, p, p, p, p, sz, p]
+        lib.mla_latent_compact_workspace_bytes.restype = sz
+        lib.mla_latent_compact_workspace_bytes.argtypes = [i, i]
         lib.mla_latent_compact.restype = i
         lib.mla_latent_compact.argtypes = [p, p, p, i, i, p, i, p, i, p, i, p, sz, p]
         _lib = lib
@@ -693,7 +695,7 @@ def mla_latent_key_weights(q_nope, q_pe, c_pages, pe_pages, block_table, kv_len,
     _check(weights, "weights", torch.float32, (num_pages, page_size), dev)
     if draft_mask is not None:
         _check(draft_mask, "draft_mask", torch.int64, (T,), dev)
-    nbytes = library().mla_latent_key_weights_workspace_bytes(T, H, B)
+    nbytes = library().mla_latent_key_weights_workspace_bytes(T, H, B, max_pages * page_size)
     _enqueue("mla_latent_key_weights", dev, stream, workspace, nbytes, (
         q_nope.data_ptr(), q_pe.data_ptr(), c_pages.data_ptr(), pe_pages.data_ptr(), num_pages,
         page_size, block_table.data_ptr(), max_pages, kv_len.data_ptr(), cu_q.data_ptr(),
@@ -771,7 +773,8 @@ def mla_latent_compact(c_pages, pe_pages, block_table, kept, kept_len, weights=N
                                   ("kept", kept, (B, K)), ("kept_len", kept_len, (B,))))
     if weights is not None:
         _check(weights, "weights", torch.float32, (num_pages, page_size), dev)
-    _enqueue("mla_latent_compact", dev, stream, workspace, 256, (
+    nbytes = library().mla_latent_compact_workspace_bytes(B, K)
+    _enqueue("mla_latent_compact", dev, stream, workspace, nbytes, (
         c_pages.data_ptr(), pe_pages.data_ptr(), _addr(weights), num_pages, page_size,
         block_table.data_ptr(), max_pages, kept.data_ptr(), K, kept_len.data_ptr(), B))
 

@@ -1,7 +1,8 @@
 // evict.cu -- which rows of a paged cache stay within a budget, and moving them together.
 //
 //   paged_evict_kernel     the rows that each sequence keeps, and the pages that come free
-//   latent_compact_kernel  the kept rows to the front of their sequence's pages, in place
+//   compact_chunks_kernel, latent_compact_kernel
+//                          the kept rows to the front of their sequence's pages, in place
 #include <cuda.h>
 
 #include <algorithm>
@@ -246,19 +247,66 @@ __global__ void __launch_bounds__(kEvThreads) paged_evict_kernel(const PagedEvic
 }
 
 // ---- compaction -------------------------------------------------------------------------
-// Row kept[i] of a sequence becomes its row i, for rising lists.  kept[i] >= i, so within a run of
-// rows read at a time every source lies at or behind the run's own targets: a CTA that takes the
-// runs in order, reads a whole run, and writes it after a barrier, never overwrites what is still
-// to be read.  Columns do not meet, so a row's 1152 bytes are cut into slices, a CTA each.
-// Bound by HBM: 2 * 1156 bytes per row that moves.
-constexpr int kCpThreads = 256;
-constexpr int kCpU = 8;  // rows of a thread in a run
+// Row kept[i] of a sequence becomes its row i, for rising lists, so kept[i] >= i.  Chunks of 32 rows
+// go to warps in order, as they come free.  A warp reads its chunk's rows into shared memory, says
+// so, waits until every row that lies where it is going to write has been read by the chunk it belongs to,
+// and writes.  Those are the rows kept[k] in [32 c, 32 c + 32), which belong to chunks up to
+// c: all of them have been handed out before, and reading waits for nothing, so every wait ends.
+// Where half of the rows go, the chunks waited for are half as far down and long since read; where
+// few go, they are the two or three before, which are being read at the same time.
+//
+// Bound by HBM: 2 * 1156 bytes per row that moves; six warps per SM with 36 KB each keep 33 MB in
+// flight.  (A CTA per sequence and slice of the columns, which reads and writes runs of rows in turn,
+// took 107 us for 64 sequences and 460 for 65536 rows of one.)
+constexpr int kCpRows = 32;                      // of a chunk, a lane each
+constexpr int kCpWarps = 6;
+constexpr int kCpSlot = kCpRows * (1024 + 128);  // a chunk's latent rows, then its rotary keys
+constexpr int kCpSmem = kCpWarps * kCpSlot + 64;
+static_assert(kCpSmem <= 232448, "shared memory per block");
 
-struct CompactSeq {
-  const int32_t* table;
-  const int32_t* kept;
-  int k;
-};
+__device__ __forceinline__ int64_t kept_rows(const LatentCompactArgs& a, int b) {
+  return min((int64_t)min(max(a.kept_len[b], 0), a.K), (int64_t)a.max_pages << a.page_shift);
+}
+
+// By one block: the chunks in front of each sequence, no chunk taken, none read.
+__global__ void __launch_bounds__(kEvThreads) compact_chunks_kernel(const LatentCompactArgs a) {
+  grid_dep_launch();
+  __shared__ int part[kEvWarps];
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kEvThreads) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < a.B) {
+      const int64_t k = kept_rows(a, b);
+      if (k != a.kept_len[b]) set_status(a.status, MLA_ERR_KVLEN);
+      n = (int)((k + kCpRows - 1) / kCpRows);
+    }
+    int total;
+    const int own = block_scan(n, part, &total);
+    if (b < a.B) a.chunk0[b] = before + own;
+    before += total;
+  }
+  if (threadIdx.x == 0) {
+    a.chunk0[a.B] = before;
+    a.chunk0[a.B + 1] = 0;  // the next chunk to hand out
+  }
+  for (int64_t i = threadIdx.x; i < before; i += kEvThreads) a.read[i] = 0;
+}
+
+// The first of n rising values that is >= x, by a warp.
+__device__ __forceinline__ int first_at_least(const int32_t* v, int n, int x, int lane) {
+  int lo = 0, hi = n;  // every value before lo is below x, hi's is not (or is the end)
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + (lane + 1) * step - 1;
+    const uint32_t below = __ballot_sync(0xffffffffu, at < hi && v[at] < x);
+    const int k = __popc(below);  // whole steps below x
+    lo += k * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
 // The slot of position p, or -1 where the table holds no page.
 __device__ __forceinline__ int64_t slot_of(const LatentCompactArgs& a, const int32_t* table, int p) {
   const int page = table[p >> a.page_shift];
@@ -268,64 +316,102 @@ __device__ __forceinline__ int64_t slot_of(const LatentCompactArgs& a, const int
   }
   return ((int64_t)page << a.page_shift) + (p & ((1 << a.page_shift) - 1));
 }
-// Source and target of kept row i; false where it stays or the list is no such list.
-__device__ __forceinline__ bool move_of(const LatentCompactArgs& a, const CompactSeq& q, int i,
-                                        int64_t& from, int64_t& to) {
-  if (i >= q.k) return false;
-  const int p = q.kept[i];
-  if (p == i) return false;
-  if (p < i || p >= (int64_t)a.max_pages << a.page_shift) {
-    set_status(a.status, MLA_ERR_KVLEN);
-    return false;
-  }
-  from = slot_of(a, q.table, p);
-  to = slot_of(a, q.table, i);
-  return from >= 0 && to >= 0;
-}
 
-// kLanes: 16-byte pieces of a slice, a lane each.
-template <typename V, int kLanes>
-__device__ __forceinline__ void compact_rows(const LatentCompactArgs& a, const CompactSeq& q,
-                                             V* base, int pitch, int col) {
-  constexpr int kRowsPer = kCpThreads / kLanes;
-  const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
-  for (int i0 = 0; i0 < q.k; i0 += kCpU * kRowsPer) {
-    V v[kCpU];
-    int64_t to[kCpU];
-#pragma unroll
-    for (int u = 0; u < kCpU; ++u) {
-      int64_t from;
-      const bool moves = move_of(a, q, i0 + u * kRowsPer + row, from, to[u]);
-      if (moves)
-        v[u] = base[from * pitch + col + lane];
-      else
-        to[u] = -1;
+__global__ void __launch_bounds__(32 * kCpWarps) latent_compact_kernel(const LatentCompactArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kCpWarps * kCpSlot) + warp;
+  uint8_t* c_row = smem + warp * kCpSlot + lane * 1024;
+  uint8_t* pe_row = smem + warp * kCpSlot + kCpRows * 1024 + lane * 128;
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  grid_dep_wait();
+  const int64_t chunks = a.chunk0[a.B];
+  const uint64_t policy = l2_policy_evict_first();
+  uint32_t loads = 0;
+  for (;;) {
+    int64_t g = 0;
+    if (lane == 0)
+      g = (int64_t)atomicAdd(reinterpret_cast<unsigned long long*>(a.chunk0 + a.B + 1), 1ull);
+    g = __shfl_sync(0xffffffffu, g, 0);
+    if (g >= chunks) break;
+    int b = 0;  // the last sequence whose chunks begin at or before g
+    for (int hi = a.B; hi - b > 1;) {
+      const int step = (hi - b + 31) / 32, at = b + lane * step;
+      const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.chunk0[at] <= g);
+      b += (31 - __clz(le | 1u)) * step;
+      hi = min(hi, b + step);
     }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kCpU; ++u)
-      if (to[u] >= 0) base[to[u] * pitch + col + lane] = v[u];
+    const int64_t first = a.chunk0[b];
+    const int c = (int)(g - first), i = c * kCpRows + lane, k = (int)kept_rows(a, b);
+    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
+    const int32_t* kept = a.kept + (int64_t)b * a.K;
+    // Source and target of this lane's row; none where it stays, or the list is no such list.
+    int64_t from = -1, to = -1;
+    if (i < k) {
+      const int p = kept[i];
+      if (p < i || p >= (int64_t)a.max_pages << a.page_shift) {
+        set_status(a.status, MLA_ERR_KVLEN);
+      } else if (p != i) {
+        from = slot_of(a, table, p);
+        to = slot_of(a, table, i);
+      }
+    }
+    const bool moves = from >= 0 && to >= 0;
+    const int n = __popc(__ballot_sync(0xffffffffu, moves));
+    float w = 0.f;
+    if (n > 0) {
+      if (lane == 0) mbar_arrive_expect_tx(bar, n * (1024 + 128));
+      __syncwarp();
+      if (moves) {
+        bulk_g2s(c_row, a.c_pages + from * 512, 1024, bar, policy);
+        bulk_g2s(pe_row, a.pe_pages + from * 64, 128, bar, policy);
+        if (a.weights) w = a.weights[from];
+      }
+      // Meanwhile: the chunks that this one's targets are read by.
+      const int end = min(i - lane + kCpRows, k);
+      const int k0 = first_at_least(kept, k, i - lane, lane), k1 = first_at_least(kept, k, end, lane);
+      bool ok = true;
+      const uint32_t addr = smem_u32(bar);
+      const uint64_t t0 = globaltimer_ns();
+      while (ok && !mbar_try_wait(addr, loads & 1)) ok = globaltimer_ns() - t0 <= kWaitLimitNs;
+      ++loads;
+      asm volatile("" ::"f"(w) : "memory");  // the weight is here
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) atomicExch(a.read + g, 1);
+      for (int q = k0 / kCpRows + lane; ok && q < c && q * kCpRows < k1; q += 32) {
+        const int* flag = a.read + first + q;
+        int seen;
+        do {
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(flag) : "memory");
+          ok = seen != 0 || globaltimer_ns() - t0 <= kWaitLimitNs;
+        } while (ok && seen == 0);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) set_status(a.status, MLA_ERR_TIMEOUT);
+        // Rows may still be landing, which takes microseconds; the block ends behind them.
+        for (const uint64_t t1 = globaltimer_ns(); globaltimer_ns() - t1 < 2000000ull;) {
+        }
+        break;
+      }
+      asm volatile("fence.proxy.async;" ::: "memory");
+      if (moves) {
+        bulk_s2g(a.c_pages + to * 512, c_row, 1024);
+        bulk_s2g(a.pe_pages + to * 64, pe_row, 128);
+        if (a.weights) a.weights[to] = w;
+      }
+      bulk_commit_group();
+      bulk_wait_read_all();
+      __syncwarp();
+    } else if (lane == 0) {
+      atomicExch(a.read + g, 1);  // nothing of it is read
+    }
   }
-}
-
-template <int kLanes>
-__global__ void __launch_bounds__(kCpThreads) latent_compact_kernel(const LatentCompactArgs a) {
-  constexpr int kSlices = 64 / kLanes;  // of a latent row; the rotary key has 8 / kLanes
-  const int slices = kSlices + 8 / kLanes + (a.weights ? 1 : 0);
-  const int b = blockIdx.x / slices, slice = blockIdx.x % slices;
-  CompactSeq q;
-  q.table = a.block_table + (int64_t)b * a.max_pages;
-  q.kept = a.kept + (int64_t)b * a.K;
-  const int k = a.kept_len[b];
-  q.k = (int)min((int64_t)min(max(k, 0), a.K), (int64_t)a.max_pages << a.page_shift);
-  if (q.k != k) set_status(a.status, MLA_ERR_KVLEN);
-  if (slice < kSlices)
-    compact_rows<uint4, kLanes>(a, q, reinterpret_cast<uint4*>(a.c_pages), 64, slice * kLanes);
-  else if (slice < kSlices + 8 / kLanes)
-    compact_rows<uint4, kLanes>(a, q, reinterpret_cast<uint4*>(a.pe_pages), 8,
-                                (slice - kSlices) * kLanes);
-  else
-    compact_rows<float, 1>(a, q, a.weights, 1, 0);
 }
 
 }  // namespace
@@ -371,14 +457,33 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& in, cudaStream_t stream) {
 }
 
 cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};  // bit per device: smem attribute set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(latent_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kCpSmem);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_release);
+  }
+  compact_chunks_kernel<<<1, kEvThreads, 0, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
-  const unsigned more = a.weights ? 1 : 0;
-  // Slices of 128 bytes; of 32 where few sequences would leave SMs idle.
-  if ((int64_t)a.B * 9 >= 2 * sms)
-    latent_compact_kernel<8><<<(9 + more) * a.B, kCpThreads, 0, stream>>>(a);
-  else
-    latent_compact_kernel<2><<<(36 + more) * a.B, kCpThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int64_t chunks = (int64_t)a.B * ((a.K + kCpRows - 1) / kCpRows);  // at most
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, (chunks + kCpWarps - 1) / kCpWarps));
+  cfg.blockDim = dim3(32 * kCpWarps);
+  cfg.dynamicSmemBytes = kCpSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_compact_kernel, a);
 }
 
 }  // namespace mla

@@ -137,12 +137,17 @@ TreeLayout tree_layout(int T, int H, int B, int sms) {
 // Workspace of the key weights: the status word; the queries folded into the latent space in two
 // parts [T, H, 1024] bf16 and each row's log-sum; the tree attention's partition with two partial
 // (max, sum) of 128 rows per CTA pair; the sum's partition, with two partial sums of 256 keys and two
-// counters per pair.
+// counters per pair; scores that are kept between the two passes, as many as there can be up to
+// kMostKept bytes.
+constexpr size_t kMostKept = size_t(1) << 28;
 struct KeyWeightsLayout {
-  size_t q_lat, lse, tile0, unit0, range0, first, part_note, part_ml, step0, count, part_sum, total;
+  size_t q_lat, lse, tile0, unit0, range0, first, part_note, part_ml, store0, read0, step0, count,
+      part_sum, store, total;
+  int64_t room;  // floats of the store
+  bool all_kept;
   int pairs;
 };
-KeyWeightsLayout key_weights_layout(int T, int H, int B, int sms) {
+KeyWeightsLayout key_weights_layout(int T, int H, int B, int64_t keys, int sms) {
   KeyWeightsLayout l;
   l.pairs = std::min(std::max(1, sms / 2), 256);  // the partition has a thread per pair
   l.q_lat = kStatusBytes;
@@ -153,10 +158,30 @@ KeyWeightsLayout key_weights_layout(int T, int H, int B, int sms) {
   l.first = l.range0 + r256((size_t)(l.pairs + 3) * 8);
   l.part_note = l.first + r256((size_t)l.pairs * 48);
   l.part_ml = l.part_note + r256((size_t)l.pairs * 32);
-  l.step0 = l.part_ml + (size_t)2 * l.pairs * 128 * 2 * 4;
+  l.store0 = l.part_ml + (size_t)2 * l.pairs * 128 * 2 * 4;
+  l.read0 = l.store0 + r256((size_t)(B + 1) * 8);
+  l.step0 = l.read0 + r256((size_t)(B + 1) * 8);
   l.count = l.step0 + r256((size_t)(B + 1) * 8);
   l.part_sum = l.count + r256((size_t)2 * l.pairs * 4);
-  l.total = l.part_sum + (size_t)2 * l.pairs * 256 * 4;
+  l.store = l.part_sum + (size_t)2 * l.pairs * 256 * 4;
+  const double most = (double)T * H * (double)((keys + 127) / 128 * 128) * 4;  // every row sees all
+  const size_t kept = (size_t)std::min(most, (double)kMostKept);
+  l.all_kept = most <= (double)kMostKept && (int64_t)T * H <= kKeptRows;
+  l.room = (int64_t)(kept / 4);
+  l.total = l.store + kept;
+  return l;
+}
+
+// Workspace of the compaction: the status word, the chunks of 32 rows in front of each sequence with
+// a counter of those handed out, and a flag per chunk.
+struct CompactLayout {
+  size_t chunk0, read, total;
+};
+CompactLayout compact_layout(int B, int K) {
+  CompactLayout l;
+  l.chunk0 = kStatusBytes;
+  l.read = l.chunk0 + r256((size_t)(B + 2) * 8);
+  l.total = l.read + r256((size_t)B * (((size_t)K + 31) / 32) * 4);
   return l;
 }
 
@@ -884,11 +909,11 @@ mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q_pe,
              : MLA_ERR_CUDA;
 }
 
-size_t mla_latent_key_weights_workspace_bytes(int T, int H, int B) {
-  if (T < 1 || H < 1 || H > 1024 || B < 1) return 0;
+size_t mla_latent_key_weights_workspace_bytes(int T, int H, int B, int max_keys) {
+  if (T < 1 || H < 1 || H > 1024 || B < 1 || max_keys < 1) return 0;
   int sms = 0;
   if (check_device(&sms) != MLA_OK || sms <= 0) sms = 152;
-  return key_weights_layout(T, H, B, sms).total;
+  return key_weights_layout(T, H, B, max_keys, sms).total;
 }
 
 mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t* q_pe,
@@ -920,7 +945,7 @@ mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t* q_pe,
   int sms = 0;
   const mla_status st = check_device(&sms);
   if (st != MLA_OK) return st;
-  const KeyWeightsLayout lay = key_weights_layout(T, H, B, sms);
+  const KeyWeightsLayout lay = key_weights_layout(T, H, B, (int64_t)max_pages * page_size, sms);
   if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   KeyWeightsArgs k{};
@@ -940,7 +965,12 @@ mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t* q_pe,
   a.B = B; a.T = T; a.H = H; a.pairs = lay.pairs;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   k.lse = reinterpret_cast<float*>(w + lay.lse);
+  k.steps.store0 = reinterpret_cast<int64_t*>(w + lay.store0);
+  k.steps.read0 = reinterpret_cast<int64_t*>(w + lay.read0);
   k.steps.step0 = reinterpret_cast<int64_t*>(w + lay.step0);
+  k.steps.room = lay.room;
+  k.store = reinterpret_cast<float*>(w + lay.store);
+  k.all_kept = lay.all_kept;
   k.steps.count = reinterpret_cast<int*>(w + lay.count);
   k.part_sum = reinterpret_cast<float*>(w + lay.part_sum);
   k.weights = weights; k.decay = decay;
@@ -994,6 +1024,11 @@ mla_status mla_paged_evict(const float* weights, int num_pages, int page_size,
              : MLA_ERR_CUDA;
 }
 
+size_t mla_latent_compact_workspace_bytes(int B, int K) {
+  if (B < 1 || B > 65535 || K < 1) return 0;
+  return compact_layout(B, K).total;
+}
+
 mla_status mla_latent_compact(uint16_t* c_pages, uint16_t* pe_pages, float* weights, int num_pages,
                               int page_size, const int32_t* block_table, int max_pages,
                               const int32_t* kept, int K, const int32_t* kept_len, int B,
@@ -1009,12 +1044,15 @@ mla_status mla_latent_compact(uint16_t* c_pages, uint16_t* pe_pages, float* weig
   for (const void* w : words)
     if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0) return MLA_ERR_ALIGN;
   if (!aligned16(c_pages) || !aligned16(pe_pages) || !aligned16(workspace)) return MLA_ERR_ALIGN;
-  if (workspace_bytes < kStatusBytes) return MLA_ERR_WORKSPACE;
+  const CompactLayout lay = compact_layout(B, K);
+  if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
   const mla_status st = check_device(nullptr);
   if (st != MLA_OK) return st;
   LatentCompactArgs a{};
   a.c_pages = c_pages; a.pe_pages = pe_pages; a.weights = weights; a.block_table = block_table;
   a.kept = kept; a.kept_len = kept_len; a.status = static_cast<int*>(workspace);
+  a.chunk0 = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(workspace) + lay.chunk0);
+  a.read = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + lay.read);
   a.B = B; a.K = K; a.num_pages = num_pages; a.page_shift = page_shift(page_size);
   a.max_pages = max_pages;
   return launch_latent_compact(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess

@@ -267,6 +267,8 @@ struct LatentCompactArgs {
   const int32_t* block_table;
   const int32_t* kept;
   const int32_t* kept_len;
+  int64_t* chunk0;  // workspace [B + 2]
+  int* read;        // workspace [B * ceil(K / 32)]
   int* status;
   int B, K, num_pages, page_shift, max_pages;
 };
@@ -301,11 +303,17 @@ struct TreeArgs {
   float scale_log2;
 };
 cudaError_t launch_tree_fold(const TreeArgs& a, cudaStream_t stream);  // q_lat, partition
-// The key weights' share of the work (see key_weights.cu): steps in front of each sequence and in
-// all [B+1], and counters of the shared key tiles' segments [2 pairs].
+// The key weights' share of the work (see key_weights.cu).  A sequence's scores are kept from the
+// first pass for the second, from float store0[b] of the store on, where they fit; the others
+// (store0 -1) are computed again.  Key tiles of the former and steps of the latter in front of each
+// sequence and in all [B+1]; counters of the shared key tiles' segments [2 pairs].
+constexpr int kKeptRows = 512;  // of a sequence, at most (see tree_part.cuh)
 struct KeySteps {
+  int64_t* store0;
+  int64_t* read0;
   int64_t* step0;
   int* count;
+  int64_t room;  // floats of the store
 };
 // The folded query in two bf16 parts, q_lat [T,H,1024]; both partitions.
 cudaError_t launch_tree_fold_two(const TreeArgs& a, const KeySteps& steps, cudaStream_t stream);
@@ -318,6 +326,8 @@ struct KeyWeightsArgs {
   KeySteps steps;    // workspace
   float* lse;        // workspace [T,H]: log2 of each row's sum of weights; infinite without keys
   float* part_sum;   // workspace [2 pairs][256]: sums of a key tile's segments
+  float* store;      // workspace [steps.room]
+  bool all_kept;     // the store holds whatever the sequences' lengths are
   float* weights;    // [num_pages, page_size]
   float decay;
 };

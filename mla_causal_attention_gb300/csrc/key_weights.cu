@@ -4,8 +4,10 @@
 //   s_ihj = scale * (q_lat[i,h] . c_j + q_pe[i,h] . k_pe_j)     over the keys j that token i sees,
 //   w_j   = sum_{i,h} exp(s_ihj - L_ih),    L_ih = log sum_j exp(s_ihj)
 // is added to what the key's slot holds.  Each row's L has to be known before the sum over the rows
-// can begin, so the scores are computed twice; kept in memory they would be 4 bytes to write and 4 to
-// read per row and key, which takes as long as 2176 operations on the tensor cores.
+// can begin.  Sequence by sequence the scores are kept for it, as long as a store of up to 256 MB has
+// room (most of it stays in L2), and computed again for the others: written and read again, 8 bytes per
+// row and key take as long as their 2176 operations on the tensor cores, but with few rows it is
+// the keys, 1152 bytes each, that are not read twice.
 //
 // Kernels, each a programmatic dependent launch of the one before:
 //   tree_proj_kernel<fold, two>  the queries folded into the latent space (tree_proj.cu), in two bf16
@@ -14,7 +16,8 @@
 //   row_stats_kernel             each row's maximum and sum, flash style, by the tree attention's
 //                                partition (128 rows against tiles of 128 keys)
 //   row_lse_kernel               L of the rows whose keys several pairs shared
-//   key_sum_kernel               w_j: tiles of 256 keys against tiles of 128 rows
+//   key_read_kernel              w_j from the scores that were kept
+//   key_sum_kernel               w_j of the other sequences: tiles of 256 keys against tiles of 128 rows
 //
 // What bounds it: 2 * 2 * 1088 operations per row and key (the latent columns twice, once for each
 // part), or 2 * 1152 bytes per key where a sequence has few rows.
@@ -112,6 +115,20 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
                  "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+// Eight words w[at ..] to p, in one store if the workspace is 32-byte aligned.
+template <int N>
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[N], int at, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[at]),
+                 "r"(w[at + 1]), "r"(w[at + 2]), "r"(w[at + 3]), "r"(w[at + 4]), "r"(w[at + 5]),
+                 "r"(w[at + 6]), "r"(w[at + 7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[at], w[at + 1], w[at + 2], w[at + 3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[at + 4], w[at + 5], w[at + 6], w[at + 7]);
+  }
+}
+
 // A CTA leaves once neither it nor its peer has anything in flight into its shared memory.  In the
 // regular course every copy and MMA has been waited for by now.  After a wait gave up, copies may
 // still be landing: they take microseconds.
@@ -140,6 +157,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // ---- each row's maximum and sum ---------------------------------------------------------
 namespace stats {
 
+constexpr int kAhead = 2;        // tiles between a tile's L2 prefetch and its loads
 constexpr int kOffQ = 0;                       // 17 sub-tiles: q_lat's two parts, q_pe
 constexpr int kOffK = kOffQ + 17 * kSub64;     // 9 sub-tiles: latent columns, rotary key
 constexpr int kOffRed = kOffK + 9 * kSub64;    // [64 rows] (maximum, sum) of the upper keys
@@ -218,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   bool more = walk.start(a, pair_id, lane, g);
   const int box = min(1 << a.page_shift, 64);  // keys per TMA box
   const int boxes = 64 / box;                  // boxes per 64 keys
+  const int pool = a.num_pages << a.page_shift;
 
   if (warp == 0) {
     // ================= keys and queries =================
@@ -232,6 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                    ? key_row(a, g.b, g.s.kv, tile * kTile + 64 * rank + lane * box) : 0;
       };
       int rows_next = look(g.k0);
+      // Keys that few units read come from HBM, and are asked into L2 two tiles before their loads.
+      const bool ask = g.s.n * a.H <= kKeptRows;
+      int ahead = ask && g.k0 + kAhead < g.k1 ? look(g.k0 + kAhead) : 0;
       if (ns > 0) ok = mbar_wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -274,6 +296,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               }
           }
           __syncwarp();
+        }
+        if (ask && k + kAhead < g.k1) {
+          if (lane < boxes_of(g.s.kv - (k + kAhead) * kTile - 64 * rank, 64, box) && ahead < pool) {
+            bulk_prefetch_l2(a.c_pages + (size_t)ahead * kLD, box * kLD * 2);
+            bulk_prefetch_l2(a.pe_pages + (size_t)ahead * 64, box * 128);
+          }
+          if (k + 1 + kAhead < g.k1) ahead = look(k + 1 + kAhead);
         }
       }
     }
@@ -338,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const float sl2 = a.scale_log2;
     // What a slot holds, for the merge: first row, rows, whether it is its unit's first segment
     // and its last.  One thread clears the pair's two notes and fills in those of its segments.
+    const bool wide = (reinterpret_cast<uintptr_t>(p.a.store) & 31u) == 0;
     const bool notes = rank == 0 && threadIdx.x == 128;
     if (notes) {
       a.part_note[2 * pair_id] = make_int4(0, 0, 0, 0);
@@ -352,6 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int i = row / a.H;                      // new token
       const bool masked = a.draft_mask != nullptr;
       const uint64_t mask = masked && real ? (uint64_t)a.draft_mask[g.s.q0 + i] : 0ull;
+      // Where this thread's scores are kept: [unit][key tile][its rows][128 keys].
+      const int64_t kept = real ? p.a.steps.store0[g.b] : -1;
+      const int unit_rows = min(kRows, g.s.n * a.H - g.m * kRows);
+      float* keep = p.a.store + kept +
+                    ((int64_t)g.m * kRows * seq_tiles(g.s) + row - g.m * kRows) * kTile + 64 * half;
       float m = -INFINITY, l = 0.f;
       for (int k = g.k0; k < g.k1; ++k, ++t) {
         ok = ok && mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, status, abort_flag);
@@ -376,6 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int e = 0; e < 32; ++e)
               if (!((w >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
           }
+        }
+        if (kept >= 0) {
+          float* to = keep + (int64_t)k * unit_rows * kTile;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store32(to + 32 * c + e, x[c], e, wide);
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -459,6 +501,83 @@ __global__ void __launch_bounds__(kRows) row_lse_kernel(const KeyWeightsArgs a) 
 
 }  // namespace stats
 
+// ---- the sum over the rows, of scores that were kept ------------------------------------
+// A block takes tiles of 128 keys; its eight warps share the rows, a lane has four keys.  Bound by
+// reading the scores, 4 bytes per row and key, mostly from L2.
+namespace kept {
+
+constexpr int kReadThreads = 256;
+constexpr int kDeep = 8;  // rows in flight per warp
+
+__global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeightsArgs a) {
+  __shared__ float part[8][kTile];
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  const int64_t tiles = a.steps.read0[a.t.B];
+  const float sl2 = a.t.scale_log2;
+  for (int64_t x = blockIdx.x; x < tiles; x += gridDim.x) {
+    const int b = find_warp(a.steps.read0, a.t.B, x, lane);
+    const TreeSeq s = tree_seq(a.t, b);
+    const int k = (int)(x - a.steps.read0[b]), rows = s.n * a.t.H, K = seq_tiles(s);
+    const int key = k * kTile + (int)threadIdx.x;
+    const bool mine = threadIdx.x < kTile && key < s.kv;
+    const int slot = mine ? key_row(a.t, b, s.kv, key) : 0;
+    const float* lse = a.lse + (size_t)s.q0 * a.t.H;
+    const float* store = a.store + a.steps.store0[b];
+    // Row r is in unit r / 128, whose rows of a tile lie together.
+    const auto at = [&](int r) {
+      const int m = r / kRows, unit_rows = min(kRows, rows - m * kRows);
+      return store + ((int64_t)m * kRows * K + (int64_t)k * unit_rows + (r - m * kRows)) * kTile +
+             4 * lane;
+    };
+    // Sums in two parts (see key_sum_kernel).
+    float total[4] = {}, dropped[4] = {};
+    for (int r0 = warp; r0 < rows; r0 += 8 * kDeep) {
+      float4 v[kDeep];
+      float L[kDeep];
+#pragma unroll
+      for (int e = 0; e < kDeep; ++e) {
+        const int r = r0 + 8 * e;
+        L[e] = INFINITY;
+        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+          v[e] = __ldcs(reinterpret_cast<const float4*>(at(r)));
+          L[e] = lse[r];
+        }
+      }
+      float got[4] = {};
+#pragma unroll
+      for (int e = 0; e < kDeep; ++e) {
+        if (L[e] == INFINITY) continue;  // behind the last row, or a row that sees nothing
+        got[0] += ex2_approx(fmaf(v[e].x, sl2, -L[e]));
+        got[1] += ex2_approx(fmaf(v[e].y, sl2, -L[e]));
+        got[2] += ex2_approx(fmaf(v[e].z, sl2, -L[e]));
+        got[3] += ex2_approx(fmaf(v[e].w, sl2, -L[e]));
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float y = got[c] - dropped[c], sum = total[c] + y;
+        dropped[c] = (sum - total[c]) - y;
+        total[c] = sum;
+      }
+    }
+    *reinterpret_cast<float4*>(&part[warp][4 * lane]) =
+        make_float4(total[0], total[1], total[2], total[3]);
+    __syncthreads();
+    if (mine && slot < a.t.num_pages << a.t.page_shift) {
+      float got = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) got += part[w][threadIdx.x];
+      float* w = a.weights + slot;
+      *w = key < s.ctx && a.decay != 0.f ? fmaf(*w, a.decay, got) : got;
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace kept
+
 // ---- the sum over the rows --------------------------------------------------------------
 namespace sum {
 
@@ -466,8 +585,9 @@ constexpr int kStages = 4;                     // of the rows: a latent sub-tile
 constexpr int kStage = 2 * kSub64;
 constexpr int kOffK = 0;                       // 9 sub-tiles of 128 keys
 constexpr int kOffQ = kOffK + 9 * kSub128;
-constexpr int kOffRow = kOffQ + kStages * kStage;  // [2 step parities][128 rows] {L, token, mask}
-constexpr int kOffBar = kOffRow + 2 * 128 * 16;
+constexpr int kOffRow = kOffQ + kStages * kStage;  // [2 step parities][128 rows] RowNote
+constexpr int kOffKey = kOffRow + 2 * 128 * 16;    // [2 step parities][128 keys] KeyNote
+constexpr int kOffBar = kOffKey + 2 * 128 * 8;
 constexpr int kSmem = kOffBar + 256 + 1024;
 static_assert(kSmem <= 232448, "shared memory per block");
 constexpr uint32_t kTmemCols = 256;            // two score tiles, 128 columns each
@@ -479,17 +599,26 @@ struct Bars {
   uint64_t q_empty[kStages];
   uint64_t s_full[2];   // scores of a step in TMEM
   uint64_t s_free[2];   // even: the scores have been read (8 warps)
+  uint64_t n_full[2];   // a step's notes are written (by warp 3)
+  uint64_t n_free[2];   // they have been read (4 warps)
   uint32_t tmem_base;
   int abort_flag;
   int last;             // this CTA's segment was the last of its key tile's
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-// What a step's rows need besides their scores.
+// What a step's scores are read with, brought by a warp of its own: behind each of them lies a chain
+// of loads, and the warps that sum would wait for it (7 of 20 thousand cycles for a segment of one
+// step).  One per row (those behind the last count as seeing nothing), and one per key: its slot, or
+// -1 where there is nothing to write, and what that goes on from.
 struct RowNote {
   float lse;
   int token;
   uint64_t mask;
+};
+struct KeyNote {
+  int slot;
+  float held;
 };
 
 // Row tiles [r0, r1) of sequence b against its keys 256 k ..
@@ -559,6 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int rank = (int)tp::cta_rank();
   const int pair_id = blockIdx.x >> 1;
   int* status = a.status;
+  grid_dep_wait();  // the rows' sums, and with them the partition and the folded queries
+  if (p.a.steps.step0[a.B] == 0) return;  // everything was kept
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 3; ++i) {
@@ -572,6 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_free[i], 8);
+      mbar_init(&bars->n_full[i], 1);
+      mbar_init(&bars->n_free[i], 4);
     }
     bars->abort_flag = 0;
     fence_barrier_init();
@@ -593,25 +726,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   tp::cluster_sync();  // both CTAs' barriers are ready before either signals the other's
   tc::fence_after_sync();
   const uint32_t tbase = bars->tmem_base;
-  grid_dep_wait();  // the rows' sums, and with them the partition and the folded queries
+  // Every role looks its next segment up while it works on one: that takes a chain of loads.
   KeyWalk walk;
   walk.start(p.a, pair_id, lane);
-  KeySeg g;
+  KeySeg g, after;
+  bool more = walk.next(p.a, g);
 
   if (warp == 0) {
     // ================= keys =================
     const uint32_t k_full = tp::even_addr(&bars->k_full[0]);
     const int box = min(1 << a.page_shift, 64);  // keys per TMA box
     const int boxes = 128 / box;                 // boxes of this CTA's keys, at most 8
+    const int pool = a.num_pages << a.page_shift;
+    const auto look = [&](const KeySeg& s) {  // lane q: the row of box q of this CTA's keys
+      return lane < boxes
+                 ? key_row(a, s.b, s.s.kv, s.k * kKeyTile + 128 * rank + lane * box) : 0;
+    };
     int ns = 0;
     bool ok = true;
-    for (; ok && walk.next(p.a, g); ++ns) {
-      const int key0 = g.k * kKeyTile + 128 * rank;
-      const int mine = lane < boxes ? key_row(a, g.b, g.s.kv, key0 + lane * box) : 0;
-      const int nb = boxes_of(g.s.kv - key0, 128, box);
+    int next = more ? look(g) : 0;
+    for (; ok && more; ++ns, g = after) {
+      const int nb = boxes_of(g.s.kv - (g.k * kKeyTile + 128 * rank), 128, box);
       int row[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) row[q] = __shfl_sync(0xffffffffu, mine, q);
+      for (int q = 0; q < 8; ++q) row[q] = __shfl_sync(0xffffffffu, next, q);
+      more = walk.next(p.a, after);
+      if (more) next = look(after);
 #pragma unroll 1
       for (int grp = 0; grp < 3; ++grp) {
         if (ns > 0) ok = mbar_wait(&bars->k_empty[grp], (ns - 1) & 1, status, abort_flag);
@@ -640,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t q_full = tp::even_addr(&bars->q_full[0]);
     uint32_t u = 0;  // stages over the run
     bool ok = true;
-    while (ok && walk.next(p.a, g)) {
+    for (; ok && more; g = after) {
+      bool then = false;
       for (int r = g.r0; r < g.r1 && ok; ++r) {
         const int half = columns(g, r) / 2;  // rows of this CTA
         const CUtensorMap* tq = half == 64 ? &p.tm_q64 : &p.tm_q32;
@@ -664,8 +805,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
           }
           __syncwarp();
+          if (r == g.r0 && c == 0) then = walk.next(p.a, after);
         }
       }
+      more = then;
     }
   } else if (warp == 1 && rank == 0) {
     // ================= MMAs =================
@@ -674,14 +817,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t t = 0, u = 0;  // steps, stages over the run
     int ns = 0;
     bool ok = true;
-    for (; ok && walk.next(p.a, g); ++ns) {
+    for (; ok && more; ++ns, g = after) {
+      bool then = false;
       for (int r = g.r0; r < g.r1 && ok; ++r, ++t) {
         // The scores to be overwritten, those of step t - 2, have been read.
         if (t > 1) ok = mbar_wait(&bars->s_free[t & 1], ((t >> 1) - 1) & 1, status, abort_flag);
         const uint32_t d = tbase + (t & 1) * 128;
         const uint32_t idesc = columns(g, r) == 128 ? tc::idesc_bf16_f32(256, 128, false)
                                                     : tc::idesc_bf16_f32(256, 64, false);
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 9; ++c, ++u) {
           const uint32_t st = u % kStages;
           if (r == g.r0 && c % 3 == 0)
@@ -705,7 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           }
           __syncwarp();
         }
+        if (r == g.r0) then = walk.next(p.a, after);
       }
+      more = then;
     }
     // The releases that no one has waited for have arrived before this CTA leaves.
     if (ok && ns > 0) {
@@ -714,42 +860,74 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (uint32_t k = u - kStages; k < u; ++k)
         mbar_wait(&bars->q_empty[k % kStages], (k / kStages) & 1, status, abort_flag);
     }
+  } else if (warp == 3) {
+    // ================= notes =================
+    const bool masked = a.draft_mask != nullptr;
+    uint32_t t = 0;
+    bool ok = true;
+    for (; ok && more; more = walk.next(p.a, g)) {
+      for (int r = g.r0; r < g.r1 && ok; ++r, ++t) {
+        RowNote row[4];
+        KeyNote key[4];
+        const bool last = r + 1 == g.r1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = r * kRows + 32 * k + lane;
+          row[k] = {INFINITY, 0, 0ull};
+          if (at < g.rows) {
+            row[k].lse = p.a.lse[(size_t)g.s.q0 * a.H + at];
+            row[k].token = at / a.H;
+            if (masked) row[k].mask = (uint64_t)a.draft_mask[g.s.q0 + row[k].token];
+          }
+          if (last) {
+            const int j = g.k * kKeyTile + 128 * rank + 32 * k + lane;
+            const int slot = j < g.s.kv ? key_row(a, g.b, g.s.kv, j) : -1;
+            key[k].slot = slot < a.num_pages << a.page_shift ? slot : -1;
+            key[k].held = 0.f;
+            if (key[k].slot >= 0 && j < g.s.ctx && p.a.decay != 0.f)
+              key[k].held = p.a.weights[key[k].slot];
+          }
+        }
+        if (t > 1) ok = mbar_wait(&bars->n_free[t & 1], ((t >> 1) - 1) & 1, status, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        RowNote* rows = reinterpret_cast<RowNote*>(smem + kOffRow) + (t & 1) * 128;
+        KeyNote* keys = reinterpret_cast<KeyNote*>(smem + kOffKey) + (t & 1) * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          rows[32 * k + lane] = row[k];
+          if (last) keys[32 * k + lane] = key[k];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->n_full[t & 1]);
+      }
+    }
   } else if (warp >= 4) {
     // ================= weights and their sums =================
     const int q4 = warp & 3, tid = threadIdx.x - 128;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    RowNote* notes = reinterpret_cast<RowNote*>(smem + kOffRow);
     const uint32_t s_free = tp::even_addr(&bars->s_free[0]);
     const float sl2 = a.scale_log2;
     const bool masked = a.draft_mask != nullptr;
     uint32_t t = 0;
     bool ok = true;
-    while (walk.next(p.a, g)) {
-      const int key = g.k * kKeyTile + 128 * rank + tid;
-      const int off = key - g.s.ctx;  // index among the new tokens, negative for a cached key
+    for (; more; g = after) {
+      const int off = g.k * kKeyTile + 128 * rank + tid - g.s.ctx;  // index among the new tokens, or < 0
+      const bool all_see = __all_sync(0xffffffffu, off < 0);
       // Sums in two parts, the running total and what its roundings have dropped: a key's sum goes
       // over up to millions of rows.
       float total = 0.f, dropped = 0.f;
-      bool gone = false;
-      for (int r = g.r0; r < g.r1; ++r, ++t) {
-        // Each thread brings one of the tile's rows; those behind the last count as seeing nothing.
-        RowNote* note = notes + (t & 1) * 128;
-        {
-          const int row = r * kRows + tid;
-          RowNote mine = {INFINITY, 0, 0ull};
-          if (row < g.rows) {
-            mine.lse = p.a.lse[(size_t)g.s.q0 * a.H + row];
-            mine.token = row / a.H;
-            if (masked) mine.mask = (uint64_t)a.draft_mask[g.s.q0 + mine.token];
-          }
-          note[tid] = mine;
-        }
+      KeyNote key = {};
+      bool then = false;
+      for (int r = g.r0; r < g.r1 && ok; ++r, ++t) {
+        if (r == g.r0) then = walk.next(p.a, after);
+        ok = ok && mbar_wait(&bars->n_full[t & 1], (t >> 1) & 1, status, abort_flag);
         ok = ok && mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, status, abort_flag);
-        gone = !readers_and(ok);
-        if (gone) break;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc::fence_after_sync();
+        const RowNote* note = reinterpret_cast<const RowNote*>(smem + kOffRow) + (t & 1) * 128;
         const int cols = columns(g, r);
-        const bool all_see = __all_sync(0xffffffffu, off < 0);
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {
@@ -762,26 +940,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (lane == 0) tp::arrive(s_free + 8 * (t & 1));
           }
+          if (all_see) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float lse = note[c + e].lse;
-            bool sees = lse != INFINITY;
-            if (!all_see && off >= 0) {
-              if (masked)
-                sees = sees && off < 64 && ((note[c + e].mask >> off) & 1ull);
-              else
-                sees = sees && off <= note[c + e].token;
+            for (int e = 0; e < 32; ++e) {
+              const float lse = note[c + e].lse;
+              const float w = ex2_approx(fmaf(__uint_as_float(x[e]), sl2, -lse));
+              part[e & 3] += lse != INFINITY ? w : 0.f;
             }
-            const float w = ex2_approx(fmaf(__uint_as_float(x[e]), sl2, -lse));
-            part[e & 3] += sees ? w : 0.f;
+          } else {
+#pragma unroll 8
+            for (int e = 0; e < 32; ++e) {
+              const RowNote row = note[c + e];
+              bool sees = row.lse != INFINITY;
+              if (off >= 0)
+                sees = sees && (masked ? off < 64 && ((row.mask >> off) & 1ull) : off <= row.token);
+              const float w = ex2_approx(fmaf(__uint_as_float(x[e]), sl2, -row.lse));
+              part[e & 3] += sees ? w : 0.f;
+            }
           }
         }
+        if (r + 1 == g.r1) key = (reinterpret_cast<const KeyNote*>(smem + kOffKey) + (t & 1) * 128)[tid];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->n_free[t & 1]);
         const float y = (part[0] + part[1]) + (part[2] + part[3]) - dropped;
         const float sum = total + y;
         dropped = (sum - total) - y;
         total = sum;
       }
-      if (gone) break;
       float got = total;
       bool mine = true;
       if (g.r1 - g.r0 < g.tiles) {
@@ -794,10 +979,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int at = rank * 128 + tid;
         p.a.part_sum[(size_t)(pair_id == c0 ? slot0 : 2 * pair_id) * kKeyTile + at] = total;
         __threadfence();
-        readers_and(true);
-        if (tid == 0) bars->last = atomicAdd(p.a.steps.count + 2 * c0 + rank, 1) == c1 - c0;
-        readers_and(true);
-        mine = bars->last != 0;
+        ok = readers_and(ok);
+        if (ok && tid == 0) bars->last = atomicAdd(p.a.steps.count + 2 * c0 + rank, 1) == c1 - c0;
+        ok = readers_and(ok);
+        mine = ok && bars->last != 0;
         if (mine) {
           __threadfence();
           got = 0.f;
@@ -805,13 +990,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             got += __ldcg(p.a.part_sum + (size_t)(c == c0 ? slot0 : 2 * c) * kKeyTile + at);
         }
       }
-      if (mine && key < g.s.kv) {
-        const int slot = key_row(a, g.b, g.s.kv, key);
-        if (slot < a.num_pages << a.page_shift) {
-          float* w = p.a.weights + slot;
-          *w = off < 0 && p.a.decay != 0.f ? fmaf(*w, p.a.decay, got) : got;
-        }
-      }
+      if (!ok) break;
+      if (mine && key.slot >= 0) p.a.weights[key.slot] = fmaf(key.held, p.a.decay, got);
+      more = then;
     }
   }
   leave(abort_flag, warp, tbase, kTmemCols);
@@ -903,11 +1084,14 @@ cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, stats::row_lse_kernel, a);
   if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(2 * a.t.pairs * 6);
+  cfg.blockDim = dim3(kept::kReadThreads);
+  e = cudaLaunchKernelEx(&cfg, kept::key_read_kernel, a);
+  if (e != cudaSuccess || a.all_kept) return e;
+  cfg.gridDim = dim3(2 * a.t.pairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sum::kSmem;
-  e = cudaLaunchKernelEx(&cfg, sum::key_sum_kernel, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, sum::key_sum_kernel, p);
 }
 
 }  // namespace mla

@@ -282,35 +282,64 @@ __device__ __forceinline__ int row_tiles(const TreeArgs& a, const TreeSeq& s) {
   return (s.n * a.H + kRows - 1) / kRows;
 }
 
-// By one block of 256 threads: the steps in front of each sequence; the counters cleared.
+// Floats that a sequence's scores take if they are kept: rows x whole tiles of 128 keys.  Those of many
+// rows are computed again.  Kept and computed again, us: 64 sequences of 4000 keys and 64 rows 100,
+// 135; 128 rows 126, 149; 256 rows 213, 239; 16 of 512 rows 116, 128; 4 of 1024 rows 73, 74; one of
+// 4096 rows 119, 73.
+__device__ __forceinline__ int64_t store_size(const TreeArgs& a, const TreeSeq& s) {
+  const int64_t rows = (int64_t)s.n * a.H;
+  return rows <= kKeptRows ? rows * seq_tiles(s) * kTile : 0;
+}
+
+// By one block of 256 threads: which sequences' scores are kept, in order as long as there is room;
+// the tiles and steps in front of each sequence; the counters cleared.
 static __device__ __noinline__ void key_steps(const TreeArgs& a, const KeySteps& k) {
-  __shared__ int64_t s_w[8];
+  __shared__ int64_t s_sum[3][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < 2 * a.pairs; i += 256) k.count[i] = 0;
-  int64_t W = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 256) {
-    int64_t w = 0;
-    if (b0 + tid < a.B) {
-      const TreeSeq s = tree_seq(a, b0 + tid);
-      w = (int64_t)key_tiles(s) * row_tiles(a, s);
-    }
-    int64_t inc = w;
+  // The sum of x over the threads before this one; all is the block's.
+  const auto scan = [&](int64_t x, int which, int64_t& all) {
+    int64_t inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    if (lane == 31) s_w[warp] = inc;
+    if (lane == 31) s_sum[which][warp] = inc;
     __syncthreads();
-    int64_t before = W;
+    all = 0;
     for (int i = 0; i < 8; ++i) {
-      if (i < warp) before += s_w[i];
-      W += s_w[i];
+      if (i < warp) inc += s_sum[which][i];
+      all += s_sum[which][i];
     }
-    if (b0 + tid < a.B) k.step0[b0 + tid] = before + inc - w;
+    return inc - x;
+  };
+  int64_t size = 0, tiles = 0, steps = 0;  // of the sequences before
+  for (int b0 = 0; b0 < a.B; b0 += 256) {
+    const int b = b0 + tid;
+    TreeSeq s = {};
+    if (b < a.B) s = tree_seq(a, b);
+    int64_t all;
+    const int64_t own = store_size(a, s), from = size + scan(own, 0, all);
+    size += all;
+    const bool keep = own > 0 && from + own <= k.room;
+    const int64_t t = keep ? seq_tiles(s) : 0;
+    const int64_t w = keep ? 0 : (int64_t)key_tiles(s) * row_tiles(a, s);
+    const int64_t t0 = tiles + scan(t, 1, all);
+    tiles += all;
+    const int64_t w0 = steps + scan(w, 2, all);
+    steps += all;
+    if (b < a.B) {
+      k.store0[b] = keep ? from : -1;
+      k.read0[b] = t0;
+      k.step0[b] = w0;
+    }
     __syncthreads();
   }
-  if (tid == 0) k.step0[a.B] = W;
+  if (tid == 0) {
+    k.read0[a.B] = tiles;
+    k.step0[a.B] = steps;
+  }
 }
 
 // Zeroes the mixes of sequences that have new tokens and no keys: no unit writes them, and the folded

@@ -131,7 +131,7 @@ COMPACT = ["c_pages", "pe_pages", "weights", "num_pages", "page_size", "block_ta
 
 def _compact_args(base):
     a = {n: base + 1024 * i for i, n in enumerate(COMPACT)}
-    a.update(num_pages=8, page_size=16, max_pages=4, B=2, K=9, workspace_bytes=256, stream=None)
+    a.update(num_pages=8, page_size=16, max_pages=4, B=2, K=9, workspace_bytes=768, stream=None)
     return a
 
 
@@ -139,7 +139,7 @@ def _compact_args(base):
     ({"c_pages": None}, S.ERR_NULL), ({"pe_pages": None}, S.ERR_NULL),
     ({"block_table": None}, S.ERR_NULL), ({"kept": None}, S.ERR_NULL),
     ({"kept_len": None}, S.ERR_NULL), ({"workspace": None}, S.ERR_WORKSPACE),
-    ({"workspace_bytes": 8}, S.ERR_WORKSPACE), ({"B": 0}, S.ERR_SHAPE), ({"B": 65536}, S.ERR_SHAPE),
+    ({"workspace_bytes": 767}, S.ERR_WORKSPACE), ({"B": 0}, S.ERR_SHAPE), ({"B": 65536}, S.ERR_SHAPE),
     ({"K": 0}, S.ERR_SHAPE), ({"max_pages": 0}, S.ERR_SHAPE), ({"page_size": 15}, S.ERR_SHAPE),
     ({"num_pages": 1 << 28}, S.ERR_SHAPE),
 ])
@@ -157,6 +157,8 @@ def test_compact_refuses_alignment(lib, base):
     if not torch.cuda.is_available():
         a = _compact_args(base)
         a["weights"] = None
+        assert lib.mla_latent_compact_workspace_bytes(2, 9) == 768
+        assert lib.mla_latent_compact_workspace_bytes(0, 9) == 0
         assert _accepted(lib.mla_latent_compact(*[a[n] for n in COMPACT]))
 
 
@@ -168,7 +170,7 @@ WEIGHTS = ["q_nope", "q_pe", "c_pages", "pe_pages", "num_pages", "page_size", "b
 def _weights_args(lib, base):
     a = {n: base + 1024 * i for i, n in enumerate(WEIGHTS)}
     a.update(num_pages=8, page_size=16, max_pages=4, B=2, T=3, H=4, scale=0.1, decay=1.0,
-             workspace_bytes=lib.mla_latent_key_weights_workspace_bytes(3, 4, 2), stream=None)
+             workspace_bytes=lib.mla_latent_key_weights_workspace_bytes(3, 4, 2, 64), stream=None)
     return a
 
 
@@ -195,8 +197,11 @@ def test_weights_refuse_alignment_and_small_workspaces(lib, base):
         a[name] += off
         assert lib.mla_latent_key_weights(*[a[n] for n in WEIGHTS]) == S.ERR_ALIGN, name
     size = lib.mla_latent_key_weights_workspace_bytes
-    assert size(0, 4, 2) == size(3, 0, 2) == size(3, 1025, 2) == size(3, 4, 0) == 0
-    assert size(3, 4, 2) > 3 * 4 * (2048 + 4)
+    assert size(0, 4, 2, 64) == size(3, 0, 2, 64) == size(3, 1025, 2, 64) == size(3, 4, 0, 64) == 0
+    assert size(3, 4, 2, 0) == 0
+    assert size(3, 4, 2, 64) > 3 * 4 * (2048 + 4 + 128 * 4)
+    # scores are kept up to 256 MB
+    assert size(64, 64, 2, 1 << 30) - size(64, 64, 2, 128) == (1 << 28) - 64 * 64 * 512
     a = _weights_args(lib, base)
     if not torch.cuda.is_available():
         assert _accepted(lib.mla_latent_key_weights(*[a[n] for n in WEIGHTS]))
