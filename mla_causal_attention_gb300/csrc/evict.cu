@@ -29,37 +29,50 @@ __device__ __forceinline__ void cluster_barrier() {
       "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
-// A word of CTA `rank`'s shared memory, at the place of this CTA's p.
-__device__ __forceinline__ int peer_load(const int* p, uint32_t rank) {
+// One or two words of CTA `rank`'s shared memory, at the place of this CTA's p.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   uint32_t at;
-  int v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return at;
+}
+__device__ __forceinline__ int2 peer_load2(const int* p, uint32_t rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(peer_addr(p, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ int peer_load(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(peer_addr(p, rank)) : "memory");
   return v;
 }
 
 // ---- choice -----------------------------------------------------------------------------
 // Sequence b of len rows keeps k = min(len, budget): its first s = min(sinks, k), its last
 // r = min(recent, k - s), and the m = k - s - r heaviest of those between, of equal ones the lower
-// rows.  The m-th heaviest is found by its digits, 11, 11 and 10 bits of a whole number that orders
+// rows.  The m-th heaviest is found by its digits, four of 8 bits of a whole number that orders
 // as the weights do: a histogram of the digit over the rows that agree with the digits found so
 // far, and the bin in which the m-th lies.  Then the rows above it, and as many of those equal to
 // it as are missing, are listed by a prefix sum over ballots.
 //
-// A cluster of CTAs per sequence, each with an equal run of the rows between, whose numbers it
-// keeps in shared memory for the passes; the histograms are added up through distributed shared
-// memory.  The work is 4 bytes per row: what bounds it is latency, of the loads through the block
-// table and of the barriers between the passes.
-constexpr int kEvThreads = 1024;
+// A cluster of CTAs per sequence, each with an equal run of the rows between and each warp with an
+// equal run of those; the histograms are added up through distributed shared memory.  The numbers
+// stay in registers for all passes, or, with more than 8 to a thread, in shared memory.  The work is 4
+// bytes per row: what bounds it is latency, of the loads through the block table and of the barriers
+// between the passes.
+constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kEvPer = 8;        // rows of a thread at a time
+constexpr int kPasses = 4, kBins = 256;  // (three of 2048: every CTA reads all histograms, 10 us a pass)
 
 struct EvictSmem {
-  int hist[3][kBins];
-  int part[kEvWarps];             // of a block-wide scan
+  int hist[kPasses][kBins];
+  int part[kPasses + 1][kEvWarps];  // of block-wide scans
   int above[kEvWarps], ties[kEvWarps];  // rows of each warp's run
-  int cta[2];                     // rows above, ties of this CTA
-  int bin, left;                  // the bin found, and the rank that is left within it
+  alignas(8) int cta[2];          // rows above, ties of this CTA
+  int bin[kPasses], left[kPasses];  // the bin found, and the rank that is left within it
 };
 
 struct EvictSeq {
@@ -90,7 +103,9 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sum over the block's threads; *total is the sum.  Two barriers.
+// Exclusive prefix sum over the block's threads; *total is the sum.  One barrier; `part` is not to be
+// used again before another.
+template <int kWarps>
 __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = v;
@@ -101,19 +116,12 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
   }
   if (lane == 31) part[warp] = inc;
   __syncthreads();
-  int p = part[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, p, o);
-    if (lane >= o) p += x;
-  }
-  *total = __shfl_sync(0xffffffffu, p, 31);
-  const int before = __shfl_sync(0xffffffffu, p, (warp + 31) & 31);
-  __syncthreads();
-  return inc - v + (warp ? before : 0);
+  const int p = lane < kWarps ? part[lane] : 0;
+  *total = __reduce_add_sync(0xffffffffu, p);
+  return inc - v + __reduce_add_sync(0xffffffffu, lane < warp ? p : 0);
 }
 
-__global__ void __launch_bounds__(kEvThreads) paged_evict_kernel(const PagedEvictArgs a) {
+__global__ void __launch_bounds__(kEvThreads, 2) paged_evict_kernel(const PagedEvictArgs a) {
   extern __shared__ uint32_t keys[];  // this CTA's numbers, the first a.held of them
   __shared__ EvictSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -123,7 +131,160 @@ __global__ void __launch_bounds__(kEvThreads) paged_evict_kernel(const PagedEvic
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
   int32_t* kept = a.kept + (int64_t)b * a.K;
   const int share = rank * kEvThreads + tid, shares = C * kEvThreads;
-  if (q.bad && share == 0) set_status(a.status, MLA_ERR_KVLEN);
+  // Pages past the kept rows, behind those of the sequences before: the last CTA lists them.  What it
+  // loads for that is on its way together with the weights.
+  const bool lists = a.freed && rank == C - 1;
+  const int gone0 = pages_for(a, q.k), gone = pages_for(a, q.len) - gone0;
+  int before = 0, page0 = 0;
+  if (lists) {
+    for (int i = tid; i < b; i += kEvThreads) {
+      const EvictSeq o = evict_seq(a, i);
+      before += pages_for(a, o.len) - pages_for(a, o.k);
+    }
+    if (tid < gone) page0 = table[gone0 + tid];
+  }
+
+  if (q.m > 0) {
+    // This CTA's run of the rows between the ends, and this warp's of those.
+    const int mid = q.len - q.s - q.r;  // > m
+    const int per = (mid + C - 1) / C;
+    const int i0 = min(rank * per, mid), n = min(per, mid - i0);
+    const int run = (((n + kEvWarps - 1) / kEvWarps) + 31) & ~31;
+    const int w0 = min(warp * run, n), w1 = min(w0 + run, n);
+    const int rounds = (run + 32 * kEvPer - 1) / (32 * kEvPer);
+    bool bad = false;
+    // Rows w0 + lane + 32 (kEvPer round + e) of this thread, from the pool: the loads of a round at once.
+    uint32_t v[kEvPer];
+    const auto weigh = [&](int round) {
+      const int first = w0 + 32 * kEvPer * round + lane;
+      int page[kEvPer];
+#pragma unroll
+      for (int e = 0; e < kEvPer; ++e)
+        page[e] = first + 32 * e < w1 ? table[(q.s + i0 + first + 32 * e) >> a.page_shift] : 0;
+#pragma unroll
+      for (int e = 0; e < kEvPer; ++e) {
+        const int row = q.s + i0 + first + 32 * e;
+        const bool held = page[e] >= 0 && page[e] < a.num_pages;
+        float w = __uint_as_float(0x7fc00000u);  // counts as lowest
+        if (first + 32 * e < w1 && held)
+          w = a.weights[((int64_t)page[e] << a.page_shift) + (row & ((1 << a.page_shift) - 1))];
+        v[e] = __float_as_uint(w);
+        bad |= !held;
+      }
+#pragma unroll
+      for (int e = 0; e < kEvPer; ++e) v[e] = order_of(__uint_as_float(v[e]));
+    };
+    const auto fetch = [&](int round) {
+      if (rounds == 1) return;  // they are in the registers
+      const int first = w0 + 32 * kEvPer * round + lane;
+      if (w1 > a.held) return weigh(round);
+#pragma unroll
+      for (int e = 0; e < kEvPer; ++e) v[e] = first + 32 * e < w1 ? keys[first + 32 * e] : 0u;
+    };
+    weigh(0);
+    for (int i = tid; i < kPasses * kBins; i += kEvThreads) (&sm.hist[0][0])[i] = 0;
+    if (rounds > 1 && w1 <= a.held)
+      for (int r = 0; r < rounds; ++r) {
+        const int first = w0 + 32 * kEvPer * r + lane;
+        if (r > 0) weigh(r);
+#pragma unroll
+        for (int e = 0; e < kEvPer; ++e)
+          if (first + 32 * e < w1) keys[first + 32 * e] = v[e];
+      }
+    __syncthreads();
+
+    uint32_t found = 0;  // the digits of the m-th heaviest so far, from the top
+    int left = q.m;      // its rank among the rows that agree with them
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int shift = 24 - 8 * pass;
+      const uint32_t agree = pass == 0 ? 0u : ~0u << (shift + 8);
+      for (int r = 0; r < rounds; ++r) {
+        fetch(r);
+        const int first = w0 + 32 * kEvPer * r + lane;
+#pragma unroll
+        for (int e = 0; e < kEvPer; ++e)
+          if (first + 32 * e < w1 && (v[e] & agree) == found)
+            atomicAdd(&sm.hist[pass][(v[e] >> shift) & 255], 1);
+      }
+      cluster_barrier();
+      // Thread t < 256 adds up bin 255 - t, so that a prefix sum counts from the top.
+      const int bin = kBins - 1 - tid;
+      int at = 0;
+      if (tid < kBins) {
+        for (int c0 = 0; c0 < C; c0 += 8) {
+          int x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = peer_load(&sm.hist[pass][bin], min(c0 + e, C - 1));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) at += c0 + e < C ? x[e] : 0;
+        }
+      }
+      int total;
+      const int above = block_scan<kEvWarps>(at, sm.part[pass], &total);
+      if (above < left && left <= above + at) {
+        sm.bin[pass] = bin;
+        sm.left[pass] = left - above;
+      }
+      __syncthreads();
+      found |= (uint32_t)sm.bin[pass] << shift;
+      left = sm.left[pass];
+    }
+
+    // `left` of the rows equal to `found` are kept, the lowest ones.
+    int above = 0, ties = 0;
+    for (int r = 0; r < rounds; ++r) {
+      fetch(r);
+#pragma unroll
+      for (int e = 0; e < kEvPer; ++e) {
+        const bool real = w0 + 32 * (kEvPer * r + e) + lane < w1;
+        above += real && v[e] > found;
+        ties += real && v[e] == found;
+      }
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    if (lane == 0) {
+      sm.above[warp] = above;
+      sm.ties[warp] = ties;
+    }
+    __syncthreads();
+    above = lane < kEvWarps ? sm.above[lane] : 0;
+    ties = lane < kEvWarps ? sm.ties[lane] : 0;
+    if (warp == 0) {
+      const int x = __reduce_add_sync(0xffffffffu, above), y = __reduce_add_sync(0xffffffffu, ties);
+      if (lane == 0) {
+        sm.cta[0] = x;
+        sm.cta[1] = y;
+      }
+    }
+    cluster_barrier();
+    if (lane >= warp) above = ties = 0;
+    if (lane < rank) {  // at most 16 CTAs
+      const int2 o = peer_load2(sm.cta, lane);
+      above += o.x;
+      ties += o.y;
+    }
+    above = __reduce_add_sync(0xffffffffu, above);  // before this warp's run
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    const uint32_t below = (1u << lane) - 1;
+    for (int r = 0; r < rounds; ++r) {
+      fetch(r);
+#pragma unroll
+      for (int e = 0; e < kEvPer; ++e) {
+        const int row = w0 + 32 * (kEvPer * r + e) + lane;
+        const bool up = row < w1 && v[e] > found, tie = row < w1 && v[e] == found;
+        const uint32_t ups = __ballot_sync(0xffffffffu, up), eqs = __ballot_sync(0xffffffffu, tie);
+        const int my_ties = ties + __popc(eqs & below);
+        const int at = q.s + above + __popc(ups & below) + min(my_ties, left);
+        // (the bound holds unless someone writes the weights meanwhile)
+        if ((up || (tie && my_ties < left)) && at < q.k - q.r) kept[at] = q.s + i0 + row;
+        above += __popc(ups);
+        ties += __popc(eqs);
+      }
+    }
+    if (bad) set_status(a.status, MLA_ERR_PAGE);
+  }
 
   // What needs no choice: the ends, or everything; the rest of the row.
   const int head = q.k < q.len ? q.s : q.k;
@@ -131,119 +292,21 @@ __global__ void __launch_bounds__(kEvThreads) paged_evict_kernel(const PagedEvic
   for (int i = share; i < a.K - q.k; i += shares) kept[q.k + i] = -1;
   if (q.k < q.len)
     for (int i = share; i < q.r; i += shares) kept[q.k - q.r + i] = q.len - q.r + i;
-  if (share == 0) a.kept_len[b] = q.k;
-
-  // Pages past the kept rows, behind those of the sequences before.
-  if (a.freed && rank == C - 1) {
-    int before = 0, own_total;
-    for (int i = tid; i < b; i += kEvThreads) {
-      const EvictSeq o = evict_seq(a, i);
-      before += pages_for(a, o.len) - pages_for(a, o.k);
-    }
-    block_scan(before, sm.part, &own_total);
-    const int from = pages_for(a, q.k), n = pages_for(a, q.len) - from;
-    for (int i = tid; i < n; i += kEvThreads) {
-      const int page = table[from + i];
+  if (share == 0) {
+    a.kept_len[b] = q.k;
+    if (q.bad) set_status(a.status, MLA_ERR_KVLEN);
+  }
+  if (lists) {
+    int at;
+    block_scan<kEvWarps>(before, sm.part[kPasses], &at);
+    for (int i = tid; i < gone; i += kEvThreads) {
+      const int page = i == tid ? page0 : table[gone0 + i];
       if (page < 0 || page >= a.num_pages) set_status(a.status, MLA_ERR_PAGE);
-      a.freed[own_total + i] = page;
+      a.freed[at + i] = page;
     }
-    if (b == a.B - 1 && tid == 0) a.n_freed[0] = own_total + n;
+    if (b == a.B - 1 && tid == 0) a.n_freed[0] = at + gone;
   }
-  if (q.m == 0) return;  // the whole cluster: nothing to choose
-
-  // This CTA's run of the rows between the ends.
-  const int mid = q.len - q.s - q.r;  // > m
-  const int per = (mid + C - 1) / C;
-  const int i0 = min(rank * per, mid), n = min(per, mid - i0);
-  const auto weigh = [&](int i) {
-    const int row = q.s + i0 + i;
-    const int page = table[row >> a.page_shift];
-    if (page < 0 || page >= a.num_pages) {
-      set_status(a.status, MLA_ERR_PAGE);
-      return 0u;
-    }
-    return order_of(a.weights[((int64_t)page << a.page_shift) + (row & ((1 << a.page_shift) - 1))]);
-  };
-  const auto number = [&](int i) { return i < a.held ? keys[i] : weigh(i); };
-  for (int i = tid; i < 3 * kBins; i += kEvThreads) (&sm.hist[0][0])[i] = 0;
-  for (int i = tid; i < min(n, a.held); i += kEvThreads) keys[i] = weigh(i);
-  __syncthreads();
-
-  uint32_t found = 0;  // the digits of the m-th heaviest so far, from the top
-  int left = q.m;      // its rank among the rows that agree with them
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    const uint32_t agree = pass == 0 ? 0u : ~0u << (shift + bits);
-    for (int i = tid; i < n; i += kEvThreads) {
-      const uint32_t v = number(i);
-      if ((v & agree) == found) atomicAdd(&sm.hist[pass][(v >> shift) & ((1 << bits) - 1)], 1);
-    }
-    cluster_barrier();
-    // Thread t adds up bins 2047 - 2 t and 2046 - 2 t, so that a prefix sum counts from the top.
-    const int hi = kBins - 1 - 2 * tid, lo = hi - 1;
-    int at_hi = 0, at_lo = 0;
-    for (int c = 0; c < C; ++c) {
-      at_hi += peer_load(&sm.hist[pass][hi], c);
-      at_lo += peer_load(&sm.hist[pass][lo], c);
-    }
-    int total;
-    const int above = block_scan(at_hi + at_lo, sm.part, &total);
-    if (above < left && left <= above + at_hi + at_lo) {
-      const bool first = left <= above + at_hi;
-      sm.bin = first ? hi : lo;
-      sm.left = left - above - (first ? 0 : at_hi);
-    }
-    __syncthreads();
-    found |= (uint32_t)sm.bin << shift;
-    left = sm.left;
-    __syncthreads();
-  }
-
-  // `left` of the rows equal to `found` are kept, the lowest ones.  Warps have runs of rows.
-  const int run = ((n + kEvWarps - 1) / kEvWarps + 31) & ~31;
-  const int w0 = min(warp * run, n), w1 = min(w0 + run, n);
-  int above = 0, ties = 0;
-  for (int i = w0 + lane; i < w0 + ((w1 - w0 + 31) & ~31); i += 32) {
-    const uint32_t v = i < w1 ? number(i) : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i < w1 && v > found));
-    ties += __popc(__ballot_sync(0xffffffffu, i < w1 && v == found));
-  }
-  if (lane == 0) {
-    sm.above[warp] = above;
-    sm.ties[warp] = ties;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const int x = __reduce_add_sync(0xffffffffu, sm.above[lane]);
-    const int y = __reduce_add_sync(0xffffffffu, sm.ties[lane]);
-    if (lane == 0) {
-      sm.cta[0] = x;
-      sm.cta[1] = y;
-    }
-  }
-  cluster_barrier();
-  above = lane < warp ? sm.above[lane] : 0;
-  ties = lane < warp ? sm.ties[lane] : 0;
-  if (lane < rank) {  // at most 16 CTAs
-    above += peer_load(&sm.cta[0], lane);
-    ties += peer_load(&sm.cta[1], lane);
-  }
-  above = __reduce_add_sync(0xffffffffu, above);  // before this warp's run
-  ties = __reduce_add_sync(0xffffffffu, ties);
-  const uint32_t below = (1u << lane) - 1;
-  for (int i = w0 + lane; i < w0 + ((w1 - w0 + 31) & ~31); i += 32) {
-    const uint32_t v = i < w1 ? number(i) : 0u;
-    const bool up = i < w1 && v > found, tie = i < w1 && v == found;
-    const uint32_t ups = __ballot_sync(0xffffffffu, up), eqs = __ballot_sync(0xffffffffu, tie);
-    const int my_ties = ties + __popc(eqs & below);
-    const int at = q.s + above + __popc(ups & below) + min(my_ties, left);
-    // (the bound holds unless someone writes the weights meanwhile)
-    if ((up || (tie && my_ties < left)) && at < q.k - q.r) kept[at] = q.s + i0 + i;
-    above += __popc(ups);
-    ties += __popc(eqs);
-  }
-  cluster_barrier();  // no CTA leaves while another may read its counts
+  if (q.m > 0) cluster_barrier();  // no CTA leaves while another may read its counts
 }
 
 // ---- compaction -------------------------------------------------------------------------
@@ -269,11 +332,12 @@ __device__ __forceinline__ int64_t kept_rows(const LatentCompactArgs& a, int b) 
 }
 
 // By one block: the chunks in front of each sequence, no chunk taken, none read.
-__global__ void __launch_bounds__(kEvThreads) compact_chunks_kernel(const LatentCompactArgs a) {
+constexpr int kListThreads = 1024;
+__global__ void __launch_bounds__(kListThreads) compact_chunks_kernel(const LatentCompactArgs a) {
   grid_dep_launch();
-  __shared__ int part[kEvWarps];
+  __shared__ int part[kListThreads / 32];
   int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kEvThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += kListThreads) {
     const int b = b0 + threadIdx.x;
     int n = 0;
     if (b < a.B) {
@@ -282,15 +346,16 @@ __global__ void __launch_bounds__(kEvThreads) compact_chunks_kernel(const Latent
       n = (int)((k + kCpRows - 1) / kCpRows);
     }
     int total;
-    const int own = block_scan(n, part, &total);
+    const int own = block_scan<kListThreads / 32>(n, part, &total);
     if (b < a.B) a.chunk0[b] = before + own;
     before += total;
+    __syncthreads();
   }
   if (threadIdx.x == 0) {
     a.chunk0[a.B] = before;
     a.chunk0[a.B + 1] = 0;  // the next chunk to hand out
   }
-  for (int64_t i = threadIdx.x; i < before; i += kEvThreads) a.read[i] = 0;
+  for (int64_t i = threadIdx.x; i < before; i += kListThreads) a.read[i] = 0;
 }
 
 // The first of n rising values that is >= x, by a warp.
@@ -420,12 +485,14 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& in, cudaStream_t stream) {
   PagedEvictArgs a = in;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
   const int64_t most = (int64_t)a.max_pages << a.page_shift;
-  // CTAs of a sequence: as the SMs allow, each with 2048 rows or more where sequences can be as
-  // long as the table; up to 16 of them (a cluster's size on this GPU).
+  // CTAs of a sequence: as many as the SMs take at once, two each, if sequences can be as long as the
+  // table allows: those beyond 2048 rows each would have nothing to do.  Up to 8, and 16 for few
+  // sequences (clusters of 16 find room only three at a time: 8 of 30000 rows 65 us).
   int C = 1;
-  while (C < 16 && (int64_t)a.B * 2 * C <= sms && most > (int64_t)2048 * C) C *= 2;
+  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= 2 * sms && most > (int64_t)2048 * C) C *= 2;
   constexpr int kMostHeld = 49152;  // numbers that fit beside the histograms
-  a.held = (int)std::min<int64_t>((most + C - 1) / C, kMostHeld);
+  const int64_t per = (most + C - 1) / C;
+  a.held = per <= kEvThreads * kEvPer ? 0 : (int)std::min<int64_t>(per, kMostHeld);
   static std::atomic<uint64_t> attr_done{0};  // bit per device: attributes set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -468,7 +535,7 @@ cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t strea
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_release);
   }
-  compact_chunks_kernel<<<1, kEvThreads, 0, stream>>>(a);
+  compact_chunks_kernel<<<1, kListThreads, 0, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
