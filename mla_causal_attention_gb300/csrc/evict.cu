@@ -544,7 +544,7 @@ cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t strea
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, (chunks + kCpWarps - 1) / kCpWarps));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, chunks));
   cfg.blockDim = dim3(32 * kCpWarps);
   cfg.dynamicSmemBytes = kCpSmem;
   cfg.stream = stream;

@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kApplyThreads) rope_apply_kernel(const RopeApp
       to[i] = real ? t * a.y_row + h * a.y_head : -1;
       if (real) {
         const T* src = x + t * a.x_row + h * a.x_head;
-        lo[i].raw = *reinterpret_cast<const uint4*>(src + x0);
-        hi[i].raw = *reinterpret_cast<const uint4*>(src + x1);
+        lo[i].raw = __ldcs(reinterpret_cast<const uint4*>(src + x0));
+        hi[i].raw = __ldcs(reinterpret_cast<const uint4*>(src + x1));
       }
       if (kShared ? i == 0 : real) {
         const float* cs = table_row(a, t);
