@@ -811,15 +811,20 @@ _LAYOUTS = {"half": 0, "interleaved": 1}
 
 def _row_steps(t, name, shape, device):
     """(row, head) strides of a [T, R] or [T, H, R] tensor whose last dimension is contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous, got strides {st}")
+    try:  # the usual case, in few steps
+        st = t.stride()
+        if t.shape != shape or t.get_device() != device.index or st[-1] != 1:
+            st = None
+    except AttributeError:
+        st = None
+    if st is None:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        raise ValueError(f"{name}: the last dimension must be contiguous, got strides {t.stride()}")
     return st[0], st[1] if len(shape) == 3 else 0
 
 

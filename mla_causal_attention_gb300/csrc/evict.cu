@@ -62,11 +62,10 @@ __device__ __forceinline__ int peer_load(const int* p, uint32_t rank) {
 // stay in registers for all passes, or, with more than 8 to a thread, in shared memory.  The work is 4
 // bytes per row: what bounds it is latency, of the loads through the block table and of the barriers
 // between the passes.
-constexpr int kEvThreads = 512;
-constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvPer = 8;        // rows of a thread at a time
 constexpr int kPasses = 4, kBins = 256;  // (three of 2048: every CTA reads all histograms, 10 us a pass)
 
+template <int kEvWarps>
 struct EvictSmem {
   int hist[kPasses][kBins];
   int part[kPasses + 1][kEvWarps];  // of block-wide scans
@@ -121,9 +120,13 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
   return inc - v + __reduce_add_sync(0xffffffffu, lane < warp ? p : 0);
 }
 
-__global__ void __launch_bounds__(kEvThreads, 2) paged_evict_kernel(const PagedEvictArgs a) {
+// kEvThreads: 512, two CTAs on an SM, or 1024 where a CTA's rows are more than the registers of 512 hold.
+template <int kEvThreads>
+__global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
+    paged_evict_kernel(const PagedEvictArgs a) {
+  constexpr int kEvWarps = kEvThreads / 32;
   extern __shared__ uint32_t keys[];  // this CTA's numbers, the first a.held of them
-  __shared__ EvictSmem sm;
+  __shared__ EvictSmem<kEvWarps> sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int b = blockIdx.x / C;
@@ -481,17 +484,11 @@ __global__ void __launch_bounds__(32 * kCpWarps) latent_compact_kernel(const Lat
 
 }  // namespace
 
-cudaError_t launch_paged_evict(const PagedEvictArgs& in, cudaStream_t stream) {
-  PagedEvictArgs a = in;
-  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
-  const int64_t most = (int64_t)a.max_pages << a.page_shift;
-  // CTAs of a sequence: as many as the SMs take at once, two each, if sequences can be as long as the
-  // table allows: those beyond 2048 rows each would have nothing to do.  Up to 8, and 16 for few
-  // sequences (clusters of 16 find room only three at a time: 8 of 30000 rows 65 us).
-  int C = 1;
-  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= 2 * sms && most > (int64_t)2048 * C) C *= 2;
+namespace {
+
+template <int kEvThreads>
+cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, cudaStream_t stream) {
   constexpr int kMostHeld = 49152;  // numbers that fit beside the histograms
-  const int64_t per = (most + C - 1) / C;
   a.held = per <= kEvThreads * kEvPer ? 0 : (int)std::min<int64_t>(per, kMostHeld);
   static std::atomic<uint64_t> attr_done{0};  // bit per device: attributes set
   int dev = 0;
@@ -499,10 +496,11 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& in, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMostHeld * 4);
+    e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_release);
   }
@@ -518,9 +516,22 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& in, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_evict_kernel, a);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, paged_evict_kernel<kEvThreads>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream) {
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
+  const int64_t most = (int64_t)a.max_pages << a.page_shift;
+  // CTAs of a sequence: as many as the SMs take at once, two each, if sequences can be as long as the
+  // table allows: those beyond 2048 rows each would have nothing to do.  Up to 8, and 16 for few
+  // sequences (clusters of 16 find room only three at a time: 8 of 30000 rows 65 us, 12 with 8).
+  int C = 1;
+  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= 2 * sms && most > (int64_t)2048 * C) C *= 2;
+  const int64_t per = (most + C - 1) / C;
+  return per > 512 * kEvPer ? launch_evict<1024>(a, C, per, stream)
+                            : launch_evict<512>(a, C, per, stream);
 }
 
 cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t stream) {

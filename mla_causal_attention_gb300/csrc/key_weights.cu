@@ -499,32 +499,110 @@ __global__ void __launch_bounds__(kRows) row_lse_kernel(const KeyWeightsArgs a) 
   a.lse[(size_t)n0.x + r] = row_lse(m, l);
 }
 
+// The slots of the unit whose rows begin with `row`, in the order of its keys, by a warp; their number,
+// 0 if it was not shared.
+__device__ __forceinline__ int unit_slots(const KeyWeightsArgs& a, int row, int lane, int16_t* list) {
+  const int slots = 2 * a.t.pairs;
+  int s0 = -1;
+  for (int i = lane; i < slots; i += 32) {
+    const int4 n = a.t.part_note[i];
+    if (n.z != 0 && n.x == row) s0 = i;
+  }
+  s0 = __reduce_max_sync(0xffffffffu, s0);
+  if (s0 < 0) return 0;
+  if (lane == 0) list[0] = (int16_t)s0;
+  int n = 1;
+  bool last = false;
+  for (int s = (s0 | 1) + 1; s < slots && !last; s += 64) {
+    const int at = s + 2 * lane;
+    const int4 x = at < slots ? a.t.part_note[at] : make_int4(0, 0, 0, 0);
+    const uint32_t ends = __ballot_sync(0xffffffffu, x.y != 0 && x.w != 0);
+    const uint32_t upto = ends ? (2u << (__ffs(ends) - 1)) - 1 : 0xffffffffu;
+    const uint32_t some = __ballot_sync(0xffffffffu, x.y != 0) & upto;
+    if ((some >> lane) & 1u) list[n + __popc(some & ((1u << lane) - 1))] = (int16_t)at;
+    n += __popc(some);
+    last = ends != 0;
+  }
+  return n;
+}
+
 }  // namespace stats
 
 // ---- the sum over the rows, of scores that were kept ------------------------------------
 // A block takes tiles of 128 keys; its eight warps share the rows, a lane has four keys.  Bound by
-// reading the scores, 4 bytes per row and key, mostly from L2.
+// reading the scores, 4 bytes per row and key, mostly from L2.  kMerge: the blocks work out the L of
+// their rows themselves, which saves a kernel between two others; where all rows of a call are no
+// more than a sequence's may be (one token on 1000 keys: 22.5 -> KMERGE us).
 namespace kept {
 
 constexpr int kReadThreads = 256;
 constexpr int kDeep = 8;  // rows in flight per warp
 
+template <bool kMerge>
 __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeightsArgs a) {
   __shared__ float part[8][kTile];
+  __shared__ float own_lse[kMerge ? kKeptRows : 1];
+  __shared__ int16_t list[kMerge ? kKeptRows / kRows : 1][256];  // slots of the sequence's units
+  __shared__ int parts[kMerge ? kKeptRows / kRows : 1];
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   const int64_t tiles = a.steps.read0[a.t.B];
   const float sl2 = a.t.scale_log2;
-  for (int64_t x = blockIdx.x; x < tiles; x += gridDim.x) {
-    const int b = find_warp(a.steps.read0, a.t.B, x, lane);
-    const TreeSeq s = tree_seq(a.t, b);
-    const int k = (int)(x - a.steps.read0[b]), rows = s.n * a.t.H, K = seq_tiles(s);
+  // An equal run of tiles for every block, mostly of one sequence, which it looks up once.
+  const int64_t x0 = tiles * blockIdx.x / gridDim.x, x1 = tiles * (blockIdx.x + 1) / gridDim.x;
+  int64_t base = 0, next = -1;
+  int b = 0, rows = 0, K = 0;
+  TreeSeq s = {};
+  const float* lse = nullptr;
+  const float* store = nullptr;
+  for (int64_t x = x0; x < x1; ++x) {
+    if (x >= next) {
+      b = find_warp(a.steps.read0, a.t.B, x, lane);
+      base = a.steps.read0[b];
+      next = a.steps.read0[b + 1];
+      s = tree_seq(a.t, b);
+      rows = s.n * a.t.H;
+      K = seq_tiles(s);
+      lse = a.lse + (size_t)s.q0 * a.t.H;
+      store = a.store + a.steps.store0[b];
+      if constexpr (kMerge) {
+        __syncthreads();  // the rows' L of the sequence before have been read
+        if (warp * kRows < rows) {
+          const int n = stats::unit_slots(a, s.q0 * a.t.H + warp * kRows, lane, list[warp]);
+          if (lane == 0) parts[warp] = n;
+        }
+        __syncthreads();
+        for (int r = threadIdx.x; r < rows; r += kReadThreads) {
+          const int u = r / kRows, n = parts[u];
+          const float2* ml = reinterpret_cast<const float2*>(a.t.part_ml) + r % kRows;
+          float m = -INFINITY, l = 0.f;
+          for (int i = 0; i < n; i += 8) {  // eight partials in flight
+            float2 o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              o[e] = i + e < n ? ml[(size_t)list[u][i + e] * kRows] : make_float2(-INFINITY, 0.f);
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, o[e].x);
+            const float mb = top == -INFINITY ? 0.f : top;
+            l *= ex2_approx(m - mb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) l += o[e].y * ex2_approx(o[e].x - mb);
+            m = top;
+          }
+          own_lse[r] = n > 0 ? row_lse(m, l) : lse[r];
+        }
+        __syncthreads();
+        lse = own_lse;
+      }
+    }
+    const int k = (int)(x - base);
     const int key = k * kTile + (int)threadIdx.x;
     const bool mine = threadIdx.x < kTile && key < s.kv;
     const int slot = mine ? key_row(a.t, b, s.kv, key) : 0;
-    const float* lse = a.lse + (size_t)s.q0 * a.t.H;
-    const float* store = a.store + a.steps.store0[b];
+    const bool writes = mine && slot < a.t.num_pages << a.t.page_shift;
+    const float held = writes && key < s.ctx && a.decay != 0.f ? a.weights[slot] : 0.f;
     // Row r is in unit r / 128, whose rows of a tile lie together.
     const auto at = [&](int r) {
       const int m = r / kRows, unit_rows = min(kRows, rows - m * kRows);
@@ -565,12 +643,11 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
     *reinterpret_cast<float4*>(&part[warp][4 * lane]) =
         make_float4(total[0], total[1], total[2], total[3]);
     __syncthreads();
-    if (mine && slot < a.t.num_pages << a.t.page_shift) {
+    if (writes) {
       float got = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) got += part[w][threadIdx.x];
-      float* w = a.weights + slot;
-      *w = key < s.ctx && a.decay != 0.f ? fmaf(*w, a.decay, got) : got;
+      a.weights[slot] = fmaf(held, a.decay, got);
     }
     __syncthreads();
   }
@@ -1080,13 +1157,18 @@ cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
   cfg.dynamicSmemBytes = stats::kSmem;
   e = cudaLaunchKernelEx(&cfg, stats::row_stats_kernel, p);
   if (e != cudaSuccess) return e;
-  cfg.blockDim = dim3(kRows);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, stats::row_lse_kernel, a);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(2 * a.t.pairs * 6);
+  if (!a.all_kept) {
+    cfg.blockDim = dim3(kRows);
+    e = cudaLaunchKernelEx(&cfg, stats::row_lse_kernel, a);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t tiles =  // at most
+      (int64_t)a.t.B * ((((int64_t)a.t.max_pages << a.t.page_shift) + kTile - 1) / kTile);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(2 * a.t.pairs * 12, tiles));
   cfg.blockDim = dim3(kept::kReadThreads);
-  e = cudaLaunchKernelEx(&cfg, kept::key_read_kernel, a);
+  e = a.all_kept ? cudaLaunchKernelEx(&cfg, kept::key_read_kernel<true>, a)
+                 : cudaLaunchKernelEx(&cfg, kept::key_read_kernel<false>, a);
   if (e != cudaSuccess || a.all_kept) return e;
   cfg.gridDim = dim3(2 * a.t.pairs);
   cfg.blockDim = dim3(kThreads);
