@@ -67,11 +67,11 @@ constexpr int kPasses = 4, kBins = 256;  // (three of 2048: every CTA reads all 
 
 template <int kEvWarps>
 struct EvictSmem {
-  int hist[kPasses][kBins];
-  int part[kPasses + 1][kEvWarps];  // of block-wide scans
+  alignas(16) int hist[kPasses][kBins];
+  alignas(16) int sum[2][kBins];  // all CTAs' histograms, by the parity of the pass
+  int part[kEvWarps];             // of a block-wide scan
   int above[kEvWarps], ties[kEvWarps];  // rows of each warp's run
   alignas(8) int cta[2];          // rows above, ties of this CTA
-  int bin[kPasses], left[kPasses];  // the bin found, and the rank that is left within it
 };
 
 struct EvictSeq {
@@ -125,7 +125,7 @@ template <int kEvThreads>
 __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
     paged_evict_kernel(const PagedEvictArgs a) {
   constexpr int kEvWarps = kEvThreads / 32;
-  extern __shared__ uint32_t keys[];  // this CTA's numbers, the first a.held of them
+  extern __shared__ uint32_t keys[];  // numbers of each warp's first a.held rounds of rows
   __shared__ EvictSmem<kEvWarps> sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
@@ -134,18 +134,20 @@ __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
   int32_t* kept = a.kept + (int64_t)b * a.K;
   const int share = rank * kEvThreads + tid, shares = C * kEvThreads;
-  // Pages past the kept rows, behind those of the sequences before: the last CTA lists them.  What it
-  // loads for that is on its way together with the weights.
-  const bool lists = a.freed && rank == C - 1;
+  // Pages past the kept rows, behind those of the sequences before.  What is loaded for that is on its
+  // way together with the weights.
   const int gone0 = pages_for(a, q.k), gone = pages_for(a, q.len) - gone0;
   int before = 0, page0 = 0;
-  if (lists) {
+  if (a.freed) {
     for (int i = tid; i < b; i += kEvThreads) {
       const EvictSeq o = evict_seq(a, i);
       before += pages_for(a, o.len) - pages_for(a, o.k);
     }
-    if (tid < gone) page0 = table[gone0 + tid];
+    if (share < gone) page0 = table[gone0 + share];
   }
+  const auto all_ctas = [&] {  // a barrier over the cluster
+    if (C > 1) cluster_barrier(); else __syncthreads();
+  };
 
   if (q.m > 0) {
     // This CTA's run of the rows between the ends, and this warp's of those.
@@ -177,22 +179,20 @@ __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
 #pragma unroll
       for (int e = 0; e < kEvPer; ++e) v[e] = order_of(__uint_as_float(v[e]));
     };
+    uint32_t* mine = keys + (size_t)warp * a.held * 32 * kEvPer + lane;  // 32 kEvPer to a round
     const auto fetch = [&](int round) {
       if (rounds == 1) return;  // they are in the registers
-      const int first = w0 + 32 * kEvPer * round + lane;
-      if (w1 > a.held) return weigh(round);
+      if (round >= a.held) return weigh(round);
 #pragma unroll
-      for (int e = 0; e < kEvPer; ++e) v[e] = first + 32 * e < w1 ? keys[first + 32 * e] : 0u;
+      for (int e = 0; e < kEvPer; ++e) v[e] = mine[32 * (kEvPer * round + e)];
     };
     weigh(0);
     for (int i = tid; i < kPasses * kBins; i += kEvThreads) (&sm.hist[0][0])[i] = 0;
-    if (rounds > 1 && w1 <= a.held)
-      for (int r = 0; r < rounds; ++r) {
-        const int first = w0 + 32 * kEvPer * r + lane;
+    if (rounds > 1)
+      for (int r = 0; r < min(rounds, a.held); ++r) {
         if (r > 0) weigh(r);
 #pragma unroll
-        for (int e = 0; e < kEvPer; ++e)
-          if (first + 32 * e < w1) keys[first + 32 * e] = v[e];
+        for (int e = 0; e < kEvPer; ++e) mine[32 * (kEvPer * r + e)] = v[e];
       }
     __syncthreads();
 
@@ -210,28 +210,48 @@ __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
           if (first + 32 * e < w1 && (v[e] & agree) == found)
             atomicAdd(&sm.hist[pass][(v[e] >> shift) & 255], 1);
       }
-      cluster_barrier();
-      // Thread t < 256 adds up bin 255 - t, so that a prefix sum counts from the top.
-      const int bin = kBins - 1 - tid;
-      int at = 0;
-      if (tid < kBins) {
-        for (int c0 = 0; c0 < C; c0 += 8) {
-          int x[8];
+      all_ctas();
+      const int* sum = sm.hist[pass];
+      if (C > 1) {
+        if (tid < kBins) {
+          int at = 0;
+          for (int c0 = 0; c0 < C; c0 += 8) {
+            int x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = peer_load(&sm.hist[pass][bin], min(c0 + e, C - 1));
+            for (int e = 0; e < 8; ++e) x[e] = peer_load(&sm.hist[pass][tid], min(c0 + e, C - 1));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) at += c0 + e < C ? x[e] : 0;
+            for (int e = 0; e < 8; ++e) at += c0 + e < C ? x[e] : 0;
+          }
+          sm.sum[pass & 1][tid] = at;
         }
+        __syncthreads();
+        sum = sm.sum[pass & 1];
       }
-      int total;
-      const int above = block_scan<kEvWarps>(at, sm.part[pass], &total);
-      if (above < left && left <= above + at) {
-        sm.bin[pass] = bin;
-        sm.left[pass] = left - above;
+      // Every warp finds the bin for itself: lane l has bins 8 (31 - l) .. + 7, so that a prefix sum
+      // counts from the top.
+      const int lo = 8 * (31 - lane);
+      const int4 x = *reinterpret_cast<const int4*>(sum + lo), y = *reinterpret_cast<const int4*>(sum + lo + 4);
+      const int d[8] = {y.w, y.z, y.y, y.x, x.w, x.z, x.y, x.x};
+      int all = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) all += d[e];
+      int upto = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += z;
       }
-      __syncthreads();
-      found |= (uint32_t)sm.bin[pass] << shift;
-      left = sm.left[pass];
+      const uint32_t reach = __ballot_sync(0xffffffffu, upto >= left);
+      const int at = __ffs(reach) - 1;  // the first lane by which the m-th is counted
+      int bin = lo + 7, rest = left - (upto - all);
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (rest > d[e] && bin == lo + 7 - e) {
+          rest -= d[e];
+          --bin;
+        }
+      found |= (uint32_t)__shfl_sync(0xffffffffu, bin, at) << shift;
+      left = __shfl_sync(0xffffffffu, rest, at);
     }
 
     // `left` of the rows equal to `found` are kept, the lowest ones.
@@ -254,14 +274,16 @@ __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
     __syncthreads();
     above = lane < kEvWarps ? sm.above[lane] : 0;
     ties = lane < kEvWarps ? sm.ties[lane] : 0;
-    if (warp == 0) {
-      const int x = __reduce_add_sync(0xffffffffu, above), y = __reduce_add_sync(0xffffffffu, ties);
-      if (lane == 0) {
-        sm.cta[0] = x;
-        sm.cta[1] = y;
+    if (C > 1) {
+      if (warp == 0) {
+        const int x = __reduce_add_sync(0xffffffffu, above), y = __reduce_add_sync(0xffffffffu, ties);
+        if (lane == 0) {
+          sm.cta[0] = x;
+          sm.cta[1] = y;
+        }
       }
+      cluster_barrier();
     }
-    cluster_barrier();
     if (lane >= warp) above = ties = 0;
     if (lane < rank) {  // at most 16 CTAs
       const int2 o = peer_load2(sm.cta, lane);
@@ -299,17 +321,17 @@ __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
     a.kept_len[b] = q.k;
     if (q.bad) set_status(a.status, MLA_ERR_KVLEN);
   }
-  if (lists) {
+  if (a.freed) {
     int at;
-    block_scan<kEvWarps>(before, sm.part[kPasses], &at);
-    for (int i = tid; i < gone; i += kEvThreads) {
-      const int page = i == tid ? page0 : table[gone0 + i];
+    block_scan<kEvWarps>(before, sm.part, &at);
+    for (int i = share; i < gone; i += shares) {
+      const int page = i == share ? page0 : table[gone0 + i];
       if (page < 0 || page >= a.num_pages) set_status(a.status, MLA_ERR_PAGE);
       a.freed[at + i] = page;
     }
-    if (b == a.B - 1 && tid == 0) a.n_freed[0] = at + gone;
+    if (b == a.B - 1 && share == 0) a.n_freed[0] = at + gone;
   }
-  if (q.m > 0) cluster_barrier();  // no CTA leaves while another may read its counts
+  if (q.m > 0 && C > 1) cluster_barrier();  // no CTA leaves while another may read its counts
 }
 
 // ---- compaction -------------------------------------------------------------------------
@@ -488,8 +510,10 @@ namespace {
 
 template <int kEvThreads>
 cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, cudaStream_t stream) {
-  constexpr int kMostHeld = 49152;  // numbers that fit beside the histograms
-  a.held = per <= kEvThreads * kEvPer ? 0 : (int)std::min<int64_t>(per, kMostHeld);
+  // Rounds of a warp's rows whose numbers are kept in shared memory: none where there is but one.
+  constexpr int kRound = kEvThreads * kEvPer, kMostHeld = 49152 / kRound;
+  const int64_t rounds = (per + kRound - 1) / kRound + 1;  // a warp's run is a multiple of 32 rows
+  a.held = per <= kRound ? 0 : (int)std::min<int64_t>(rounds, kMostHeld);
   static std::atomic<uint64_t> attr_done{0};  // bit per device: attributes set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -497,7 +521,7 @@ cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, cudaStream_t stre
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
     e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * kRound * 4);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -512,7 +536,7 @@ cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, cudaStream_t stre
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * C));
   cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = (size_t)a.held * 4;
+  cfg.dynamicSmemBytes = (size_t)a.held * kRound * 4;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -524,11 +548,12 @@ cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, cudaStream_t stre
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream) {
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
   const int64_t most = (int64_t)a.max_pages << a.page_shift;
-  // CTAs of a sequence: as many as the SMs take at once, two each, if sequences can be as long as the
-  // table allows: those beyond 2048 rows each would have nothing to do.  Up to 8, and 16 for few
-  // sequences (clusters of 16 find room only three at a time: 8 of 30000 rows 65 us, 12 with 8).
+  // CTAs of a sequence: one for 4096 rows that the table allows, up to 8, or 16 for few sequences, and
+  // no more than the SMs take at once.  A barrier over a cluster takes 0.6 us and there are seven: 64
+  // sequences of up to 8192 rows take 13.8 us with a CTA for 2048 rows, 10.3 for 4096, 10.9 for 8192.
+  // Clusters of 16 find room only three at a time (8 of 30000 rows 65 us, 10 with 8 CTAs).
   int C = 1;
-  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= 2 * sms && most > (int64_t)2048 * C) C *= 2;
+  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= 2 * sms && most > (int64_t)4096 * C) C *= 2;
   const int64_t per = (most + C - 1) / C;
   return per > 512 * kEvPer ? launch_evict<1024>(a, C, per, stream)
                             : launch_evict<512>(a, C, per, stream);
