@@ -572,8 +572,8 @@ MLA_API mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t
  * more than the cached length: mla_paged_plan's positions count from the cached length, so a
  * server adds what it has dropped.
  *
- * K at least every min(kv_len[b], budget[b]), B up to 65535, max_pages * page_size below 2^31; no
- * output may overlap an input or another output (MLA_ERR_ARG, as for negative sinks or recent).
+ * K at least every min(kv_len[b], budget[b]), B up to 65535, max_pages * page_size and B * max_pages
+ * below 2^31; no output may overlap an input or another output (MLA_ERR_ARG, as for negative sinks or recent).
  * Device-side problems (the call completes): a length outside the table, a budget below zero or more
  * rows to keep than K (MLA_ERR_KVLEN, clamped); a page outside the pool (MLA_ERR_PAGE: its rows
  * count as lowest).  workspace: 256 bytes (the status word), zeroed once.
@@ -594,7 +594,7 @@ MLA_API mla_status mla_paged_evict(const float* weights, int num_pages, int page
  *
  * kept [B, K] int32, each row rising, as mla_paged_evict lists it (any rising list of rows will
  * do); kept_len [B].  The sequences of a call have pages of their own: a page that two of them
- * name is moved by both at once, and holds some mixture.  B up to 65535.
+ * name is moved by both at once, and holds some mixture.  B up to 65535, B * K up to 2^35.
  * Device-side problems (the call completes): kept_len outside [0, K] (MLA_ERR_KVLEN, clamped); an
  * entry below its own index or past the table (MLA_ERR_KVLEN), or a page outside the pool
  * (MLA_ERR_PAGE): that row is not moved.  A list that does not rise moves rows that others have

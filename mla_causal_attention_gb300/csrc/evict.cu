@@ -472,7 +472,14 @@ __global__ void __launch_bounds__(32 * kCpWarps) latent_compact_kernel(const Lat
       asm volatile("" ::"f"(w) : "memory");  // the weight is here
       __threadfence();
       __syncwarp();
-      if (lane == 0) atomicExch(a.read + g, 1);
+#ifdef MLA_TEST_DROP_READ
+      // Test build only: the first chunk does not say that it has been read.  The bounded waits for
+      // it then give up.
+      const bool says = g != 0;
+#else
+      constexpr bool says = true;
+#endif
+      if (lane == 0 && says) atomicExch(a.read + g, 1);
       for (int q = k0 / kCpRows + lane; ok && q < c && q * kCpRows < k1; q += 32) {
         const int* flag = a.read + first + q;
         int seen;

@@ -991,7 +991,7 @@ mla_status mla_paged_evict(const float* weights, int num_pages, int page_size,
   const mla_status ps = check_pool(num_pages, page_size);
   if (ps != MLA_OK) return ps;
   if (B < 1 || B > 65535 || K < 1 || max_pages < 1 || (int64_t)max_pages * page_size > 0x7fffffff ||
-      (int64_t)B * K > kMaxElems)
+      (int64_t)B * K > kMaxElems || (int64_t)B * max_pages > 0x7fffffff)
     return MLA_ERR_SHAPE;
   if (sinks < 0 || recent < 0) return MLA_ERR_ARG;
   const void* words[] = {weights, block_table, kv_len, budget, kept, kept_len, freed, n_freed};
@@ -1038,7 +1038,7 @@ mla_status mla_latent_compact(uint16_t* c_pages, uint16_t* pe_pages, float* weig
   const mla_status ps = check_pool(num_pages, page_size);
   if (ps != MLA_OK) return ps;
   if (B < 1 || B > 65535 || K < 1 || max_pages < 1 || (int64_t)max_pages * page_size > 0x7fffffff ||
-      (int64_t)B * K > kMaxElems)
+      (int64_t)B * K > (int64_t(1) << 35))
     return MLA_ERR_SHAPE;
   const void* words[] = {weights, block_table, kept, kept_len};
   for (const void* w : words)

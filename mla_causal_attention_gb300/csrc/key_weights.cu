@@ -149,6 +149,17 @@ __device__ __forceinline__ void leave(volatile int* abort_flag, int warp, uint32
   }
 }
 
+// Test build only: a warp of the first pair withholds the arrival that frees its first score tile.  The MMA
+// warp's bounded wait for it then gives up, which exercises the timeout report and the unwinding of
+// both CTAs.
+__device__ __forceinline__ bool withheld(uint32_t t) {
+#ifdef MLA_TEST_DROP_S_FREE
+  return blockIdx.x == 0 && threadIdx.x == 128 && t == 0;
+#else
+  return false;
+#endif
+}
+
 // log2 of a row's sum of weights 2^(s - m), plus m; infinite for a row that sees nothing.
 __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.f ? m + log2f(l) : l == 0.f ? INFINITY : l;
@@ -157,7 +168,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // ---- each row's maximum and sum ---------------------------------------------------------
 namespace stats {
 
-constexpr int kAhead = 2;        // tiles between a tile's L2 prefetch and its loads
+constexpr int kAhead = 1;        // tiles between a tile's L2 prefetch and its loads (2: trees 105 us, 1: 102)
 constexpr int kOffQ = 0;                       // 17 sub-tiles: q_lat's two parts, q_pe
 constexpr int kOffK = kOffQ + 17 * kSub64;     // 9 sub-tiles: latent columns, rotary key
 constexpr int kOffRed = kOffK + 9 * kSub64;    // [64 rows] (maximum, sum) of the upper keys
@@ -251,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                    ? key_row(a, g.b, g.s.kv, tile * kTile + 64 * rank + lane * box) : 0;
       };
       int rows_next = look(g.k0);
-      // Keys that few units read come from HBM, and are asked into L2 two tiles before their loads.
+      // Keys that few units read come from HBM, and are asked into L2 ahead of their loads.
       const bool ask = g.s.n * a.H <= kKeptRows;
       int ahead = ask && g.k0 + kAhead < g.k1 ? look(g.k0 + kAhead) : 0;
       if (ns > 0) ok = mbar_wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
@@ -400,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int c = 0; c < 2; ++c) pin<32>(x[c]);
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tp::arrive(s_free + 8 * (t & 1));
+        if (lane == 0 && !withheld(t)) tp::arrive(s_free + 8 * (t & 1));
         const int key = k * kTile + 64 * half;
         if ((k + 1) * kTile > g.s.ctx) {  // the tile holds new tokens or ends behind the last
           const uint64_t seen = seen_bits(key, g.s.ctx, g.s.kv, masked, mask, i);
@@ -1015,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (c + 32 >= cols) {
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tp::arrive(s_free + 8 * (t & 1));
+            if (lane == 0 && !withheld(t)) tp::arrive(s_free + 8 * (t & 1));
           }
           if (all_see) {
 #pragma unroll
@@ -1044,6 +1055,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         dropped = (sum - total) - y;
         total = sum;
       }
+      ok = readers_and(ok);  // the four warps leave together: below are barriers between them
+      if (!ok) break;
       float got = total;
       bool mine = true;
       if (g.r1 - g.r0 < g.tiles) {
@@ -1056,10 +1069,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int at = rank * 128 + tid;
         p.a.part_sum[(size_t)(pair_id == c0 ? slot0 : 2 * pair_id) * kKeyTile + at] = total;
         __threadfence();
-        ok = readers_and(ok);
-        if (ok && tid == 0) bars->last = atomicAdd(p.a.steps.count + 2 * c0 + rank, 1) == c1 - c0;
-        ok = readers_and(ok);
-        mine = ok && bars->last != 0;
+        readers_and(true);
+        if (tid == 0) bars->last = atomicAdd(p.a.steps.count + 2 * c0 + rank, 1) == c1 - c0;
+        readers_and(true);
+        mine = bars->last != 0;
         if (mine) {
           __threadfence();
           got = 0.f;
@@ -1067,7 +1080,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             got += __ldcg(p.a.part_sum + (size_t)(c == c0 ? slot0 : 2 * c) * kKeyTile + at);
         }
       }
-      if (!ok) break;
       if (mine && key.slot >= 0) p.a.weights[key.slot] = fmaf(key.held, p.a.decay, got);
       more = then;
     }
