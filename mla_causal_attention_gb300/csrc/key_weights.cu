@@ -543,7 +543,7 @@ __device__ __forceinline__ int unit_slots(const KeyWeightsArgs& a, int row, int 
 // A block takes tiles of 128 keys; its eight warps share the rows, a lane has four keys.  Bound by
 // reading the scores, 4 bytes per row and key, mostly from L2.  kMerge: the blocks work out the L of
 // their rows themselves, which saves a kernel between two others; where all rows of a call are no
-// more than a sequence's may be (one token on 1000 keys: 22.5 -> KMERGE us).
+// more than a sequence's may be (one token on 1000 keys: 19.1 -> 15.5 us on the GPU).
 namespace kept {
 
 constexpr int kReadThreads = 256;
