@@ -223,6 +223,51 @@ def test_compaction_of_shifted_runs():
     compact_case([3000], [list(range(0, 3000, 2))], 16, 1, weights=False, extra=5000)
 
 
+def test_compaction_of_many():
+    r = random.Random(5)
+    lens = [r.randint(0, 90) for _ in range(1500)]
+    compact_case(lens, [_some(r, n, r.randint(0, n)) for n in lens], 16, 3)
+
+
+def test_compaction_in_a_pool_past_4_gb():
+    page, n, far = 64, 500, 80000
+    pages_n = pages(n, page)
+    c = torch.empty(far, page, 512, dtype=torch.bfloat16, device="cuda")
+    pe = torch.empty(far, page, 64, dtype=torch.bfloat16, device="cuda")
+    rows = [torch.randn(pages_n, page, k, device="cuda").bfloat16() for k in (512, 64)]
+    c[-pages_n:], pe[-pages_n:] = rows
+    table = torch.arange(far - pages_n, far, device="cuda", dtype=torch.int32)[None].contiguous()
+    kept = list(range(0, n, 3))
+    mla.mla_latent_compact(c, pe, table, _i([kept]), _i([len(kept)]))
+    torch.cuda.synchronize()
+    for pool, old in zip((c, pe), rows):
+        old = old.view(-1, old.shape[-1])
+        new = pool[-pages_n:].reshape(-1, old.shape[-1])
+        assert torch.equal(new[:len(kept)], old[torch.tensor(kept, device="cuda")])
+        assert torch.equal(new[len(kept):], old[len(kept):])
+
+
+def test_calls_on_two_streams():
+    """Two servers' compactions at once, each with a workspace of its own."""
+    page, n = 64, 20000
+    sets = []
+    for k in range(2):
+        table = torch.randperm(pages(n, page), device="cuda", dtype=torch.int32)[None].contiguous()
+        c, pe = (torch.randn(pages(n, page), page, w, device="cuda").bfloat16() for w in (512, 64))
+        kept = _some(random.Random(k), n, n - 3000 * (k + 1))
+        sets.append((c, pe, table, _i([kept]), _i([len(kept)]), c.clone(), kept,
+                     torch.cuda.Stream(), mla.Workspace("cuda:0")))
+    torch.cuda.synchronize()
+    for c, pe, table, kept, k, _, _, st, ws in sets:
+        mla.mla_latent_compact(c, pe, table, kept, k, workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for c, pe, table, _, _, before, kept, st, ws in sets:
+        s = slots_of(table[0].tolist(), n, page).cuda()
+        at = torch.tensor(kept, device="cuda")
+        assert torch.equal(c.view(-1, 512)[s[:len(kept)]], before.view(-1, 512)[s[at]])
+        assert mla.mla_attn_get_status(ws, stream=st) == 0
+
+
 def test_compaction_skips_what_is_no_such_list():
     ws = mla.Workspace("cuda:0")
     page = 16

@@ -184,6 +184,41 @@ def test_long_cache():
     check(tree_case(6, 1, 16, (70000, 70000), (1, 1), 1024, False), 0.0)
 
 
+def test_many_sequences():
+    check(tree_case(12, 600, 4, (0, 60), (0, 3), 16, False), 1.0)
+
+
+def test_scores_of_some_sequences_are_kept():
+    """Four times 512 rows on 40000 keys: the store of 256 MB has room for three of them."""
+    d = tree_case(13, 4, 64, (39000, 40000), (8, 8), 1024, True)
+    check(d, 0.0)
+    # in another order other ones are kept; nothing else changes
+    order = torch.tensor([3, 1, 0, 2], device="cuda")
+    T = d["q_nope"].shape[0]
+    rows = (order[:, None] * 8 + torch.arange(8, device="cuda")).view(-1)
+    assert T == 32
+    e = dict(d, q_nope=d["q_nope"][rows].contiguous(), q_pe=d["q_pe"][rows].contiguous(),
+             draft_mask=d["draft_mask"][rows].contiguous(),
+             block_table=d["block_table"][order].contiguous(), kv_len=d["kv_len"][order].contiguous())
+    check(e, 0.0)
+
+
+def test_pool_past_4_gb():
+    """The pages of one sequence at the far end of a pool of 5 million rows."""
+    d = tree_case(14, 1, 16, (300, 300), (2, 2), 64, False)
+    pages, far = d["c_pages"].shape[0], 80000
+    c = torch.empty(far, 64, 512, dtype=torch.bfloat16, device="cuda")
+    pe = torch.empty(far, 64, 64, dtype=torch.bfloat16, device="cuda")
+    c[-pages:], pe[-pages:] = d["c_pages"], d["pe_pages"]
+    old = torch.rand(pages, 64, device="cuda")
+    want = call(d, old, 1.0)
+    w = torch.zeros(far, 64, device="cuda")
+    w[-pages:] = old
+    table = torch.where(d["block_table"] < 0, -1, d["block_table"] + far - pages)
+    got = call(dict(d, c_pages=c, pe_pages=pe, block_table=table.to(torch.int32)), w, 1.0)
+    assert torch.equal(got[-pages:], want) and not bool(got[:-pages].any())
+
+
 def test_device_side_problems_are_reported():
     ws = mla.Workspace("cuda:0")
     d = tree_case(7, 2, 16, (100, 200), (3, 5), 16, True)
