@@ -1002,6 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (; more; g = after) {
       const int off = g.k * kKeyTile + 128 * rank + tid - g.s.ctx;  // index among the new tokens, or < 0
       const bool all_see = __all_sync(0xffffffffu, off < 0);
+      const uint32_t bit = off >= 0 && off < 64 ? 1u << (off & 31) : 0u;  // of a mask's upper or lower word
       // Sums in two parts, the running total and what its roundings have dropped: a key's sum goes
       // over up to millions of rows.
       float total = 0.f, dropped = 0.f;
@@ -1036,14 +1037,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               part[e & 3] += lse != INFINITY ? w : 0.f;
             }
           } else {
-#pragma unroll 8
+#pragma unroll
             for (int e = 0; e < 32; ++e) {
               const RowNote row = note[c + e];
-              bool sees = row.lse != INFINITY;
-              if (off >= 0)
-                sees = sees && (masked ? off < 64 && ((row.mask >> off) & 1ull) : off <= row.token);
+              const uint32_t word = off >= 32 ? (uint32_t)(row.mask >> 32) : (uint32_t)row.mask;
+              const bool sees = off < 0 || (masked ? (word & bit) != 0 : off <= row.token);
               const float w = ex2_approx(fmaf(__uint_as_float(x[e]), sl2, -row.lse));
-              part[e & 3] += sees ? w : 0.f;
+              part[e & 3] += sees && row.lse != INFINITY ? w : 0.f;
             }
           }
         }
