@@ -171,10 +171,9 @@ def library():
 
 
 def _status_string(s: int) -> str:
-    try:
-        return library().mla_status_string(int(s)).decode()
-    except Exception:  # pragma: no cover - library missing
+    if _lib is None:  # library() itself raises, with its lock held, where there is none
         return "libmla_attn.so unavailable"
+    return _lib.mla_status_string(int(s)).decode()
 
 
 def mla_attn_workspace_bytes(B: int, H: int, Tq: int, Tk: int) -> int:
