@@ -825,7 +825,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t k_full = tp::even_addr(&bars->k_full[0]);
     const int box = min(1 << a.page_shift, 64);  // keys per TMA box
     const int boxes = 128 / box;                 // boxes of this CTA's keys, at most 8
-    const int pool = a.num_pages << a.page_shift;
     const auto look = [&](const KeySeg& s) {  // lane q: the row of box q of this CTA's keys
       return lane < boxes
                  ? key_row(a, s.b, s.s.kv, s.k * kKeyTile + 128 * rank + lane * box) : 0;
