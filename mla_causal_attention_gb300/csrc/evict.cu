@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
         const bool up = row < w1 && v[e] > found, tie = row < w1 && v[e] == found;
         const uint32_t ups = __ballot_sync(0xffffffffu, up), eqs = __ballot_sync(0xffffffffu, tie);
         const int my_ties = ties + __popc(eqs & below);
-        const int at = q.s + above + __popc(ups & below) + min(my_ties, left);
-        // (the bound holds unless someone writes the weights meanwhile)
-        if ((up || (tie && my_ties < left)) && at < q.k - q.r) kept[at] = q.s + i0 + row;
+        const int at = above + __popc(ups & below) + min(my_ties, left);
+        // (the bounds hold unless someone writes the weights meanwhile)
+        if ((up || (tie && my_ties < left)) && at >= 0 && at < q.m) kept[q.s + at] = q.s + i0 + row;
         above += __popc(ups);
         ties += __popc(eqs);
       }

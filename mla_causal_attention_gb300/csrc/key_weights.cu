@@ -829,10 +829,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       return lane < boxes
                  ? key_row(a, s.b, s.s.kv, s.k * kKeyTile + 128 * rank + lane * box) : 0;
     };
-    int ns = 0;
+    int ns = 0, steps = 0;  // of the segment before, for all of which its keys are in use
     bool ok = true;
     int next = more ? look(g) : 0;
     for (; ok && more; ++ns, g = after) {
+      const uint64_t patience = kWaitLimitNs + (uint64_t)steps * 20000;  // a step takes 2 to 3 us
+      steps = g.r1 - g.r0;
       const int nb = boxes_of(g.s.kv - (g.k * kKeyTile + 128 * rank), 128, box);
       int row[8];
 #pragma unroll
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (more) next = look(after);
 #pragma unroll 1
       for (int grp = 0; grp < 3; ++grp) {
-        if (ns > 0) ok = mbar_wait(&bars->k_empty[grp], (ns - 1) & 1, status, abort_flag);
+        if (ns > 0) ok = mbar_wait(&bars->k_empty[grp], (ns - 1) & 1, status, abort_flag, patience);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (tc::elect_one()) {

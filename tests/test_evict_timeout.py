@@ -67,6 +67,28 @@ def test_key_weights_wait_gives_up(ctx, new):
     assert torch.equal(run(ws), want) and mla.mla_attn_get_status(ws) == 0
 
 
+def test_waits_grow_with_the_rows():
+    """A pair's keys stay in use for 312 tiles of rows, some 0.8 ms: longer than the limit of this build
+    (0.2 ms), which the wait for them grows beyond."""
+    d = tree_case(41, 1, 64, (19400, 19400), (600, 600), 64, False)
+    old = torch.zeros(d["c_pages"].shape[:2], device="cuda")
+    ws = mla.Workspace("cuda:0")
+
+    def run():
+        w = old.clone()
+        mla.mla_latent_key_weights(d["q_nope"], d["q_pe"], d["c_pages"], d["pe_pages"],
+                                   d["block_table"], d["kv_len"], d["cu_q"], None, d["w_kvb"], SCALE, w,
+                                   workspace=ws)
+        torch.cuda.synchronize()
+        return w, mla.mla_attn_get_status(ws)
+
+    want, status = run()
+    assert status == 0
+    path = build_test_variant("wait_long_weights", "key_weights.cu", ["-DMLA_WAIT_LIMIT_NS=200000ull"])
+    got, status = _with(path, ("mla_latent_key_weights",), run)
+    assert status == 0 and torch.equal(got, want)
+
+
 def test_compaction_wait_gives_up():
     n, page = 4000, 64
     pages = -(-n // page)
