@@ -238,7 +238,8 @@ def _ptr(t):
 
 def _check(t, name, dtype, shape, device):
     try:  # the usual case, in few steps
-        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        if (t.dtype is dtype and t.get_device() == device.index and t.shape == shape
+                and t.is_contiguous()):
             return
     except AttributeError:
         pass
@@ -679,9 +680,9 @@ def mla_latent_key_weights(q_nope, q_pe, c_pages, pe_pages, block_table, kv_len,
     The arguments are those of mla_latent_tree_fwd (the tokens' rows appended); weights [num_pages,
     page_size] float32, one per slot, updated in place: a cached key's is multiplied by ``decay``
     and goes on from there (0: whatever it held), a new token's begins.  Returns weights."""
-    dev = q_nope.device
-    if dev.type != "cuda":
+    if not q_nope.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
+    dev = q_nope.device
     T, H = q_nope.shape[:2]
     num_pages, page_size = c_pages.shape[:2]
     B, max_pages = block_table.shape
@@ -724,9 +725,9 @@ def mla_paged_evict(weights, block_table, kv_len, budget, sinks: int = 0, recent
     max_keep: columns of ``kept`` (default: what the table can hold), at least every kept_len.
     ``out``: a PagedEviction (or a tuple like it) to fill instead of new tensors; entries of its
     ``freed`` behind n_freed are left as they were."""
-    dev = weights.device
-    if dev.type != "cuda":
+    if not weights.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
+    dev = weights.device
     i32 = torch.int32
     num_pages, page_size = weights.shape
     B, max_pages = block_table.shape
@@ -760,9 +761,9 @@ def mla_latent_compact(c_pages, pe_pages, block_table, kept, kept_len, weights=N
     c_pages [num_pages, page_size, 512], pe_pages [num_pages, page_size, 64] (bf16), weights
     [num_pages, page_size] (float32) or None; block_table [B, max_pages], kept [B, K], rising as
     mla_paged_evict lists it, kept_len [B] (int32)."""
-    dev = c_pages.device
-    if dev.type != "cuda":
+    if not c_pages.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
+    dev = c_pages.device
     num_pages, page_size = c_pages.shape[:2]
     B, max_pages = block_table.shape
     K = kept.shape[-1]
@@ -808,23 +809,22 @@ _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 
 
-def _row_steps(t, name, shape, device):
-    """(row, head) strides of a [T, R] or [T, H, R] tensor whose last dimension is contiguous."""
+def _row_steps(t, name, shape, index):
+    """Strides of a [T, R] or [T, H, R] tensor whose last dimension is contiguous."""
     try:  # the usual case, in few steps
-        st = t.stride()
-        if t.shape != shape or t.get_device() != device.index or st[-1] != 1:
-            st = None
+        if t.shape == shape and t.get_device() == index:
+            st = t.stride()
+            if st[-1] == 1:
+                return st
     except AttributeError:
-        st = None
-    if st is None:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-        raise ValueError(f"{name}: the last dimension must be contiguous, got strides {t.stride()}")
-    return st[0], st[1] if len(shape) == 3 else 0
+        pass
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name}: the last dimension must be contiguous, got strides {t.stride()}")
 
 
 def mla_rope_apply(x, positions, rope_table, layout: str = "half",
@@ -837,32 +837,36 @@ def mla_rope_apply(x, positions, rope_table, layout: str = "half",
     layout, out_layout (default: layout): "half" pairs columns d and d + R/2, "interleaved" 2d and
     2d + 1.  inverse turns back; the gradient of a call is the inverse call on y's gradient with
     the layouts exchanged.  ``out``: written instead of a new tensor; may be x itself."""
-    dev = x.device
-    if dev.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x must be [T, H, R] or [T, R], got {tuple(x.shape)}")
-    kind = _TYPES.get(x.dtype)
-    if kind is None:
-        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    to = layout if out_layout is None else out_layout
-    if layout not in _LAYOUTS or to not in _LAYOUTS:
-        raise ValueError(f"layouts are 'half' and 'interleaved', got {layout!r} and {to!r}")
-    shape = x.shape
-    T, R = shape[0], shape[-1]
-    H = shape[1] if len(shape) == 3 else 1
-    x_row, x_head = _row_steps(x, "x", shape, dev)
+    dev, shape, kind = x.device, x.shape, x.dtype
+    index = dev.index
+    if len(shape) == 3:
+        T, H, R = shape
+    elif len(shape) == 2:
+        (T, R), H = shape, 1
+    else:
+        raise ValueError(f"x must be [T, H, R] or [T, R], got {tuple(shape)}")
+    code = _TYPES.get(kind)
+    if code is None:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {kind}")
+    from_layout = _LAYOUTS.get(layout)
+    to_layout = from_layout if out_layout is None else _LAYOUTS.get(out_layout)
+    if from_layout is None or to_layout is None:
+        raise ValueError(f"layouts are 'half' and 'interleaved', got {layout!r} and {out_layout!r}")
+    sx = _row_steps(x, "x", shape, index)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
-    elif out.dtype is not x.dtype:
-        raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
-    y_row, y_head = _row_steps(out, "out", shape, dev)
+        out = torch.empty(shape, dtype=kind, device=dev)
+    elif out.dtype is not kind:
+        raise TypeError(f"out must be {kind}, got {out.dtype}")
+    sy = sx if out is x else _row_steps(out, "out", shape, index)
     rows = rope_table.shape[0]
     _check(rope_table, "rope_table", torch.float32, (rows, R), dev)
     _check(positions, "positions", torch.int32, (T,), dev)
+    x_head, y_head = (sx[1], sy[1]) if len(shape) == 3 else (0, 0)
     _enqueue("mla_rope_apply", dev, stream, workspace, 256, (
-        x.data_ptr(), x_row, x_head, out.data_ptr(), y_row, y_head, kind, T, H, R,
-        positions.data_ptr(), rope_table.data_ptr(), rows, _LAYOUTS[layout], _LAYOUTS[to],
+        x.data_ptr(), sx[0], x_head, out.data_ptr(), sy[0], y_head, code, T, H, R,
+        positions.data_ptr(), rope_table.data_ptr(), rows, from_layout, to_layout,
         1 if inverse else 0))
     return out
 
