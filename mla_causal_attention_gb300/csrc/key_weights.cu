@@ -171,6 +171,10 @@ namespace stats {
 constexpr int kAhead = 1;        // tiles between a tile's L2 prefetch and its loads (2: trees 105 us, 1: 102)
 constexpr int kOffQ = 0;                       // 17 sub-tiles: q_lat's two parts, q_pe
 constexpr int kOffK = kOffQ + 17 * kSub64;     // 9 sub-tiles: latent columns, rotary key
+constexpr int kGroup = 3 * kSub64;             // what a barrier stands for
+constexpr int kMorePlaces = 5;                 // of such groups, two of them behind 32 rows of queries
+constexpr int kOffMore = kOffK - 2 * kGroup;
+static_assert(kOffMore >= kOffQ + 18 * kSub64 / 2, "64 rows are read at the last 32");
 constexpr int kOffRed = kOffK + 9 * kSub64;    // [64 rows] (maximum, sum) of the upper keys
 constexpr int kOffBar = kOffRed + 512;
 constexpr int kSmem = kOffBar + 256 + 1024;    // + barriers + alignment slack
@@ -181,8 +185,8 @@ constexpr uint32_t kTmemCols = 128;            // two score tiles, 64 columns ea
 struct Bars {
   uint64_t q_full;      // even: the segment's queries landed in both CTAs
   uint64_t q_empty;     // the segment's last score MMA has read them
-  uint64_t k_full[3];   // even: sub-tiles 3 g .. 3 g + 2 of the keys landed in both CTAs
-  uint64_t k_empty[3];
+  uint64_t k_full[kMorePlaces];   // even: three sub-tiles of keys landed in both CTAs
+  uint64_t k_empty[kMorePlaces];
   uint64_t s_full[2];   // scores of a tile in TMEM
   uint64_t s_free[2];   // even: the scores have been read (8 warps)
   uint32_t tmem_base;
@@ -195,6 +199,14 @@ __device__ __forceinline__ int rows_first(const TreeArgs& a, const Seg& g) {
   return g.s.n * a.H - g.m * kRows <= 64 ? 32 : 64;
 }
 
+// Places of key groups.
+__device__ __forceinline__ int places(const TreeArgs& a, const Seg& g) {
+  return g.s.n * a.H <= 64 ? kMorePlaces : 3;
+}
+__device__ __forceinline__ int place_at(int at) {
+  return at < 3 ? kOffK + at * kGroup : kOffMore + (at - 3) * kGroup;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     row_stats_kernel(const __grid_constant__ KeyParams p) {
   namespace tp = tc::pair;
@@ -203,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   uint8_t* sQ = smem + kOffQ;
-  uint8_t* sK = smem + kOffK;
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
   volatile int* abort_flag = &bars->abort_flag;
   const TreeArgs& a = p.a.t;
@@ -215,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 2);
     mbar_init(&bars->q_empty, 1);
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kMorePlaces; ++i) {
       mbar_init(&bars->k_full[i], 2);
       mbar_init(&bars->k_empty[i], 1);
     }
@@ -253,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ================= keys and queries =================
     const uint32_t q_full = tp::even_addr(&bars->q_full);
     const uint32_t k_full = tp::even_addr(&bars->k_full[0]);
-    uint32_t t = 0;  // tiles over the run
-    int ns = 0;      // segments
+    uint32_t phase = 0;  // bit per place
+    int ns = 0;          // segments
     bool ok = true;
     for (; ok && more; g = after) {
       const auto look = [&](int tile) {  // lane q: the row of box q of this CTA's half
@@ -269,16 +280,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const int q_row = g.s.q0 * a.H + g.m * kRows + rows_first(a, g) * rank;
+      const int ring = places(a, g);
+      const int sub_q = ring == 3 ? kSub64 : kSub64 / 2;
       if (tc::elect_one()) {
-        tp::arrive_expect_tx(q_full, 17 * kSub64);
+        const CUtensorMap* ql = ring == 3 ? &p.tm_q64 : &p.tm_q32;
+        tp::arrive_expect_tx(q_full, 17 * sub_q);
 #pragma unroll 1
-        for (int s = 0; s < 16; ++s)
-          tp::tma_load_3d(sQ + s * kSub64, &p.tm_q64, q_full, 64 * s, q_row, 0);
-        tp::tma_load_3d(sQ + 16 * kSub64, &p.tm_qr64, q_full, 0, q_row, 0);
+        for (int s = 0; s < 16; ++s) tp::tma_load_3d(sQ + s * sub_q, ql, q_full, 64 * s, q_row, 0);
+        tp::tma_load_3d(sQ + 16 * sub_q, ring == 3 ? &p.tm_qr64 : &p.tm_qr32, q_full, 0, q_row, 0);
       }
       __syncwarp();
       ++ns;
-      for (int k = g.k0; k < g.k1 && ok; ++k, ++t) {
+      int at = 0;  // place
+      for (int k = g.k0; k < g.k1 && ok; ++k) {
         const int rows = rows_next;
         if (k + 1 < g.k1) rows_next = look(k + 1);
         if (k == g.k0) more = walk.next(a, after);
@@ -288,12 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int q = 0; q < 4; ++q) row[q] = __shfl_sync(0xffffffffu, rows, q);
 #pragma unroll 1
         for (int grp = 0; grp < 3; ++grp) {
-          if (t > 0) ok = mbar_wait(&bars->k_empty[grp], (t - 1) & 1, status, abort_flag);
+          ok = mbar_wait(&bars->k_empty[at], ~(phase >> at) & 1, status, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (tc::elect_one()) {
-            const uint32_t bar = k_full + 8 * grp;
-            uint8_t* dst = sK + 3 * grp * kSub64;
+            const uint32_t bar = k_full + 8 * at;
+            uint8_t* dst = smem + place_at(at);
             const CUtensorMap* last = grp < 2 ? &p.tm_c : &p.tm_kr;
             const int col = 192 * grp;
             tp::arrive_expect_tx(bar, 3 * nb * box * 128);
@@ -307,6 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               }
           }
           __syncwarp();
+          phase ^= 1u << at;
+          at = at + 1 < ring ? at + 1 : 0;
         }
         if (ask && k + kAhead < g.k1) {
           if (lane < boxes_of(g.s.kv - (k + kAhead) * kTile - 64 * rank, 64, box) && ahead < pool) {
@@ -321,12 +337,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ================= score MMAs =================
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, false);
     const uint64_t d_k = tc::smem_desc_sw128(0, 16, 1024);  // K-major
-    const uint32_t q_lo = smem_u32(sQ) >> 4, k_lo = smem_u32(sK) >> 4;
-    uint32_t t = 0;  // tiles over the run
-    int ns = 0;      // segments
+    const uint32_t q_lo = smem_u32(sQ) >> 4;
+    uint32_t t = 0;      // tiles over the run
+    uint32_t phase = 0;  // bit per place
+    int ns = 0;          // segments
     bool ok = true;
     for (; ok && more; g = after) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, ns & 1, status, abort_flag));
+      const int ring = places(a, g);
+      const uint32_t sub_q = (ring == 3 ? kSub64 : kSub64 / 2) >> 4;
+      int at = 0;
       for (int k = g.k0; k < g.k1 && ok; ++k, ++t) {
         // The score tile to be overwritten, that of tile t - 2, has been read.
         if (t > 1) ok = mbar_wait(&bars->s_free[t & 1], ((t >> 1) - 1) & 1, status, abort_flag);
@@ -334,28 +354,31 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const bool last = k + 1 == g.k1;
 #pragma unroll 1
         for (int grp = 0; grp < 3; ++grp) {
-          ok = ok && mbar_wait(&bars->k_full[grp], t & 1, status, abort_flag);
+          ok = ok && mbar_wait(&bars->k_full[at], (phase >> at) & 1, status, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc::fence_after_sync();
+          const uint32_t k_lo = smem_u32(smem + place_at(at)) >> 4;
           if (tc::elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 12; ++kk) {
               const int sub = 3 * grp + (kk >> 2);
-              const uint64_t kd = d_k | (uint64_t)(k_lo + sub * (kSub64 >> 4) + (kk & 3) * 2);
+              const uint64_t kd = d_k | (uint64_t)(k_lo + (kk >> 2) * (kSub64 >> 4) + (kk & 3) * 2);
               // latent columns against both parts; the rotary key, the ninth, against q_pe
-              const uint32_t q_at = q_lo + (sub < 8 ? sub : 16) * (kSub64 >> 4) + (kk & 3) * 2;
+              const uint32_t q_at = q_lo + (sub < 8 ? sub : 16) * sub_q + (kk & 3) * 2;
               tp::mma_ss(d, d_k | (uint64_t)q_at, kd, kIdS, (grp | kk) != 0 ? 1u : 0u);
               if (sub < 8)
-                tp::mma_ss(d, d_k | (uint64_t)(q_at + 8 * (kSub64 >> 4)), kd, kIdS, 1u);
+                tp::mma_ss(d, d_k | (uint64_t)(q_at + 8 * sub_q), kd, kIdS, 1u);
             }
-            tp::commit_both(&bars->k_empty[grp]);
+            tp::commit_both(&bars->k_empty[at]);
             if (grp == 2) {
               if (last) tp::commit_both(&bars->q_empty);
               tp::commit_both(&bars->s_full[t & 1]);
             }
           }
           __syncwarp();
+          phase ^= 1u << at;
+          at = at + 1 < ring ? at + 1 : 0;
         }
         if (k == g.k0) more = walk.next(a, after);
       }
@@ -363,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     // The releases that no one has waited for have arrived before this CTA leaves.
     if (ok && t > 0) {
-      for (int grp = 0; grp < 3; ++grp)
-        mbar_wait(&bars->k_empty[grp], (t - 1) & 1, status, abort_flag);
+      for (int at = 0; at < kMorePlaces; ++at)
+        mbar_wait(&bars->k_empty[at], ~(phase >> at) & 1, status, abort_flag);
       mbar_wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
     }
   } else if (warp >= 4) {
