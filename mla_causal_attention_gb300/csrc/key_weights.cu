@@ -24,7 +24,8 @@
 //
 // row_stats: the tree attention's scores without its mix.  A pair holds 64 rows of queries in each
 //   CTA, 136 KB in the two parts, and streams the keys, 64 per CTA; S = Q K^T, M128 N128, every key
-//   sub-tile against both parts.  Thread = (row, half of the keys), running maximum and sum in
+//   sub-tile against both parts.  A sequence of up to 64 rows has 32 in each CTA, 68 KB, which leaves
+//   room for 120 KB of keys in flight instead of 72.  Thread = (row, half of the keys), running maximum and sum in
 //   registers.
 // key_sum: the other way round.  A pair holds 256 keys, 128 per CTA (144 KB), and streams the rows;
 //   S^T = K Q^T, M256 N128 (N64 for up to 64 rows), so that a thread has one key and adds up the
@@ -115,18 +116,25 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
                  "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
-// Eight words w[at ..] to p, in one store if the workspace is 32-byte aligned.
+// Eight words w[at ..] to p, in one store with an L2 policy if p is aligned.
 template <int N>
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[N], int at, bool wide) {
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[N], int at, bool wide,
+                                        uint64_t policy) {
   if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[at]),
-                 "r"(w[at + 1]), "r"(w[at + 2]), "r"(w[at + 3]), "r"(w[at + 4]), "r"(w[at + 5]),
-                 "r"(w[at + 6]), "r"(w[at + 7])
-                 : "memory");
+    asm volatile(
+        "st.global.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(p),
+        "r"(w[at]), "r"(w[at + 1]), "r"(w[at + 2]), "r"(w[at + 3]), "r"(w[at + 4]),
+        "r"(w[at + 5]), "r"(w[at + 6]), "r"(w[at + 7]), "l"(policy)
+        : "memory");
   } else {
     reinterpret_cast<uint4*>(p)[0] = make_uint4(w[at], w[at + 1], w[at + 2], w[at + 3]);
     reinterpret_cast<uint4*>(p)[1] = make_uint4(w[at + 4], w[at + 5], w[at + 6], w[at + 7]);
   }
+}
+
+// Whether rows of the store begin with a line of L2.
+__device__ __forceinline__ bool kept_lines(const KeyWeightsArgs& a) {
+  return (reinterpret_cast<uintptr_t>(a.store) & 127u) == 0;
 }
 
 // A CTA leaves once neither it nor its peer has anything in flight into its shared memory.  In the
@@ -169,6 +177,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 namespace stats {
 
 constexpr int kAhead = 1;        // tiles between a tile's L2 prefetch and its loads (2: trees 105 us, 1: 102)
+constexpr int kOnceRows = 96;    // up to so many rows a sequence's keys are soon dropped from L2
 constexpr int kOffQ = 0;                       // 17 sub-tiles: q_lat's two parts, q_pe
 constexpr int kOffK = kOffQ + 17 * kSub64;     // 9 sub-tiles: latent columns, rotary key
 constexpr int kGroup = 3 * kSub64;             // what a barrier stands for
@@ -199,7 +208,9 @@ __device__ __forceinline__ int rows_first(const TreeArgs& a, const Seg& g) {
   return g.s.n * a.H - g.m * kRows <= 64 ? 32 : 64;
 }
 
-// Places of key groups.
+// Places of key groups.  More are of use where HBM is the bound: rows of one unit that fill half of
+// it (decode batch 112.5 us -> 109.5).  A half unit next to full ones would run ahead of them,
+// who read the same keys (B = 64, 192 rows, 4000 keys: 192 us with three places, 198 with five).
 __device__ __forceinline__ int places(const TreeArgs& a, const Seg& g) {
   return g.s.n * a.H <= 64 ? kMorePlaces : 3;
 }
@@ -273,8 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                    ? key_row(a, g.b, g.s.kv, tile * kTile + 64 * rank + lane * box) : 0;
       };
       int rows_next = look(g.k0);
-      // Keys that few units read come from HBM, and are asked into L2 ahead of their loads.
-      const bool ask = g.s.n * a.H <= kKeptRows;
+      // Keys that few units read come from HBM, and are asked into L2 ahead of their loads.  With
+      // rows so few that HBM is the bound they are better read once and soon dropped, so
+      // that the scores stay (B = 64, 4000 keys, 16 rows: 81 us -> 72, 64 rows: 109 -> 102;
+      // 128 rows, bound by their MMAs, 121 the first way, 123 the second).
+      const bool once = g.s.n * a.H <= kOnceRows;
+      const bool ask = !once && g.s.n * a.H <= kKeptRows;
+      const uint64_t policy = once ? l2_policy_evict_first() : l2_policy_evict_normal();
       int ahead = ask && g.k0 + kAhead < g.k1 ? look(g.k0 + kAhead) : 0;
       if (ns > 0) ok = mbar_wait(&bars->q_empty, (ns - 1) & 1, status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
@@ -315,9 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int q = 0; q < 4; ++q)
               if (q < nb) {
                 uint8_t* to = dst + q * box * 128;
-                tp::tma_load_3d(to, &p.tm_c, bar, col, row[q], 0);
-                tp::tma_load_3d(to + kSub64, &p.tm_c, bar, col + 64, row[q], 0);
-                tp::tma_load_3d(to + 2 * kSub64, last, bar, grp < 2 ? col + 128 : 0, row[q], 0);
+                tp::tma_load_3d_hint(to, &p.tm_c, bar, col, row[q], 0, policy);
+                tp::tma_load_3d_hint(to + kSub64, &p.tm_c, bar, col + 64, row[q], 0, policy);
+                tp::tma_load_3d_hint(to + 2 * kSub64, last, bar, grp < 2 ? col + 128 : 0, row[q], 0,
+                                     policy);
               }
           }
           __syncwarp();
@@ -399,9 +416,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     float2* red = reinterpret_cast<float2*>(smem + kOffRed);
     const uint32_t s_free = tp::even_addr(&bars->s_free[0]);
     const float sl2 = a.scale_log2;
+    // Scores stay in L2 until they are read; key_read_kernel lifts it again, line by line, so that
+    // nothing of it is left behind the call (decode batch 108 us without, 103 with).
+    const uint64_t stay = l2_policy_evict_last();
+    const bool wide = kept_lines(p.a);
     // What a slot holds, for the merge: first row, rows, whether it is its unit's first segment
     // and its last.  One thread clears the pair's two notes and fills in those of its segments.
-    const bool wide = (reinterpret_cast<uintptr_t>(p.a.store) & 31u) == 0;
     const bool notes = rank == 0 && threadIdx.x == 128;
     if (notes) {
       a.part_note[2 * pair_id] = make_int4(0, 0, 0, 0);
@@ -451,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) store32(to + 32 * c + e, x[c], e, wide);
+            for (int e = 0; e < 32; e += 8) store32(to + 32 * c + e, x[c], e, wide, stay);
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -583,6 +603,7 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
   grid_dep_wait();
   const int64_t tiles = a.steps.read0[a.t.B];
   const float sl2 = a.t.scale_log2;
+  const bool lines = kept_lines(a);
   // An equal run of tiles for every block, mostly of one sequence, which it looks up once.
   const int64_t x0 = tiles * blockIdx.x / gridDim.x, x1 = tiles * (blockIdx.x + 1) / gridDim.x;
   int64_t base = 0, next = -1;
@@ -654,7 +675,9 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
         L[e] = INFINITY;
         v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows) {
-          v[e] = __ldcs(reinterpret_cast<const float4*>(at(r)));
+          const float* from = at(r);
+          v[e] = __ldcs(reinterpret_cast<const float4*>(from));
+          if (lines && lane % 8 == 0) l2_evict_normal(from);
           L[e] = lse[r];
         }
       }
