@@ -658,33 +658,31 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
     const int slot = mine ? key_row(a.t, b, s.kv, key) : 0;
     const bool writes = mine && slot < a.t.num_pages << a.t.page_shift;
     const float held = writes && key < s.ctx && a.decay != 0.f ? a.weights[slot] : 0.f;
-    // Row r is in unit r / 128, whose rows of a tile lie together.
-    const auto at = [&](int r) {
-      const int m = r / kRows, unit_rows = min(kRows, rows - m * kRows);
-      return store + ((int64_t)m * kRows * K + (int64_t)k * unit_rows + (r - m * kRows)) * kTile +
-             4 * lane;
-    };
     // Sums in two parts (see key_sum_kernel).
     float total[4] = {}, dropped[4] = {};
     for (int r0 = warp; r0 < rows; r0 += 8 * kDeep) {
+      // The 64 rows of a round are in one unit, whose rows of a tile lie together.
+      const int m = r0 / kRows, unit_rows = min(kRows, rows - m * kRows);
+      const float* from =
+          store + ((int64_t)m * kRows * K + (int64_t)k * unit_rows + (r0 - m * kRows)) * kTile +
+          4 * lane;
+      const float* of = lse + r0;
       float4 v[kDeep];
       float L[kDeep];
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
-        const int r = r0 + 8 * e;
         L[e] = INFINITY;
         v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-          const float* from = at(r);
-          v[e] = __ldcs(reinterpret_cast<const float4*>(from));
-          if (lines && lane % 8 == 0) l2_evict_normal(from);
-          L[e] = lse[r];
+        if (r0 + 8 * e < rows) {
+          v[e] = __ldcs(reinterpret_cast<const float4*>(from + 8 * e * kTile));
+          if (lines && lane % 8 == 0) l2_evict_normal(from + 8 * e * kTile);
+          L[e] = of[8 * e];
         }
       }
+      // A row that is not there, or that sees nothing (L infinite, its scores -inf), adds 2^-inf = 0.
       float got[4] = {};
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
-        if (L[e] == INFINITY) continue;  // behind the last row, or a row that sees nothing
         got[0] += ex2_approx(fmaf(v[e].x, sl2, -L[e]));
         got[1] += ex2_approx(fmaf(v[e].y, sl2, -L[e]));
         got[2] += ex2_approx(fmaf(v[e].z, sl2, -L[e]));
