@@ -283,8 +283,8 @@ __device__ __forceinline__ int row_tiles(const TreeArgs& a, const TreeSeq& s) {
 }
 
 // Floats that a sequence's scores take if they are kept: rows x whole tiles of 128 keys.  Those of many
-// rows are computed again.  Kept and computed again, us: 64 sequences of 4000 keys and 64 rows 106,
-// 148; 128 rows 127, 149; 256 rows 213, 230; 16 of 512 rows 121, 119, 8 of 512 rows on 1000 keys 39,
+// rows are computed again.  Kept and computed again, us: 64 sequences of 4000 keys and 64 rows 88,
+// 148; 128 rows 124, 149; 256 rows 210, 230; 16 of 512 rows 121, 119, 8 of 512 rows on 1000 keys 37,
 // 47; 4 of 1024 rows 73, 72; one of 4096 rows 119, 72.
 __device__ __forceinline__ int64_t store_size(const TreeArgs& a, const TreeSeq& s) {
   const int64_t rows = (int64_t)s.n * a.H;

@@ -203,6 +203,23 @@ def test_scores_of_some_sequences_are_kept():
     check(e, 0.0)
 
 
+@pytest.mark.parametrize("at", [16, 32, 64, 128])
+@pytest.mark.parametrize("n", [(1, 1), (1, 9)])
+def test_a_workspace_that_begins_anywhere(n, at):
+    """16-byte alignment is enough; the kept scores' rows begin with a line of L2 or they do not.
+    With 32 heads and 1 to 9 tokens a pair goes from sequences of half a unit to full ones and back."""
+    d = tree_case(21, 200, 32, (1, 700), n, 16, False)
+    old = torch.rand(d["c_pages"].shape[:2], device="cuda")
+    want = check(d, 0.5, old=old)
+    T, H = d["q_nope"].shape[:2]
+    B, pages = d["block_table"].shape
+    size = mla.binding.library().mla_latent_key_weights_workspace_bytes(T, H, B, pages * 16)
+    ws = mla.Workspace("cuda:0")
+    ws.buf = torch.zeros(size + at, dtype=torch.uint8, device="cuda")[at:]
+    assert torch.equal(call(d, old, 0.5, workspace=ws), want)
+    assert mla.mla_attn_get_status(ws) == 0
+
+
 def test_pool_past_4_gb():
     """The pages of one sequence at the far end of a pool of 5 million rows."""
     d = tree_case(14, 1, 16, (300, 300), (2, 2), 64, False)
