@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       int rows_next = look(g.k0);
       // Keys that few units read come from HBM, and are asked into L2 ahead of their loads.  With
       // rows so few that HBM is the bound they are better read once and soon dropped, so
-      // that the scores stay (B = 64, 4000 keys, 16 rows: 81 us -> 72, 64 rows: 109 -> 102;
-      // 128 rows, bound by their MMAs, 121 the first way, 123 the second).
+      // that the scores stay (64 sequences of 4000 keys, 16 rows: 81 us -> 72; 64 rows on U[512, 8192]
+      // keys: 109 -> 102; 128 rows, bound by their MMAs: 121 the first way, 123 the second).
       const bool once = g.s.n * a.H <= kOnceRows;
       const bool ask = !once && g.s.n * a.H <= kKeptRows;
       const uint64_t policy = once ? l2_policy_evict_first() : l2_policy_evict_normal();
