@@ -25,8 +25,8 @@
 // row_stats: the tree attention's scores without its mix.  A pair holds 64 rows of queries in each
 //   CTA, 136 KB in the two parts, and streams the keys, 64 per CTA; S = Q K^T, M128 N128, every key
 //   sub-tile against both parts.  A sequence of up to 64 rows has 32 in each CTA, 68 KB, which leaves
-//   room for 120 KB of keys in flight instead of 72.  Thread = (row, half of the keys), running maximum and sum in
-//   registers.
+//   room for 120 KB of keys in flight instead of 72.  Thread = (row, half of the keys), running
+//   maximum and sum in registers.
 // key_sum: the other way round.  A pair holds 256 keys, 128 per CTA (144 KB), and streams the rows;
 //   S^T = K Q^T, M256 N128 (N64 for up to 64 rows), so that a thread has one key and adds up the
 //   weights of the tile's rows: no sum crosses threads.  M256 halves what is streamed per
