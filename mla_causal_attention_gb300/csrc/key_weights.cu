@@ -654,12 +654,14 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
     }
     const int k = (int)(x - base);
     const int key = k * kTile + (int)threadIdx.x;
+    const bool some_hidden = (k + 1) * kTile > s.ctx;  // the tile holds new tokens
     const bool mine = threadIdx.x < kTile && key < s.kv;
     const int slot = mine ? key_row(a.t, b, s.kv, key) : 0;
     const bool writes = mine && slot < a.t.num_pages << a.t.page_shift;
     const float held = writes && key < s.ctx && a.decay != 0.f ? a.weights[slot] : 0.f;
     // Sums in two parts (see key_sum_kernel).
     float total[4] = {}, dropped[4] = {};
+    bool no_number = false;
     for (int r0 = warp; r0 < rows; r0 += 8 * kDeep) {
       // The 64 rows of a round are in one unit, whose rows of a tile lie together.
       const int m = r0 / kRows, unit_rows = min(kRows, rows - m * kRows);
@@ -681,6 +683,15 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
       }
       // A row that is not there, or that sees nothing (L infinite, its scores -inf), adds 2^-inf = 0.
       float got[4] = {};
+      if (some_hidden) {  // a row without an L would spoil the keys that it hides: it comes below
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e)
+          if (L[e] != L[e]) {
+            no_number = true;
+            L[e] = INFINITY;
+            v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+      }
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
         got[0] += ex2_approx(fmaf(v[e].x, sl2, -L[e]));
@@ -693,6 +704,21 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
         const float y = got[c] - dropped[c], sum = total[c] + y;
         dropped[c] = (sum - total[c]) - y;
         total[c] = sum;
+      }
+    }
+    if (no_number) {
+      // Rows that see a key that is no number have no L: what they see gets no number, what they
+      // do not see nothing.
+      const bool masked = a.t.draft_mask != nullptr;
+#pragma unroll 1
+      for (int r = warp; r < rows; r += 8) {
+        if (lse[r] == lse[r]) continue;
+        const int i = r / a.t.H;  // new token
+        const uint64_t mask = masked ? (uint64_t)a.t.draft_mask[s.q0 + i] : 0ull;
+        const uint64_t seen = seen_bits(k * kTile + 4 * lane, s.ctx, s.kv, masked, mask, i);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if ((seen >> c) & 1u) total[c] = lse[r];
       }
     }
     *reinterpret_cast<float4*>(&part[warp][4 * lane]) =
