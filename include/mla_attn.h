@@ -572,8 +572,9 @@ MLA_API mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t
  * more than the cached length: mla_paged_plan's positions count from the cached length, so a
  * server adds what it has dropped.
  *
- * K at least every min(kv_len[b], budget[b]), B up to 65535, max_pages * page_size and B * max_pages
- * below 2^31; no output may overlap an input or another output (MLA_ERR_ARG, as for negative sinks or recent).
+ * K at least every min(kv_len[b], budget[b]); K and max_pages * page_size up to 2^30, B up to 65535,
+ * B * max_pages below 2^31; no output may overlap an input or another output (MLA_ERR_ARG, as for
+ * negative sinks or recent).
  * Device-side problems (the call completes): a length outside the table, a budget below zero or more
  * rows to keep than K (MLA_ERR_KVLEN, clamped); a page outside the pool (MLA_ERR_PAGE: its rows
  * count as lowest).  workspace: 256 bytes (the status word), zeroed once.

@@ -20,6 +20,8 @@ namespace {
 constexpr size_t kStatusBytes = 256;  // status word + padding at the start of the workspace
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
+// Rows of a sequence or a list of them in evict.cu, whose loops go up to 2^15 past the last in 32 bits.
+constexpr int64_t kMaxRows = int64_t(1) << 30;
 
 // 0 = unknown, 1 = sm_103, 2 = other.  Per device, filled on first use.
 std::atomic<int> g_dev_kind[kMaxDevices];
@@ -990,8 +992,9 @@ mla_status mla_paged_evict(const float* weights, int num_pages, int page_size,
   if (!workspace) return MLA_ERR_WORKSPACE;
   const mla_status ps = check_pool(num_pages, page_size);
   if (ps != MLA_OK) return ps;
-  if (B < 1 || B > 65535 || K < 1 || max_pages < 1 || (int64_t)max_pages * page_size > 0x7fffffff ||
-      (int64_t)B * K > kMaxElems || (int64_t)B * max_pages > 0x7fffffff)
+  if (B < 1 || B > 65535 || K < 1 || K > kMaxRows || max_pages < 1 ||
+      (int64_t)max_pages * page_size > kMaxRows || (int64_t)B * K > kMaxElems ||
+      (int64_t)B * max_pages > 0x7fffffff)
     return MLA_ERR_SHAPE;
   if (sinks < 0 || recent < 0) return MLA_ERR_ARG;
   const void* words[] = {weights, block_table, kv_len, budget, kept, kept_len, freed, n_freed};
