@@ -595,7 +595,8 @@ MLA_API mla_status mla_paged_evict(const float* weights, int num_pages, int page
  *
  * kept [B, K] int32, each row rising, as mla_paged_evict lists it (any rising list of rows will
  * do); kept_len [B].  The sequences of a call have pages of their own: a page that two of them
- * name is moved by both at once, and holds some mixture.  B up to 65535, B * K up to 2^35.
+ * name is moved by both at once, and holds some mixture.  K and max_pages * page_size up to 2^30, B
+ * up to 65535, B * K up to 2^35.
  * Device-side problems (the call completes): kept_len outside [0, K] (MLA_ERR_KVLEN, clamped); an
  * entry below its own index or past the table (MLA_ERR_KVLEN), or a page outside the pool
  * (MLA_ERR_PAGE): that row is not moved.  A list that does not rise moves rows that others have

@@ -1040,8 +1040,8 @@ mla_status mla_latent_compact(uint16_t* c_pages, uint16_t* pe_pages, float* weig
   if (!workspace) return MLA_ERR_WORKSPACE;
   const mla_status ps = check_pool(num_pages, page_size);
   if (ps != MLA_OK) return ps;
-  if (B < 1 || B > 65535 || K < 1 || max_pages < 1 || (int64_t)max_pages * page_size > 0x7fffffff ||
-      (int64_t)B * K > (int64_t(1) << 35))
+  if (B < 1 || B > 65535 || K < 1 || K > kMaxRows || max_pages < 1 ||
+      (int64_t)max_pages * page_size > kMaxRows || (int64_t)B * K > (int64_t(1) << 35))
     return MLA_ERR_SHAPE;
   const void* words[] = {weights, block_table, kept, kept_len};
   for (const void* w : words)

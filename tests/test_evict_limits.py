@@ -32,3 +32,22 @@ def test_evict_takes_as_many_as_it_can(lib, base):  # noqa: F811
     a.update(B=1, freed=None, n_freed=None, block_table=base + (1 << 41), K=MOST,
              max_pages=MOST // 16)
     assert _accepted(lib.mla_paged_evict(*[a[n] for n in EVICT]))
+
+
+@pytest.mark.parametrize("change", [
+    {"K": MOST + 1}, {"K": (1 << 31) - 1}, {"max_pages": MOST // 1024 + 1, "page_size": 1024},
+    {"max_pages": (1 << 27) - 1},
+])
+def test_compact_refuses_more_rows_than_it_can_number(lib, base, change):  # noqa: F811
+    a = _compact_args(base)
+    a.update(B=1, workspace_bytes=1 << 40)
+    a.update(change)
+    assert lib.mla_latent_compact(*[a[n] for n in COMPACT]) == S.ERR_SHAPE
+
+
+def test_compact_takes_as_many_as_it_can(lib, base):  # noqa: F811
+    if torch.cuda.is_available():
+        return
+    a = _compact_args(base)
+    a.update(B=1, workspace_bytes=1 << 40, K=MOST, max_pages=MOST // 16)
+    assert _accepted(lib.mla_latent_compact(*[a[n] for n in COMPACT]))
