@@ -291,10 +291,12 @@ __device__ __forceinline__ int64_t store_size(const TreeArgs& a, const TreeSeq& 
   return rows <= kKeptRows ? rows * seq_tiles(s) * kTile : 0;
 }
 
-// By one block of 256 threads: which sequences' scores are kept, in order as long as there is room;
-// the tiles and steps in front of each sequence; the counters cleared.
+// By one block of 256 threads: which sequences' scores are kept; the tiles and steps in front of each
+// sequence; the counters cleared.  The store is given out in the order of the sequences.  One that asks for
+// more than is left gets nothing and takes nothing from those behind it (63 requests of one token on
+// 4000 keys behind one of 8 tokens on 140000: 336 us if it did, 291; in front of it 292).
 static __device__ __noinline__ void key_steps(const TreeArgs& a, const KeySteps& k) {
-  __shared__ int64_t s_sum[3][8];
+  __shared__ int64_t s_sum[3][8], s_left;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < 2 * a.pairs; i += 256) k.count[i] = 0;
   // The sum of x over the threads before this one; all is the block's.
@@ -319,10 +321,17 @@ static __device__ __noinline__ void key_steps(const TreeArgs& a, const KeySteps&
     const int b = b0 + tid;
     TreeSeq s = {};
     if (b < a.B) s = tree_seq(a, b);
-    int64_t all;
-    const int64_t own = store_size(a, s), from = size + scan(own, 0, all);
+    const int64_t own = store_size(a, s);
+    int64_t all, from;
+    bool keep = own > 0;
+    for (;;) {
+      from = size + scan(keep ? own : 0, 0, all);
+      const bool over = keep && from + own > k.room;  // the first that does not fit, and all behind it
+      if (over && from <= k.room) s_left = k.room - from;  // the first
+      if (!__syncthreads_or(over)) break;
+      keep = keep && !(over && own > s_left);  // that one, and whatever is larger than what it found
+    }
     size += all;
-    const bool keep = own > 0 && from + own <= k.room;
     const int64_t t = keep ? seq_tiles(s) : 0;
     const int64_t w = keep ? 0 : (int64_t)key_tiles(s) * row_tiles(a, s);
     const int64_t t0 = tiles + scan(t, 1, all);

@@ -82,3 +82,86 @@ def test_rows_that_are_no_numbers_leave_alone_what_they_do_not_see(way, what, de
     assert bool(w[lost].isnan().all()) and not bool(w[~lost].isnan().any())
     close(w, e, old, decay, but=lost)
     assert mla.mla_attn_get_status() == 0
+
+
+# ---- the store of kept scores -----------------------------------------------------------
+
+ROOM = 1 << 26      # floats
+UNTOUCHED = 0x7fc12345  # no score has these bits
+
+
+def batch(seed, lens, new, H, page=64):
+    """Sequences of `lens` keys, `new` of them new tokens, on the device."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    held = [-(-n // page) for n in lens]
+    ids = torch.randperm(sum(held), generator=g, device="cuda").tolist()
+    table, at = [], 0
+    for h in held:
+        table.append(ids[at:at + h] + [-1] * (max(held) - h))
+        at += h
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    mk = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    return dict(q_nope=mk(cu[-1], H, 128), q_pe=mk(cu[-1], H, 64), c_pages=mk(at, page, 512),
+                pe_pages=mk(at, page, 64), block_table=i(table), kv_len=i(lens), cu_q=i(cu),
+                draft_mask=None, w_kvb=(mk(H * 256, 512) / 512 ** 0.5).bfloat16())
+
+
+def kept_floats(lens, new, H):
+    """In order, whoever finds room for its scores has it."""
+    left = ROOM
+    for n, k in zip(new, lens):
+        own = n * H * (-(-k // 128) * 128)
+        if n * H <= 512 and own <= left:
+            left -= own
+    return ROOM - left
+
+
+def store_used(d):
+    """Floats at the beginning of the store that a call writes (none behind them), and its weights."""
+    T, H = d["q_nope"].shape[:2]
+    B, width = d["block_table"].shape
+    page = d["c_pages"].shape[1]
+    ws = mla.Workspace("cuda:0")
+    size = mla.binding.library().mla_latent_key_weights_workspace_bytes(T, H, B, width * page)
+    ws.buf = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    store = ws.buf[size - 4 * ROOM:].view(torch.int32)
+    store.fill_(UNTOUCHED)
+    w = call(d, torch.zeros(d["c_pages"].shape[:2], device="cuda"), 0.0, workspace=ws)
+    assert mla.mla_attn_get_status(ws) == 0
+    written = store != UNTOUCHED
+    n = int(written.sum())
+    assert bool(written[:n].all())
+    return n, w
+
+
+@pytest.mark.parametrize("lens,new", [
+    ([131201, 1000, 300], [8, 8, 1]),         # one request whose scores are more than the store holds
+    ([1000, 300, 131201], [8, 1, 8]),         # the same, behind the others
+    ([100000, 40000, 20000, 900, 11100], [8] * 5),  # behind the first, the third fits and the fourth
+    ([131072, 100], [8, 1]),                  # all of it for one
+    ([5000, 131072, 700], [9, 7, 1]),         # rows that are not kept anyway take nothing
+])
+def test_requests_without_room_leave_it_to_those_behind(lens, new):
+    d = batch(len(lens), lens, new, 64)
+    n, w = store_used(d)
+    assert n == kept_floats(lens, new, 64)
+    sums = torch.stack([w.view(-1)[slots(d, b)].double().sum() for b in range(len(lens))])
+    for s, k in zip(sums.tolist(), new):
+        assert abs(s - 64 * k) <= 64 * k * 1e-4  # every row's weights sum to 1
+
+
+def test_many_requests_fill_the_store():
+    g = torch.Generator("cpu").manual_seed(3)
+    lens = torch.randint(4, 3001, (700,), generator=g).tolist()
+    new = torch.randint(0, 5, (700,), generator=g).tolist()
+    lens[5], new[5], lens[300], new[300] = 131500, 4, 140000, 4
+    d = batch(3, lens, new, 128)
+    n, w = store_used(d)
+    want = kept_floats(lens, new, 128)
+    assert n == want > ROOM - 128 * 128
+    for b in range(0, 700, 7):
+        s = float(w.view(-1)[slots(d, b)].double().sum())
+        assert abs(s - 128 * new[b]) <= 128 * new[b] * 1e-4
