@@ -568,11 +568,17 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream) {
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
   const int64_t most = (int64_t)a.max_pages << a.page_shift;
   // CTAs of a sequence: one for 4096 rows that the table allows, up to 8, or 16 for few sequences, and
-  // no more than the SMs take at once.  A barrier over a cluster takes 0.6 us and there are seven: 64
-  // sequences of up to 8192 rows take 13.8 us with a CTA for 2048 rows, 10.3 for 4096, 10.9 for 8192.
-  // Clusters of 16 find room only three at a time (8 of 30000 rows 65 us, 10 with 8 CTAs).
+  // no more than the SMs take at once: two of 512 threads, which hold up to 4096 rows each, or one of
+  // 1024 (70 sequences of a table of 32768 rows: 30 us with 4 CTAs of 1024 threads, two waves of them,
+  // 20 with 2; 100 of 16384 rows: 28 with 2, 17 with one).  A barrier over a cluster takes 0.6 us and
+  // there are six: 64 sequences of up to 8192 rows take 13.8 us with a CTA for 2048 rows, 10.3 for 4096,
+  // 10.9 for 8192.  Clusters of 16 find room only three at a time (8 of 30000 rows 65 us, 10 with 8 CTAs).
+  // It goes by the table's width, since the lengths are on the device: 64 sequences of 8192 rows take
+  // 10.8 us in a table that wide and 14.5 in one of 131072 rows.
   int C = 1;
-  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= 2 * sms && most > (int64_t)4096 * C) C *= 2;
+  const auto at_once = [&](int c) { return (int64_t)sms * (most <= (int64_t)4096 * c ? 2 : 1); };
+  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= at_once(2 * C) && most > (int64_t)4096 * C)
+    C *= 2;
   const int64_t per = (most + C - 1) / C;
   return per > 512 * kEvPer ? launch_evict<1024>(a, C, per, stream)
                             : launch_evict<512>(a, C, per, stream);

@@ -1,0 +1,33 @@
+"""The eviction's launch follows the table's width and the number of sequences: CTAs per sequence, threads
+per CTA, numbers held in registers, in shared memory or read again.  The choice is the same in all."""
+import random
+
+import pytest
+
+from test_evict import pages, run_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B,positions,most", [
+    (70, 32768, 9000),     # 2 CTAs of 1024 threads
+    (77, 16384, 16384),    # one of 1024, two rounds of rows
+    (152, 16384, 5000),
+    (100, 8192, 8192),     # 2 of 512
+    (152, 8192, 8192),
+    (153, 8192, 4097),     # one of 1024
+    (19, 32768, 20000),    # 8 of 512
+    (39, 32768, 32768),    # 2 of 1024
+    (38, 65536, 32768),    # 4 of 1024
+    (3, 65536, 65536),     # 16 of 512
+    (3, 131072, 70000),    # 16 of 1024
+    (64, 131072, 8192),    # a table far wider than the sequences
+    (1, 4096, 4096), (1, 4112, 4100),
+])
+@pytest.mark.parametrize("kind", ["plain", "odd"])
+def test_choice_in_every_launch(B, positions, most, kind):
+    r = random.Random(B + positions)
+    lens = [r.randint(0, most) for _ in range(B - 1)] + [most]
+    budgets = [r.randint(0, 1 + n) for n in lens]
+    wide = positions // 16 - max(pages(n, 16) for n in lens)
+    run_case(lens, budgets, 3, 17, 16, kind, B, K=max(1, max(map(min, lens, budgets))), extra=wide)
