@@ -59,7 +59,8 @@ __device__ __forceinline__ int peer_load(const int* p, uint32_t rank) {
 //
 // A cluster of CTAs per sequence, each with an equal run of the rows between and each warp with an
 // equal run of those; the histograms are added up through distributed shared memory.  The numbers
-// stay in registers for all passes, or, with more than 8 to a thread, in shared memory.  The work is 4
+// stay in registers for all passes, or, with more than 8 to a thread, in shared memory, and what that
+// does not hold is read again.  The work is 4
 // bytes per row: what bounds it is latency, of the loads through the block table and of the barriers
 // between the passes.
 constexpr int kEvPer = 8;        // rows of a thread at a time
@@ -121,10 +122,12 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
 }
 
 // kEvThreads: 512, two CTAs on an SM, or 1024 where a CTA's rows are more than the registers of 512 hold.
+constexpr int kFewThreads = 512, kManyThreads = 1024;
 template <int kEvThreads>
 __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
     paged_evict_kernel(const PagedEvictArgs a) {
   constexpr int kEvWarps = kEvThreads / 32;
+  constexpr bool kRounds = kEvThreads == kManyThreads;  // a thread may have more rows than registers
   extern __shared__ uint32_t keys[];  // numbers of each warp's first a.held rounds of rows
   __shared__ EvictSmem<kEvWarps> sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(kEvThreads, 1024 / kEvThreads)
     const int i0 = min(rank * per, mid), n = min(per, mid - i0);
     const int run = (((n + kEvWarps - 1) / kEvWarps) + 31) & ~31;
     const int w0 = min(warp * run, n), w1 = min(w0 + run, n);
-    const int rounds = (run + 32 * kEvPer - 1) / (32 * kEvPer);
+    const int rounds = kRounds ? (run + 32 * kEvPer - 1) / (32 * kEvPer) : 1;
     bool bad = false;
     // Rows w0 + lane + 32 (kEvPer round + e) of this thread, from the pool: the loads of a round at once.
     uint32_t v[kEvPer];
@@ -530,7 +533,8 @@ namespace {
 template <int kEvThreads>
 cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, cudaStream_t stream) {
   // Rounds of a warp's rows whose numbers are kept in shared memory: none where there is but one.
-  constexpr int kRound = kEvThreads * kEvPer, kMostHeld = 49152 / kRound;
+  constexpr int kRound = kEvThreads * kEvPer;
+  constexpr int kMostHeld = kEvThreads == kManyThreads ? 49152 / kRound : 0;
   const int64_t rounds = (per + kRound - 1) / kRound + 1;  // a warp's run is a multiple of 32 rows
   a.held = per <= kRound ? 0 : (int)std::min<int64_t>(rounds, kMostHeld);
   static std::atomic<uint64_t> attr_done{0};  // bit per device: attributes set
@@ -539,8 +543,9 @@ cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, cudaStream_t stre
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * kRound * 4);
+    if (kMostHeld > 0)
+      e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * kRound * 4);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -580,8 +585,8 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream) {
   while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= at_once(2 * C) && most > (int64_t)4096 * C)
     C *= 2;
   const int64_t per = (most + C - 1) / C;
-  return per > 512 * kEvPer ? launch_evict<1024>(a, C, per, stream)
-                            : launch_evict<512>(a, C, per, stream);
+  return per > kFewThreads * kEvPer ? launch_evict<kManyThreads>(a, C, per, stream)
+                                    : launch_evict<kFewThreads>(a, C, per, stream);
 }
 
 cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t stream) {
