@@ -530,63 +530,111 @@ __global__ void __launch_bounds__(32 * kCpWarps) latent_compact_kernel(const Lat
 
 namespace {
 
+// Numbers that a CTA keeps in shared memory at most; in rounds of its threads' registers.
+constexpr int kMostRows = 49152;
 template <int kEvThreads>
-cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, cudaStream_t stream) {
-  // Rounds of a warp's rows whose numbers are kept in shared memory: none where there is but one.
+constexpr int kMostHeld = kEvThreads == kManyThreads ? kMostRows / (kEvThreads * kEvPer) : 0;
+
+// A launch of B clusters of C CTAs; the attributes that it needs are set once per device.
+template <int kEvThreads>
+cudaError_t evict_config(int B, int C, int held, int dev, cudaLaunchAttribute* attr,
+                         cudaLaunchConfig_t* cfg) {
   constexpr int kRound = kEvThreads * kEvPer;
-  constexpr int kMostHeld = kEvThreads == kManyThreads ? 49152 / kRound : 0;
-  const int64_t rounds = (per + kRound - 1) / kRound + 1;  // a warp's run is a multiple of 32 rows
-  a.held = per <= kRound ? 0 : (int)std::min<int64_t>(rounds, kMostHeld);
   static std::atomic<uint64_t> attr_done{0};  // bit per device: attributes set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
-    if (kMostHeld > 0)
+    cudaError_t e = cudaSuccess;
+    if (kMostHeld<kEvThreads> > 0)
       e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * kRound * 4);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kMostHeld<kEvThreads> * kRound * 4);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_evict_kernel<kEvThreads>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_release);
   }
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = C;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  *cfg = {};
+  cfg->gridDim = dim3((unsigned)(B * C));
+  cfg->blockDim = dim3(kEvThreads);
+  cfg->dynamicSmemBytes = (size_t)held * kRound * 4;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+  return cudaSuccess;
+}
+
+// Clusters of 2^log_c CTAs that the device holds at once, or 0 if it does not say.
+template <int kEvThreads>
+int clusters_at_once(int log_c, int dev) {
+  static std::atomic<int> known[64][5] = {};
+  std::atomic<int>& k = known[dev & 63][log_c];
+  int n = k.load(std::memory_order_relaxed);
+  if (n > 0) return n;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * C));
-  cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = (size_t)a.held * kRound * 4;
+  cudaLaunchConfig_t cfg;
+  if (evict_config<kEvThreads>(1, 1 << log_c, kMostHeld<kEvThreads>, dev, attr, &cfg) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, paged_evict_kernel<kEvThreads>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  k.store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int kEvThreads>
+cudaError_t launch_evict(PagedEvictArgs a, int C, int64_t per, int dev, cudaStream_t stream) {
+  // Rounds of a warp's rows whose numbers are kept in shared memory: none where there is but one.
+  constexpr int kRound = kEvThreads * kEvPer;
+  const int64_t rounds = (per + kRound - 1) / kRound + 1;  // a warp's run is a multiple of 32 rows
+  a.held = per <= kRound ? 0 : (int)std::min<int64_t>(rounds, kMostHeld<kEvThreads>);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg;
+  const cudaError_t e = evict_config<kEvThreads>(a.B, C, a.held, dev, attr, &cfg);
+  if (e != cudaSuccess) return e;
   cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, paged_evict_kernel<kEvThreads>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream) {
-  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)a.max_pages << a.page_shift;
-  // CTAs of a sequence: one for 4096 rows that the table allows, up to 8, or 16 for few sequences, and
-  // no more than the SMs take at once: two of 512 threads, which hold up to 4096 rows each, or one of
-  // 1024 (70 sequences of a table of 32768 rows: 30 us with 4 CTAs of 1024 threads, two waves of them,
-  // 20 with 2; 100 of 16384 rows: 28 with 2, 17 with one).  A barrier over a cluster takes 0.6 us and
-  // there are six: 64 sequences of up to 8192 rows take 13.8 us with a CTA for 2048 rows, 10.3 for 4096,
-  // 10.9 for 8192.  Clusters of 16 find room only three at a time (8 of 30000 rows 65 us, 10 with 8 CTAs).
-  // It goes by the table's width, since the lengths are on the device: 64 sequences of 8192 rows take
-  // 10.8 us in a table that wide and 14.5 in one of 131072 rows.
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
+  // CTAs of a sequence: one for 4096 rows that the table allows, up to 8, or 16 for up to three sequences
+  // (eight or more of them would come in waves; four to seven of 524288 rows take 62 us with 8, 31 with
+  // 16, and with 65536 rows each 14.8, 12.6; shorter ones in such tables 14.2, 15.9).
+  // CTAs of 512 threads, two on an SM, hold that many rows in registers; for more they have 1024.  A
+  // barrier over a cluster takes 0.6 us and there are six: 64 sequences of up to 8192 rows take 13.8 us
+  // with a CTA for 2048 rows, 10.3 for 4096, 10.9 for 8192.
   int C = 1;
-  const auto at_once = [&](int c) { return (int64_t)sms * (most <= (int64_t)4096 * c ? 2 : 1); };
-  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= at_once(2 * C) && most > (int64_t)4096 * C)
-    C *= 2;
-  const int64_t per = (most + C - 1) / C;
-  return per > kFewThreads * kEvPer ? launch_evict<kManyThreads>(a, C, per, stream)
-                                    : launch_evict<kFewThreads>(a, C, per, stream);
+  while (C < (a.B <= 3 ? 16 : 8) && (int64_t)a.B * 2 * C <= 2 * sms && most > (int64_t)4096 * C) C *= 2;
+  // No more than the device holds at once, where fewer still have their rows' numbers in shared memory
+  // (what does not is read six times: 37 sequences of 262144 rows take 86 us with 8 CTAs each, three
+  // waves, 149 with 2 in one).  A cluster lies within a GPC, so of large ones there is less room
+  // than the SMs have: 152, 74, 36, 14 of 2, 4, 8, 16 CTAs of 512 threads, 76, 36, 15, 7 of 1024.  A
+  // second wave: 16 sequences of 65536 rows take 28 us with 8 CTAs each, 21 with 4; 70 of 32768 rows 30
+  // with 4, 20 with 2; 100 of 16384 rows 28 with 2, 17 with one.
+  const auto rows_of = [&](int c) { return (most + c - 1) / c; };
+  const auto at_once = [&](int c) {
+    int log_c = 0;
+    while ((1 << log_c) < c) ++log_c;
+    return rows_of(c) > kFewThreads * kEvPer ? clusters_at_once<kManyThreads>(log_c, dev)
+                                             : clusters_at_once<kFewThreads>(log_c, dev);
+  };
+  while (C > 1 && rows_of(C / 2) <= kMostRows && a.B > at_once(C)) C /= 2;
+  // All by the table's width, since the lengths are on the device: 64 sequences of 8192 rows take 10.8 us
+  // in a table that wide and 29 in one of 131072 rows.
+  const int64_t per = rows_of(C);
+  return per > kFewThreads * kEvPer ? launch_evict<kManyThreads>(a, C, per, dev, stream)
+                                    : launch_evict<kFewThreads>(a, C, per, dev, stream);
 }
 
 cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t stream) {

@@ -18,7 +18,9 @@ pytestmark = pytest.mark.gpu
     (153, 8192, 4097),     # one of 1024
     (19, 32768, 20000),    # 8 of 512
     (39, 32768, 32768),    # 2 of 1024
-    (38, 65536, 32768),    # 4 of 1024
+    (36, 65536, 32768),    # 4 of 1024
+    (38, 65536, 32768),    # 2 of 1024
+    (37, 262144, 20000),   # 8 of 1024, three waves
     (3, 65536, 65536),     # 16 of 512
     (3, 131072, 70000),    # 16 of 1024
     (64, 131072, 8192),    # a table far wider than the sequences
