@@ -565,6 +565,11 @@ MLA_API mla_status mla_latent_key_weights(const uint16_t* q_nope, const uint16_t
  *                        <= p < ceil(n / page_size), in order of b, then p, and their number;
  *                        freed [B * max_pages], entries from n_freed[0] on are left as they were
  *
+ * Freed pages are listed as the table has them.  A page that several sequences name (a shared prefix), or
+ * one sequence twice, comes up each time that it is past the kept rows, whoever still needs it: a server that
+ * shares pages counts their holders.  An entry outside the pool is listed too (and reported,
+ * MLA_ERR_PAGE): read the status before the list goes to those that are free.
+ *
  * Nothing is moved and the table is not changed: mla_latent_compact moves the rows, in every layer
  * whose pages the table names (a layer may keep other rows than the next, as long as it keeps as
  * many), and only then may the freed pages go to another sequence.  kept_len is then the

@@ -723,8 +723,10 @@ def mla_paged_evict(weights, block_table, kv_len, budget, sinks: int = 0, recent
     [B, max_pages], kv_len [B], budget [B] int32.  A sequence over its budget keeps its first
     ``sinks`` and last ``recent`` rows and the heaviest of the others, ties to the lower row.
     max_keep: columns of ``kept`` (default: what the table can hold), at least every kept_len.
-    ``out``: a PagedEviction (or a tuple like it) to fill instead of new tensors; entries of its
-    ``freed`` behind n_freed are left as they were."""
+    ``out``: a PagedEviction (or a tuple like it) to fill instead of new tensors (its ``kept`` has as
+    many columns as it has); entries of its ``freed`` behind n_freed are left as they were.
+    ``freed`` has pages as the table names them: shared ones for each sequence that lets go of them, and
+    ones outside the pool, which the status reports, too."""
     if not weights.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
     dev = weights.device

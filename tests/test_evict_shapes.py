@@ -3,7 +3,10 @@ per CTA, numbers held in registers, in shared memory or read again.  The choice 
 import random
 
 import pytest
+import torch
 
+import mla_causal_attention_gb300 as mla
+from mla_causal_attention_gb300 import binding
 from test_evict import pages, run_case
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +36,19 @@ def test_choice_in_every_launch(B, positions, most, kind):
     budgets = [r.randint(0, 1 + n) for n in lens]
     wide = positions // 16 - max(pages(n, 16) for n in lens)
     run_case(lens, budgets, 3, 17, 16, kind, B, K=max(1, max(map(min, lens, budgets))), extra=wide)
+
+
+def test_freed_pages_are_listed_as_the_table_has_them():
+    ws = mla.Workspace("cuda:0")
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    w = torch.rand(8, 16, device="cuda")
+
+    def call(table):
+        p = mla.mla_paged_evict(w, i(table), i([60, 64, 33]), i([20, 16, 32]), workspace=ws)
+        return p.freed[:int(p.n_freed)].tolist(), mla.mla_attn_get_status(ws)
+
+    # shared pages come up for each sequence that lets go of them
+    assert call([[0, 1, 2, 3], [4, 1, 2, 2], [0, 1, 5, -1]]) == ([2, 3, 1, 2, 2, 5], 0)
+    # and so do entries that are no pages, with the status to say so
+    freed, status = call([[0, 1, 2, -1], [4, 8, 6, 7], [0, 1, 5, -1]])
+    assert freed == [2, -1, 8, 6, 7, 5] and status == binding.MlaStatus.ERR_PAGE
