@@ -6,7 +6,7 @@ import torch
 
 import mla_causal_attention_gb300 as mla
 from paged_helpers import tree_case
-from test_key_weights import call, reference
+from test_key_weights import SCALE, call, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +82,145 @@ def test_rows_that_are_no_numbers_leave_alone_what_they_do_not_see(way, what, de
     assert bool(w[lost].isnan().all()) and not bool(w[~lost].isnan().any())
     close(w, e, old, decay, but=lost)
     assert mla.mla_attn_get_status() == 0
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("way", WAYS)
+def test_every_way_matches_64_bits(way, tree):
+    d = case(way, 32, (0, 400), page=32, tree=tree)
+    old = torch.rand(d["c_pages"].shape[:2], device="cuda")
+    for decay in (0.0, 1.0, -0.5):
+        close(call(d, old, decay), d, old, decay)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_hidden_keys_that_are_no_numbers(way):
+    d = case(way, 33, (40, 200))
+    e = {k: x.clone() if x is not None else None for k, x in d.items()}
+    hidden = []
+    for b in range(d["kv_len"].shape[0]):  # new token 3 is hidden from every row
+        lo, hi = int(d["cu_q"][b]), int(d["cu_q"][b + 1])
+        for x in (d, e):
+            x["draft_mask"][lo:hi] &= ~8
+        at = slots(d, b)[int(d["kv_len"][b]) - (hi - lo) + 3]
+        hidden.append(at)
+        d["c_pages"].view(-1, 512)[at] = float("nan")
+        d["pe_pages"].view(-1, 64)[at] = float("inf")
+        e["c_pages"].view(-1, 512)[at] = 1.0
+        e["pe_pages"].view(-1, 64)[at] = 1.0
+    old = torch.rand(d["c_pages"].shape[:2], device="cuda")
+    w = call(d, old, 0.5)
+    assert w.view(-1)[torch.stack(hidden)].tolist() == [0.0] * len(hidden)
+    assert torch.equal(call(e, old, 0.5), w)  # what stands there does not matter
+    close(w, e, old, 0.5)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_rows_that_see_nothing(way):
+    d = case(way, 34, (0, 0))
+    lo, hi = int(d["cu_q"][0]), int(d["cu_q"][1])
+    d["draft_mask"][lo:hi] = 0         # no row of the first sequence sees anything
+    d["draft_mask"][hi:hi + 2] = 0     # two tokens of the second
+    old = torch.rand(d["c_pages"].shape[:2], device="cuda")
+    w = call(d, old, 1.0)
+    assert not bool(w.view(-1)[slots(d, 0)].any())
+    close(w, d, old, 1.0)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_decay_zero_reads_nothing(way):
+    d = case(way, 35, (100, 400))
+    old = torch.full(d["c_pages"].shape[:2], float("nan"), device="cuda")
+    w = call(d, old, 0.0)
+    H, total = d["q_nope"].shape[1], 0
+    for b in range(d["kv_len"].shape[0]):
+        at = slots(d, b)
+        n = int(d["cu_q"][b + 1] - d["cu_q"][b])
+        assert abs(float(w.view(-1)[at].double().sum()) - n * H) <= n * H * 1e-4
+        total += len(at)
+    assert int((~w.isnan()).sum()) == total
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_scores_far_apart(way):
+    d = case(way, 36, (500, 700), page=64)
+    for b in range(d["kv_len"].shape[0]):
+        at = slots(d, b)
+        grow = torch.linspace(0.5, 12.0, len(at), device="cuda")[:, None]
+        for name, n in (("c_pages", 512), ("pe_pages", 64)):
+            x = d[name].view(-1, n)
+            x[at] = (x[at].float() * grow).bfloat16()
+    old = torch.zeros(d["c_pages"].shape[:2], device="cuda")
+    close(call(d, old, 0.0), d, old, 0.0)
+
+
+@pytest.mark.parametrize("outside", [-7, -1, 1 << 20])
+@pytest.mark.parametrize("way", WAYS)
+def test_pages_outside_the_pool_count_as_zeros(way, outside):
+    d = case(way, 37, (100, 300))
+    ws = mla.Workspace("cuda:0")
+    old = torch.rand(d["c_pages"].shape[:2], device="cuda")
+    gone = d["block_table"][:, 2].long()  # positions 32 to 47 of every sequence
+    e = dict(d, c_pages=d["c_pages"].clone(), pe_pages=d["pe_pages"].clone())
+    e["c_pages"][gone] = 0.0
+    e["pe_pages"][gone] = 0.0
+    table = d["block_table"].clone()
+    table[:, 2] = outside
+    w = call(dict(d, block_table=table), old, 1.0, workspace=ws)
+    assert mla.mla_attn_get_status(ws) == mla.binding.MlaStatus.ERR_PAGE
+    assert torch.equal(w[gone], old[gone])  # nothing is written for them
+    zeros = call(e, old, 1.0)
+    zeros[gone] = old[gone]
+    assert torch.equal(w, zeros)
+
+
+@pytest.mark.parametrize("B,ctx,new", [(2, 35000, 5), (1, 70000, 10)])  # kept; computed again
+def test_long_caches(B, ctx, new):
+    d = tree_case(38, B, 64, (ctx, ctx + 100), (new, new), 1024, False)
+    old = torch.rand(d["c_pages"].shape[:2], device="cuda")
+    close(call(d, old, 0.0), d, old, 0.0)
+
+
+@pytest.mark.parametrize("way", ["kept", "computed"])
+def test_pools_past_4_gb(way):
+    d = case(way, 39, (200, 300), page=64)
+    pages, far = d["c_pages"].shape[0], 80000
+    c = torch.empty(far, 64, 512, dtype=torch.bfloat16, device="cuda")
+    pe = torch.empty(far, 64, 64, dtype=torch.bfloat16, device="cuda")
+    c[-pages:], pe[-pages:] = d["c_pages"], d["pe_pages"]
+    old = torch.rand(pages, 64, device="cuda")
+    w = torch.zeros(far, 64, device="cuda")
+    w[-pages:] = old
+    table = torch.where(d["block_table"] < 0, -1, d["block_table"] + far - pages)
+    got = call(dict(d, c_pages=c, pe_pages=pe, block_table=table.to(torch.int32)), w, 1.0)
+    assert torch.equal(got[-pages:], call(d, old, 1.0)) and not bool(got[:-pages].any())
+
+
+def test_a_captured_call_takes_the_way_of_its_replay():
+    """Which sequences' scores are kept is decided on the device, at each replay."""
+    d = batch(40, [700, 900, 300], [6, 12, 2], 64)
+    st, ws = torch.cuda.Stream(), mla.Workspace("cuda:0")
+    old = torch.rand(d["c_pages"].shape[:2], device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        call(d, old, 1.0, workspace=ws)
+        w = old.clone()
+        st.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            mla.mla_latent_key_weights(*(d[k] for k in ("q_nope", "q_pe", "c_pages", "pe_pages",
+                                                        "block_table", "kv_len", "cu_q", "draft_mask",
+                                                        "w_kvb")), SCALE, w, workspace=ws)
+        for cu, lens in (([0, 6, 18, 20], [700, 900, 300]), ([0, 8, 16, 20], [400, 900, 256]),
+                         ([0, 9, 18, 20], [513, 10, 2]), ([0, 0, 20, 20], [90, 300, 0]),
+                         ([0, 20, 20, 20], [640, 5, 0])):
+            d["cu_q"].copy_(torch.tensor(cu, dtype=torch.int32))
+            d["kv_len"].copy_(torch.tensor(lens, dtype=torch.int32))
+            w.copy_(old)
+            g.replay()
+            st.synchronize()
+            close(w, d, old, 1.0)
+        assert mla.mla_attn_get_status(ws, stream=st) == 0
 
 
 # ---- the store of kept scores -----------------------------------------------------------
