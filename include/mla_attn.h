@@ -526,7 +526,9 @@ MLA_API mla_status mla_latent_tree_fwd(const uint16_t* q_nope, const uint16_t* q
  *   weights[slot of j] = decay * weights[slot of j] + sum_{i,h} softmax_j(s_ih)_j   j < ctx, cached
  *                      =                              sum_{i,h} softmax_j(s_ih)_j   a new token's key
  *
- * in fp32, with scores that are exact to about 2^-17 of their size.  With decay 0 nothing is read
+ * in fp32.  A score is off by about 2^-16 of |q_lat| . |c_j| and 2^-17 of |W_K[h]|^T |q_nope| . |c_j|
+ * + |q_pe| . |k_pe_j| at most, times softmax_scale, with q_lat = W_K[h]^T q_nope: relative to the products
+ * that make it up, and not to a score that is a small difference of large ones.  With decay 0 nothing is read
  * from weights, whatever it holds.  A hidden key gets nothing from a row, whatever it holds, and a
  * row that sees nothing gives nothing.  Sequences without new tokens are left as they are, and so
  * are all slots behind kv_len[b].  The weights of one token sum to H.  To let the last tokens of a prompt
