@@ -161,7 +161,9 @@ __global__ void __launch_bounds__(kApplyThreads) rope_apply_kernel(const RopeApp
   }
 }
 
-// Any width, strides and alignment: a warp per row, a pair per lane and turn.
+// Any width, strides and alignment: a warp per row, a pair per lane and turn.  Element by element, which
+// takes its time: 16411 tokens of 64 heads and 64 columns 316 us in bf16 (852 GB/s) with x one element
+// past 16 bytes, 42 aligned; 256 in fp32 (2.1 TB/s), 89 aligned; 62 columns in bf16 309; 64 rows 2.
 template <typename T>
 __global__ void __launch_bounds__(kApplyThreads) rope_apply_any_kernel(const RopeApplyArgs a) {
   constexpr int kMost = kMaxRopeDim / 64;  // pairs of a lane
