@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       // Keys that few units read come from HBM, and are asked into L2 ahead of their loads.  With
       // rows so few that HBM is the bound they are better read once and soon dropped, so
       // that the scores stay (64 sequences of 4000 keys, 16 rows: 81 us -> 72; 64 rows on U[512, 8192]
-      // keys: 109 -> 102; 128 rows, bound by their MMAs: 121 the first way, 123 the second).
+      // keys: 109 -> 102; 80 rows on 4000: 104.4 -> 101.4; 96: 108.6 -> 107.9; 112: 112.5 -> 113.5; 128
+      // rows, bound by their MMAs: 117 -> 118.  With 16 sequences of 8000 keys 112 rows gain too, 65 -> 59).
       const bool once = g.s.n * a.H <= kOnceRows;
       const bool ask = !once && g.s.n * a.H <= kKeptRows;
       const uint64_t policy = once ? l2_policy_evict_first() : l2_policy_evict_normal();
