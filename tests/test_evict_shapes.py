@@ -1,12 +1,15 @@
 """The eviction's launch follows the table's width and the number of sequences: CTAs per sequence, threads
 per CTA, numbers held in registers, in shared memory or read again.  The choice is the same in all."""
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import mla_causal_attention_gb300 as mla
 from mla_causal_attention_gb300 import binding
+from mla_causal_attention_gb300.build import ROOT
 from test_evict import pages, run_case
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +55,33 @@ def test_freed_pages_are_listed_as_the_table_has_them():
     # and so do entries that are no pages, with the status to say so
     freed, status = call([[0, 1, 2, -1], [4, 8, 6, 7], [0, 1, 5, -1]])
     assert freed == [2, -1, 8, 6, 7, 5] and status == binding.MlaStatus.ERR_PAGE
+
+
+def test_a_process_whose_first_choice_is_captured():
+    """What the launch asks the device (attributes, clusters at once) it can ask within a capture."""
+    code = """
+import torch
+import mla_causal_attention_gb300 as mla
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+B, width = 70, 2048
+w = torch.rand(B * 4, 16, device="cuda")
+table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+table[:, :4] = torch.arange(B * 4, device="cuda", dtype=torch.int32).view(B, 4)
+lens, budget = i([60] * B), i([20] * B)
+out = (i([[0] * 20] * B), i([0] * B), i([0] * (B * width)), i([0]))
+ws = mla.Workspace("cuda:0")
+mla.mla_rope_apply(torch.rand(1, 2, device="cuda"), i([0]), torch.rand(1, 2, device="cuda"), workspace=ws)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    mla.mla_paged_evict(w, table, lens, budget, 2, 3, out=out, workspace=ws)
+g.replay()
+torch.cuda.synchronize()
+v = w.view(B, 64)[:, 2:57]
+best = v.topk(15).indices.sort().values + 2
+want = torch.cat((i([[0, 1]] * B), best.to(torch.int32), i([[57, 58, 59]] * B)), 1)
+print(torch.equal(out[0], want), out[1].unique().tolist(), int(out[3]), mla.mla_attn_get_status(ws))
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.stdout.split() == ["True", "[20]", "140", "0"], r.stdout + r.stderr
