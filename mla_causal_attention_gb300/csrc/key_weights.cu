@@ -662,7 +662,6 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
     const float held = writes && key < s.ctx && a.decay != 0.f ? a.weights[slot] : 0.f;
     // Sums in two parts (see key_sum_kernel).
     float total[4] = {}, dropped[4] = {};
-    bool no_number = false;
     for (int r0 = warp; r0 < rows; r0 += 8 * kDeep) {
       // The 64 rows of a round are in one unit, whose rows of a tile lie together.
       const int m = r0 / kRows, unit_rows = min(kRows, rows - m * kRows);
@@ -684,15 +683,6 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
       }
       // A row that is not there, or that sees nothing (L infinite, its scores -inf), adds 2^-inf = 0.
       float got[4] = {};
-      if (some_hidden) {  // a row without an L would spoil the keys that it hides: it comes below
-#pragma unroll
-        for (int e = 0; e < kDeep; ++e)
-          if (L[e] != L[e]) {
-            no_number = true;
-            L[e] = INFINITY;
-            v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-      }
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
         got[0] += ex2_approx(fmaf(v[e].x, sl2, -L[e]));
@@ -707,19 +697,29 @@ __global__ void __launch_bounds__(kReadThreads) key_read_kernel(const KeyWeights
         total[c] = sum;
       }
     }
-    if (no_number) {
-      // Rows that see a key that is no number have no L: what they see gets no number, what they
-      // do not see nothing.
+    if (some_hidden && !(total[0] + total[1] + total[2] + total[3] < INFINITY)) {
+      // A row that sees a key that is no number has no L, and 2^(-inf - L) is none either where it hides
+      // one of these keys: once more, by the masks.
+#pragma unroll
+      for (int c = 0; c < 4; ++c) total[c] = dropped[c] = 0.f;
       const bool masked = a.t.draft_mask != nullptr;
 #pragma unroll 1
       for (int r = warp; r < rows; r += 8) {
-        if (lse[r] == lse[r]) continue;
+        const int m = r / kRows, unit_rows = min(kRows, rows - m * kRows);
+        const float4 v = *reinterpret_cast<const float4*>(
+            store + ((int64_t)m * kRows * K + (int64_t)k * unit_rows + (r - m * kRows)) * kTile +
+            4 * lane);
+        const float x[4] = {v.x, v.y, v.z, v.w};
         const int i = r / a.t.H;  // new token
         const uint64_t mask = masked ? (uint64_t)a.t.draft_mask[s.q0 + i] : 0ull;
         const uint64_t seen = seen_bits(k * kTile + 4 * lane, s.ctx, s.kv, masked, mask, i);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if ((seen >> c) & 1u) total[c] = lse[r];
+        for (int c = 0; c < 4; ++c) {
+          const float got = (seen >> c) & 1u ? ex2_approx(fmaf(x[c], sl2, -lse[r])) : 0.f;
+          const float y = got - dropped[c], sum = total[c] + y;
+          dropped[c] = (sum - total[c]) - y;
+          total[c] = sum;
+        }
       }
     }
     *reinterpret_cast<float4*>(&part[warp][4 * lane]) =
