@@ -20,7 +20,7 @@
 //   key_sum_kernel               w_j of the other sequences: tiles of 256 keys against tiles of 128 rows
 //
 // What bounds it: 2 * 2 * 1088 operations per row and key (the latent columns twice, once for each
-// part), or 1152 bytes per key where a sequence has few rows (decode batch: 374 MB in 68 of 99 us).
+// part), or 1152 bytes per key where a sequence has few rows (decode batch: 374 MB in 68 to 70 of 99 us).
 //
 // row_stats: the tree attention's scores without its mix.  A pair holds 64 rows of queries in each
 //   CTA, 136 KB in the two parts, and streams the keys, 64 per CTA; S = Q K^T, M128 N128, every key
